@@ -6,6 +6,16 @@ and streams; the library's HIP kernels do every step of the layer:
     plan = Plan(E, K, N, top_k, swiglu_limit=7.0, act_format=A_MXFP8, max_tokens=4096)
     experts = Experts(plan, W_MXFP4, E, w13, s13, w2, s2)      # in-place repack
     run(plan, [experts], x, topk_ids, topk_weights, out, deterministic=False)
+
+Experts with 16-bit or 8-bit integer weights, for training or beside the layer, are
+products over rows sorted by expert:
+
+    first, order, token, inverse = group_routes(topk_ids, E)
+    y = grouped_mm(x, w, first, rows=token)                    # [T * top_k, N]
+    dx = grouped_mm_dx(dy, w, first)
+    dw = grouped_mm_dw(dy, x, first, rows=token, out_dtype=torch.float32)
+    xq, xs = quant_int8(x)
+    y = grouped_int8_mm(xq, xs, wq, ws, first, rows=token)
 """
 from __future__ import annotations
 
@@ -27,6 +37,10 @@ COMBINE_AUTO, COMBINE_ATOMIC, COMBINE_ROUTE_BUFFER = 0, 1, 2
 RACE_SLOTS = (("decode", None), ("general", "atomic"), ("general", "route_buffer"), ("prefill", "atomic"),
               ("prefill", "route_buffer"), ("prefill_narrow", "atomic"), ("prefill_narrow", "route_buffer"))
 NSLOTS = len(RACE_SLOTS)
+
+
+T_BF16, T_FP16, T_FP32 = 1, 2, 3
+MM_FORWARD, MM_DX, MM_DW, MM_INT8 = 1, 2, 3, 4
 
 
 class MoeError(RuntimeError):
@@ -325,6 +339,280 @@ def ep_remap(topk_ids, topk_weights, offset: int, num_local: int, out_ids=None, 
     _check(_lib.load().moe_ep_remap(_ptr(topk_ids), _ptr(topk_weights), T, k, int(offset), int(num_local),
                                     _ptr(out_ids), _ptr(out_weights), _stream(stream)))
     return out_ids, out_weights
+
+
+_T_CODES = None
+
+
+def _codes():
+    """torch dtype -> moe_dtype of the types the products take."""
+    global _T_CODES
+    if _T_CODES is None:
+        import torch
+        _T_CODES = {torch.bfloat16: T_BF16, torch.float16: T_FP16, torch.float32: T_FP32}
+    return _T_CODES
+
+
+def _operands(named):
+    """Checks (name, tensor, dtypes, shape) operands: types and shapes first, then that all are
+    contiguous on one GPU. Optional tensors are left out by the caller."""
+    for name, t, dtypes, shape in named:
+        if t is None:
+            raise ValueError(f"{name} is required")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    dev = named[0][1].device
+    for name, t, _, _ in named:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be a device tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {dev}")
+    return dev
+
+
+def _use(stream, t):
+    """Makes `stream` current for a call on operand t, so that the tensors made there belong to it too."""
+    import torch
+    if t is not None and t.device.type == "cuda" and stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the operands on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, stream) on the operands' device and that device's current stream."""
+    import torch
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def _mm_scratch(op, E, R, N, K, scratch, dev):
+    """(pointer, bytes, tensor) of a product's scratch: the caller's tensor, or one made here when it needs any."""
+    import torch
+    if scratch is not None:
+        _need(scratch, "scratch", torch.uint8)
+        if scratch.device != dev:
+            raise ValueError(f"scratch is on {scratch.device}, the operands on {dev}")
+        return scratch.data_ptr(), scratch.numel(), scratch
+    need = _lib.load().moe_mm_scratch_bytes(op, E, R, N, K)
+    if not need:
+        return None, 0, None
+    scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+    return scratch.data_ptr(), need, scratch
+
+
+def mm_scratch_bytes(op: int, E: int, R: int, N: int, K: int) -> int:
+    """Scratch bytes of a product (moe_mm_scratch_bytes): op MM_FORWARD, MM_DX, MM_DW or MM_INT8."""
+    return _lib.load().moe_mm_scratch_bytes(op, E, R, N, K)
+
+
+def _out_like(out, out_dtype, default, allowed, shape, dev, named, name="out"):
+    """The output tensor (made here unless given) and its moe_dtype."""
+    import torch
+    if out is not None:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"{name}: expected {out_dtype}, got {out.dtype}")
+        named.append((name, out, allowed, shape))
+        return out.dtype
+    dt = default if out_dtype is None else out_dtype
+    if dt not in allowed:
+        raise TypeError(f"out_dtype: expected {' or '.join(map(str, allowed))}, got {dt}")
+    return dt
+
+
+def _dims(t, name, dim):
+    if t is None or t.dim() != dim:
+        raise ValueError(f"{name} must be a tensor of {dim} dimensions")
+    return t.shape
+
+
+def grouped_mm(x, w, first, rows=None, out=None, out_dtype=None, scratch=None, stream=None):
+    """Products over ragged groups (moe_grouped_mm): out[r] = x[row(r)] @ w[e].T for the rows r of
+    group e, first[e] <= r < first[e + 1].
+
+    x [T, K] and w [E, N, K] bf16 or fp16, first int32 [E + 1]; rows int32 [R] names the row of x
+    behind each product row (None: R = T, row r itself; a number outside [0, T): a row of zeros).
+    out [R, N] in x's type or fp32; rows in no group keep what out held (unset in a new tensor)."""
+    import torch
+    if stream is not None:
+        with _use(stream, x):
+            return grouped_mm(x, w, first, rows, out, out_dtype, scratch)
+    T, K = _dims(x, "x", 2)
+    E, N, _ = _dims(w, "w", 3)
+    R = T if rows is None else _dims(rows, "rows", 1)[0]
+    kinds = (torch.bfloat16, torch.float16)
+    named = [("x", x, kinds, x.shape), ("w", w, (x.dtype,), (E, N, K)), ("first", first, (torch.int32,), (E + 1,))]
+    if rows is not None:
+        named.append(("rows", rows, (torch.int32,), (R,)))
+    dt = _out_like(out, out_dtype, x.dtype, (x.dtype, torch.float32), (R, N), x.device, named)
+    dev = _operands(named)
+    if out is None:
+        out = torch.empty((R, N), dtype=dt, device=dev)
+    sp, sb, keep = _mm_scratch(MM_FORWARD, E, R, N, K, scratch, dev)
+    _launch(dev, _lib.load().moe_grouped_mm, _codes()[x.dtype], x.data_ptr(), T, _ptr(rows), w.data_ptr(),
+            first.data_ptr(), E, R, N, K, _codes()[dt], out.data_ptr(), sp, sb)
+    return out
+
+
+def grouped_mm_dx(dy, w, first, out=None, out_dtype=None, scratch=None, stream=None):
+    """Gradient of grouped_mm for the product rows (moe_grouped_mm_dx): dx[r] = dy[r] @ w[e].
+
+    dy [R, N], w [E, N, K] bf16 or fp16; out [R, K] in dy's type or fp32. With `rows` in the forward
+    product, a token's gradient is the sum of dx over its rows (group_routes' inverse lists them)."""
+    import torch
+    if stream is not None:
+        with _use(stream, dy):
+            return grouped_mm_dx(dy, w, first, out, out_dtype, scratch)
+    R, N = _dims(dy, "dy", 2)
+    E, _, K = _dims(w, "w", 3)
+    kinds = (torch.bfloat16, torch.float16)
+    named = [("dy", dy, kinds, dy.shape), ("w", w, (dy.dtype,), (E, N, K)), ("first", first, (torch.int32,), (E + 1,))]
+    dt = _out_like(out, out_dtype, dy.dtype, (dy.dtype, torch.float32), (R, K), dy.device, named)
+    dev = _operands(named)
+    if out is None:
+        out = torch.empty((R, K), dtype=dt, device=dev)
+    sp, sb, keep = _mm_scratch(MM_DX, E, R, N, K, scratch, dev)
+    _launch(dev, _lib.load().moe_grouped_mm_dx, _codes()[dy.dtype], dy.data_ptr(), w.data_ptr(),
+            first.data_ptr(), E, R, N, K, _codes()[dt], out.data_ptr(), sp, sb)
+    return out
+
+
+def grouped_mm_dw(dy, x, first, rows=None, out=None, out_dtype=None, accumulate: bool = False, scratch=None,
+                  stream=None):
+    """Gradient of grouped_mm for the weights (moe_grouped_mm_dw): dw[e] = the sum over the rows r of
+    group e of the outer products dy[r] x[row(r)]; zeros for an empty group.
+
+    dy [R, N], x [T, K] bf16 or fp16, rows as in grouped_mm; out [E, N, K] in dy's type or fp32.
+    accumulate adds to out (fp32, required then)."""
+    import torch
+    if stream is not None:
+        with _use(stream, dy):
+            return grouped_mm_dw(dy, x, first, rows, out, out_dtype, accumulate, scratch)
+    R, N = _dims(dy, "dy", 2)
+    T, K = _dims(x, "x", 2)
+    E = _dims(first, "first", 1)[0] - 1
+    if rows is None and T != R:
+        raise ValueError(f"x: expected {R} rows as dy, got {T}")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    kinds = (torch.bfloat16, torch.float16)
+    named = [("dy", dy, kinds, dy.shape), ("x", x, (dy.dtype,), x.shape), ("first", first, (torch.int32,), (E + 1,))]
+    if rows is not None:
+        named.append(("rows", rows, (torch.int32,), (R,)))
+    dt = _out_like(out, out_dtype, dy.dtype, (dy.dtype, torch.float32), (E, N, K), dy.device, named)
+    dev = _operands(named)
+    if out is None:
+        out = torch.empty((E, N, K), dtype=dt, device=dev)
+    sp, sb, keep = _mm_scratch(MM_DW, E, R, N, K, scratch, dev)
+    _launch(dev, _lib.load().moe_grouped_mm_dw, _codes()[dy.dtype], dy.data_ptr(), x.data_ptr(), T, _ptr(rows),
+            first.data_ptr(), E, R, N, K, _codes()[dt], int(bool(accumulate)), out.data_ptr(), sp, sb)
+    return out
+
+
+def quant_int8(x, out=None, scales=None, stream=None):
+    """Rows of a bf16 or fp16 [rows, cols] tensor to 8-bit integers with one fp32 scale a row
+    (moe_quant_int8): (codes int8 [rows, cols], scales [rows])."""
+    import torch
+    if stream is not None:
+        with _use(stream, x):
+            return quant_int8(x, out, scales)
+    shape = _dims(x, "x", 2)
+    named = [("x", x, (torch.bfloat16, torch.float16), shape)]
+    if out is not None:
+        named.append(("out", out, (torch.int8,), shape))
+    if scales is not None:
+        named.append(("scales", scales, (torch.float32,), shape[:1]))
+    dev = _operands(named)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.int8, device=dev)
+    if scales is None:
+        scales = torch.empty(shape[0], dtype=torch.float32, device=dev)
+    _launch(dev, _lib.load().moe_quant_int8, _codes()[x.dtype], x.data_ptr(), shape[0], shape[1],
+            out.data_ptr(), scales.data_ptr())
+    return out, scales
+
+
+def int8_mm(x, x_scales, w, w_scales, out=None, out_dtype=None, scratch=None, stream=None):
+    """8-bit integer product with a scale per token and channel (moe_int8_mm):
+    out[m, n] = x_scales[m] * w_scales[n] * (x[m] . w[n]), the sum exact.
+
+    x int8 [M, K], x_scales fp32 [M], w int8 [N, K], w_scales fp32 [N]; out [M, N] bf16 (default),
+    fp16 or fp32."""
+    import torch
+    if stream is not None:
+        with _use(stream, x):
+            return int8_mm(x, x_scales, w, w_scales, out, out_dtype, scratch)
+    M, K = _dims(x, "x", 2)
+    N, _ = _dims(w, "w", 2)
+    named = [("x", x, (torch.int8,), x.shape), ("x_scales", x_scales, (torch.float32,), (M,)),
+             ("w", w, (torch.int8,), (N, K)), ("w_scales", w_scales, (torch.float32,), (N,))]
+    dt = _out_like(out, out_dtype, torch.bfloat16, tuple(_codes()), (M, N), x.device, named)
+    dev = _operands(named)
+    if out is None:
+        out = torch.empty((M, N), dtype=dt, device=dev)
+    sp, sb, keep = _mm_scratch(MM_INT8, 1, M, N, K, scratch, dev)
+    _launch(dev, _lib.load().moe_int8_mm, x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
+            M, N, K, _codes()[dt], out.data_ptr(), sp, sb)
+    return out
+
+
+def grouped_int8_mm(x, x_scales, w, w_scales, first, rows=None, out=None, out_dtype=None, scratch=None, stream=None):
+    """int8_mm over ragged groups (moe_grouped_int8_mm): w int8 [E, N, K], w_scales fp32 [E, N], first and
+    rows as in grouped_mm; x_scales belongs to the rows of x. out [R, N] bf16 (default), fp16 or fp32."""
+    import torch
+    if stream is not None:
+        with _use(stream, x):
+            return grouped_int8_mm(x, x_scales, w, w_scales, first, rows, out, out_dtype, scratch)
+    T, K = _dims(x, "x", 2)
+    E, N, _ = _dims(w, "w", 3)
+    R = T if rows is None else _dims(rows, "rows", 1)[0]
+    named = [("x", x, (torch.int8,), x.shape), ("x_scales", x_scales, (torch.float32,), (T,)),
+             ("w", w, (torch.int8,), (E, N, K)), ("w_scales", w_scales, (torch.float32,), (E, N)),
+             ("first", first, (torch.int32,), (E + 1,))]
+    if rows is not None:
+        named.append(("rows", rows, (torch.int32,), (R,)))
+    dt = _out_like(out, out_dtype, torch.bfloat16, tuple(_codes()), (R, N), x.device, named)
+    dev = _operands(named)
+    if out is None:
+        out = torch.empty((R, N), dtype=dt, device=dev)
+    sp, sb, keep = _mm_scratch(MM_INT8, E, R, N, K, scratch, dev)
+    _launch(dev, _lib.load().moe_grouped_int8_mm, x.data_ptr(), x_scales.data_ptr(), T, _ptr(rows), w.data_ptr(),
+            w_scales.data_ptr(), first.data_ptr(), E, R, N, K, _codes()[dt], out.data_ptr(), sp, sb)
+    return out
+
+
+def group_routes(topk_ids, num_experts: int, scratch=None, stream=None):
+    """The routes of a batch sorted by expert (moe_group_routes), for grouped_mm and its kin.
+
+    topk_ids int32 [T, k]; ids outside [0, num_experts) belong to no group. Returns int32 device tensors
+    (first [E + 1], order [T * k], token [T * k], inverse [T, k]): the groups' offsets, the route and
+    the token behind each sorted row (-1 past first[E]), and the sorted row of each route (or -1)."""
+    import torch
+    if stream is not None:
+        with _use(stream, topk_ids):
+            return group_routes(topk_ids, num_experts, scratch)
+    T, k = _dims(topk_ids, "topk_ids", 2)
+    dev = _operands([("topk_ids", topk_ids, (torch.int32,), topk_ids.shape)])
+    E = int(num_experts)
+    L = _lib.load()
+    first = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
+    order, token, inverse = torch.empty((3, T * k), dtype=torch.int32, device=dev).unbind(0)
+    need = L.moe_group_routes_scratch_bytes(T, k, E)
+    if scratch is None:
+        scratch = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        _need(scratch, "scratch", torch.uint8)
+        if scratch.device != dev:
+            raise ValueError(f"scratch is on {scratch.device}, the operands on {dev}")
+    _launch(dev, L.moe_group_routes, topk_ids.data_ptr(), T, k, E, first.data_ptr(), order.data_ptr(),
+            token.data_ptr(), inverse.data_ptr(), _ptr(scratch), 0 if scratch is None else scratch.numel())
+    return first, order, token, inverse.view(T, k)
 
 
 def debug_route(plan: Plan, tiers: Sequence, topk_ids, scratch=None, stream=None):

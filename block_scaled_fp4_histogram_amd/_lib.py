@@ -14,6 +14,7 @@ LIB_PATH = os.environ.get("MOE_LIB_PATH") or os.path.join(_PKG, "libmoe_gfx950.s
 
 # Every function include/moe.h declares, with (restype, argtypes).
 _vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
+_ll = C.c_longlong
 SIGNATURES = {
     "moe_plan": (_i, [_i, _i, _i, _i, _f, _i, _i, _i, C.POINTER(_vp)]),
     "moe_plan_destroy": (None, [_vp]),
@@ -39,6 +40,15 @@ SIGNATURES = {
     "moe_plan_enable_stage_timing": (_i, [_vp, _i]),
     "moe_plan_stage_times": (_i, [_vp, C.POINTER(_f), _i, C.POINTER(_i)]),
     "moe_ep_remap": (_i, [_vp, _vp, _i, _i, C.c_longlong, _i, _vp, _vp, _vp]),
+    "moe_group_routes_scratch_bytes": (_sz, [_i, _i, _i]),
+    "moe_group_routes": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_mm_scratch_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_grouped_mm": (_i, [_i, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "moe_grouped_mm_dx": (_i, [_i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "moe_grouped_mm_dw": (_i, [_i, _vp, _vp, _ll, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "moe_quant_int8": (_i, [_i, _vp, _i, _i, _vp, _vp, _vp]),
+    "moe_int8_mm": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "moe_grouped_int8_mm": (_i, [_vp, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "moe_debug_route": (_i, [_vp, _vp, _i, _vp, _i, _vp, _sz, _vp, _vp, _vp, _vp, _vp]),
     "moe_debug_quant_mxfp8_bf16": (_i, [_vp, _i, _i, _vp, _vp, _vp]),
     "moe_debug_quant_mxfp8_f32": (_i, [_vp, _i, _i, _vp, _vp, _vp]),

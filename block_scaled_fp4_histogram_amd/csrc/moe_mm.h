@@ -1,0 +1,46 @@
+// Internal declarations of the ragged expert products, the 8-bit integer
+// products, the row quantiser and the route grouping (moe_mm.hip, moe_rows.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+enum MmType { MM_BF16 = 1, MM_FP16 = 2, MM_FP32 = 3, MM_I8 = 4 };
+enum MmOp { MM_FORWARD = 1, MM_DX = 2, MM_DW = 3 };
+
+// One product over E groups of rows; group e holds rows first[e] .. first[e+1]
+// (first == NULL: one group of R rows).  Every kernel clamps the offsets to
+// [0, R], so no offset array makes it leave its buffers.
+struct MmArgs {
+  int op, type, out_type, accumulate;
+  const void *x;                     // MM_FORWARD, MM_DW: rows of K
+  const void *dy;                    // MM_DX, MM_DW: rows of N
+  const void *w;                     // MM_FORWARD, MM_DX: [E, N, K]
+  const int32_t *rows;               // row of x behind each product row (NULL: its own)
+  long x_rows;                       // rows of x (checked against `rows` on the device)
+  const int32_t *first;
+  int E, R, N, K;
+  const float *x_scales, *w_scales;  // MM_I8: per row of x, per channel [E, N]
+  void *out;                         // [R, N], [R, K] or [E, N, K]
+};
+
+hipError_t launch_mm(const MmArgs &a, hipStream_t s);
+
+// Row quantiser: scale = fp32(amax / 127), codes = x / scale to nearest even.
+hipError_t launch_quant_int8(int type, const void *x, long rows, int cols, int8_t *q, float *scales, hipStream_t s);
+
+constexpr int kGroupChunk = 1024;    // routes one block of the grouping kernels takes
+
+struct GroupArgs {
+  const int32_t *ids;
+  int R, topk, E, chunks;
+  int32_t *first, *order, *token, *inverse;
+  int32_t *hist, *rank;              // scratch of more than one chunk: [chunks][E] counts, per-route rank
+};
+
+hipError_t launch_group(const GroupArgs &a, hipStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,196 @@
+// C ABI of the ragged expert products, the 8-bit integer products and the
+// route grouping (declared in include/moe.h): argument validation and launches.
+#include <stdarg.h>
+#include <stdio.h>
+
+#include "moe.h"
+#include "moe_common.h"
+#include "moe_mm.h"
+
+namespace {
+
+int fail(int code, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return moe::set_error(code, buf);
+}
+
+bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+int launched(hipError_t e, const char *what) {
+  return e == hipSuccess ? MOE_OK : fail(MOE_EHIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+// Longest row (elements) of the products: a tile's rows stay within 32-bit byte offsets.
+constexpr int kMmMaxDim = 1 << 20;
+// Longest int8 reduction: (-128)^2 a term in a 32-bit sum.
+constexpr int kI8MaxK = 131056;
+
+int check_shape(const char *fn, int unit, const int32_t *first, int E, int R, int N, int K) {
+  if (R < 0) return fail(MOE_EINVAL, "%s: rows R=%d", fn, R);
+  if (N < 1 || K < 1) return fail(MOE_EINVAL, "%s: N=%d, K=%d", fn, N, K);
+  if (E < 1) return fail(MOE_EINVAL, "%s: E=%d", fn, E);
+  if (!aligned(first, 4)) return fail(MOE_EINVAL, "%s: first needs 4-byte alignment", fn);
+  if (E > moe::kMaxExperts) return fail(MOE_EUNSUPPORTED, "%s: E=%d above %d", fn, E, moe::kMaxExperts);
+  if (N % 8 || K % unit) return fail(MOE_EUNSUPPORTED, "%s: N=%d must be a multiple of 8, K=%d of %d", fn, N, K, unit);
+  if (N > kMmMaxDim || K > kMmMaxDim) return fail(MOE_EUNSUPPORTED, "%s: N=%d or K=%d above %d", fn, N, K, kMmMaxDim);
+  return MOE_OK;
+}
+
+int check_16bit(const char *fn, int dtype, int out_dtype) {
+  if (dtype != MOE_T_BF16 && dtype != MOE_T_FP16) return fail(MOE_EUNSUPPORTED, "%s: dtype %d is not bf16 or fp16", fn, dtype);
+  if (out_dtype != dtype && out_dtype != MOE_T_FP32)
+    return fail(MOE_EUNSUPPORTED, "%s: out_dtype %d is neither the operands' type nor fp32", fn, out_dtype);
+  return MOE_OK;
+}
+
+int check_ptrs(const char *fn, const void *const *p, int n) {
+  for (int i = 0; i < n; i++)
+    if (!p[i] || !aligned(p[i], 16)) return fail(MOE_EINVAL, "%s: null or misaligned pointer (16 bytes)", fn);
+  return MOE_OK;
+}
+
+int check_rows(const char *fn, const int32_t *rows, long long x_rows, int R) {
+  if (!aligned(rows, 4)) return fail(MOE_EINVAL, "%s: rows needs 4-byte alignment", fn);
+  if (x_rows < 0 || (!rows && x_rows < R)) return fail(MOE_EINVAL, "%s: x_rows=%lld for R=%d rows", fn, x_rows, R);
+  return MOE_OK;
+}
+
+}  // namespace
+
+#define TRY(expr)              \
+  do {                         \
+    const int rc_ = (expr);    \
+    if (rc_ != MOE_OK) return rc_; \
+  } while (0)
+
+extern "C" {
+
+size_t moe_mm_scratch_bytes(int op, int E, int R, int N, int K) {
+  (void)op, (void)E, (void)R, (void)N, (void)K;
+  return 0;
+}
+
+int moe_grouped_mm(int dtype, const void *x, long long x_rows, const int32_t *rows, const void *w,
+                   const int32_t *first, int E, int R, int N, int K, int out_dtype, void *out, void *scratch,
+                   size_t scratch_bytes, void *stream) {
+  const char *fn = "moe_grouped_mm";
+  TRY(check_16bit(fn, dtype, out_dtype));
+  TRY(check_shape(fn, 8, first, E, R, N, K));
+  TRY(check_rows(fn, rows, x_rows, R));
+  if (R == 0) return MOE_OK;
+  if (!first) return fail(MOE_EINVAL, "%s: null first", fn);
+  const void *p[] = {x, w, out};
+  TRY(check_ptrs(fn, p, 3));
+  moe::MmArgs a = {};
+  a.op = moe::MM_FORWARD, a.type = dtype, a.out_type = out_dtype;
+  a.x = x, a.x_rows = (long)x_rows, a.rows = rows, a.w = w, a.first = first;
+  a.E = E, a.R = R, a.N = N, a.K = K, a.out = out;
+  return launched(moe::launch_mm(a, (hipStream_t)stream), fn);
+}
+
+int moe_grouped_mm_dx(int dtype, const void *dy, const void *w, const int32_t *first, int E, int R, int N, int K,
+                      int out_dtype, void *dx, void *scratch, size_t scratch_bytes, void *stream) {
+  const char *fn = "moe_grouped_mm_dx";
+  TRY(check_16bit(fn, dtype, out_dtype));
+  TRY(check_shape(fn, 8, first, E, R, N, K));
+  if (R == 0) return MOE_OK;
+  if (!first) return fail(MOE_EINVAL, "%s: null first", fn);
+  const void *p[] = {dy, w, dx};
+  TRY(check_ptrs(fn, p, 3));
+  moe::MmArgs a = {};
+  a.op = moe::MM_DX, a.type = dtype, a.out_type = out_dtype;
+  a.dy = dy, a.w = w, a.first = first;
+  a.E = E, a.R = R, a.N = N, a.K = K, a.out = dx;
+  return launched(moe::launch_mm(a, (hipStream_t)stream), fn);
+}
+
+int moe_grouped_mm_dw(int dtype, const void *dy, const void *x, long long x_rows, const int32_t *rows,
+                      const int32_t *first, int E, int R, int N, int K, int out_dtype, int accumulate, void *dw,
+                      void *scratch, size_t scratch_bytes, void *stream) {
+  const char *fn = "moe_grouped_mm_dw";
+  TRY(check_16bit(fn, dtype, out_dtype));
+  if (accumulate && out_dtype != MOE_T_FP32) return fail(MOE_EUNSUPPORTED, "%s: accumulate needs an fp32 dw", fn);
+  TRY(check_shape(fn, 8, first, E, R, N, K));
+  TRY(check_rows(fn, rows, x_rows, R));
+  if (!first) return fail(MOE_EINVAL, "%s: null first", fn);
+  const void *p[] = {dw, dy, x};   // without rows dy and x are not read
+  TRY(check_ptrs(fn, p, R ? 3 : 1));
+  moe::MmArgs a = {};
+  a.op = moe::MM_DW, a.type = dtype, a.out_type = out_dtype, a.accumulate = accumulate;
+  a.dy = dy, a.x = x, a.x_rows = (long)x_rows, a.rows = rows, a.first = first;
+  a.E = E, a.R = R, a.N = N, a.K = K, a.out = dw;
+  return launched(moe::launch_mm(a, (hipStream_t)stream), fn);
+}
+
+int moe_quant_int8(int dtype, const void *x, int rows, int cols, int8_t *q, float *scales, void *stream) {
+  const char *fn = "moe_quant_int8";
+  if (dtype != MOE_T_BF16 && dtype != MOE_T_FP16) return fail(MOE_EUNSUPPORTED, "%s: dtype %d is not bf16 or fp16", fn, dtype);
+  if (rows < 0 || cols < 1) return fail(MOE_EINVAL, "%s: rows=%d, cols=%d", fn, rows, cols);
+  if (cols % 16 || cols > kMmMaxDim) return fail(MOE_EUNSUPPORTED, "%s: cols=%d must be a multiple of 16 up to %d", fn, cols, kMmMaxDim);
+  if (rows == 0) return MOE_OK;
+  const void *p[] = {x, q};
+  TRY(check_ptrs(fn, p, 2));
+  if (!scales || !aligned(scales, 4)) return fail(MOE_EINVAL, "%s: null or misaligned scales", fn);
+  return launched(moe::launch_quant_int8(dtype, x, rows, cols, q, scales, (hipStream_t)stream), fn);
+}
+
+int moe_grouped_int8_mm(const int8_t *x, const float *x_scales, long long x_rows, const int32_t *rows, const int8_t *w,
+                        const float *w_scales, const int32_t *first, int E, int R, int N, int K, int out_dtype,
+                        void *out, void *scratch, size_t scratch_bytes, void *stream) {
+  const char *fn = first ? "moe_grouped_int8_mm" : "moe_int8_mm";
+  if (out_dtype != MOE_T_BF16 && out_dtype != MOE_T_FP16 && out_dtype != MOE_T_FP32)
+    return fail(MOE_EUNSUPPORTED, "%s: out_dtype %d", fn, out_dtype);
+  TRY(check_shape(fn, 16, first, E, R, N, K));
+  TRY(check_rows(fn, rows, x_rows, R));
+  if (K > kI8MaxK) return fail(MOE_EUNSUPPORTED, "%s: K=%d above %d (32-bit sums)", fn, K, kI8MaxK);
+  if (!first && E != 1) return fail(MOE_EINVAL, "%s: null first", fn);
+  if (R == 0) return MOE_OK;
+  const void *p[] = {x, w, out};
+  TRY(check_ptrs(fn, p, 3));
+  if (!x_scales || !w_scales || !aligned(x_scales, 4) || !aligned(w_scales, 4))
+    return fail(MOE_EINVAL, "%s: null or misaligned scales", fn);
+  moe::MmArgs a = {};
+  a.op = moe::MM_FORWARD, a.type = moe::MM_I8, a.out_type = out_dtype;
+  a.x = x, a.x_rows = (long)x_rows, a.rows = rows, a.x_scales = x_scales, a.w = w, a.w_scales = w_scales;
+  a.first = first, a.E = E, a.R = R, a.N = N, a.K = K, a.out = out;
+  return launched(moe::launch_mm(a, (hipStream_t)stream), fn);
+}
+
+int moe_int8_mm(const int8_t *x, const float *x_scales, const int8_t *w, const float *w_scales, int M, int N, int K,
+                int out_dtype, void *out, void *scratch, size_t scratch_bytes, void *stream) {
+  return moe_grouped_int8_mm(x, x_scales, M, nullptr, w, w_scales, nullptr, 1, M, N, K, out_dtype, out, scratch,
+                             scratch_bytes, stream);
+}
+
+size_t moe_group_routes_scratch_bytes(int T, int top_k, int E) {
+  if (T < 0 || top_k < 1 || E < 1 || (long long)T * top_k > INT32_MAX) return 0;
+  const long long R = (long long)T * top_k, chunks = (R + moe::kGroupChunk - 1) / moe::kGroupChunk;
+  return chunks <= 1 ? 0 : (size_t)(4 * (chunks * E + R));
+}
+
+int moe_group_routes(const int32_t *topk_ids, int T, int top_k, int E, int32_t *first, int32_t *order, int32_t *token,
+                     int32_t *inverse, void *scratch, size_t scratch_bytes, void *stream) {
+  const char *fn = "moe_group_routes";
+  if (T < 0 || E < 1) return fail(MOE_EINVAL, "%s: T=%d, E=%d", fn, T, E);
+  if (top_k < 1 || top_k > 64) return fail(MOE_EINVAL, "%s: top_k=%d outside [1, 64]", fn, top_k);
+  if (E > moe::kMaxExperts) return fail(MOE_EUNSUPPORTED, "%s: E=%d above %d", fn, E, moe::kMaxExperts);
+  if ((long long)T * top_k > (1 << 30)) return fail(MOE_EUNSUPPORTED, "%s: more than 2^30 routes", fn);
+  const void *p[] = {first, topk_ids, order, token, inverse};   // without routes only first is written
+  for (int i = 0; i < (T ? 5 : 1); i++)
+    if (!p[i] || !aligned(p[i], 4)) return fail(MOE_EINVAL, "%s: null or misaligned pointer (4 bytes)", fn);
+  const size_t need = moe_group_routes_scratch_bytes(T, top_k, E);
+  if (need && (!scratch || !aligned(scratch, 4))) return fail(MOE_EINVAL, "%s: null or misaligned scratch", fn);
+  if (scratch_bytes < need) return fail(MOE_ESCRATCH, "%s: scratch holds %zu bytes, %zu needed", fn, scratch_bytes, need);
+  moe::GroupArgs a = {};
+  a.ids = topk_ids, a.R = T * top_k, a.topk = top_k, a.E = E;
+  a.chunks = (a.R + moe::kGroupChunk - 1) / moe::kGroupChunk;
+  a.first = first, a.order = order, a.token = token, a.inverse = inverse;
+  a.hist = (int32_t *)scratch, a.rank = (int32_t *)scratch + (size_t)a.chunks * E;
+  return launched(moe::launch_group(a, (hipStream_t)stream), fn);
+}
+
+}  // extern "C"

@@ -320,6 +320,107 @@ int moe_ep_remap(const int32_t *topk_ids, const float *topk_weights, int T, int 
  * other forms, for the cases above, or for an unknown form.  Host only. */
 int moe_plan_set_activation(moe_plan_t plan, int act);
 
+/* ---- products over ragged groups of rows ------------------------------
+ *
+ * Experts whose weights are 16-bit values or 8-bit integers, as plain products
+ * over rows sorted by expert: the building blocks of a layer that is trained,
+ * or whose weights are not in one of moe_run's block-scaled formats.
+ *
+ * Group e (0 <= e < E) holds the rows first[e] .. first[e+1] - 1 of R rows in
+ * all; `first` is a device int32 [E+1] array, non-decreasing, of values in
+ * [0, R] (values outside are clamped, so they cost rows, never a fault).
+ * Groups may be empty, and rows before first[0] or from first[E] on belong to
+ * none: nothing reads them, and the row outputs keep what they held there.
+ * Nothing is copied to the host: offsets and row numbers are read on the GPU.
+ *
+ * `rows` (device int32 [R] or NULL) names the row of x behind each product row
+ * (moe_group_routes' token output); x then has x_rows rows, and a number
+ * outside [0, x_rows) stands for a row of zeros.  NULL: row r of x itself.
+ *
+ * Matrices are row-major and contiguous, 16-byte aligned; N and K are
+ * multiples of 8 (K of 16 for the integer products) up to 2^20, E 1 .. 1024.
+ * Sums are kept in fp32 (exact int32 for integers) and rounded once, to
+ * nearest even, on output.  No kernel uses atomics: results repeat bit for bit.
+ * All calls are stream-ordered, neither allocate nor synchronise, and may be
+ * captured in a HIP graph.  They work in `scratch` (device, 16-byte aligned,
+ * at least moe_mm_scratch_bytes of the call's op and sizes; NULL when that is
+ * 0), which calls that can overlap must not share.  A call with R = 0 does
+ * nothing, except moe_grouped_mm_dw, whose sums are then zeros.
+ */
+typedef enum { MOE_T_BF16 = 1, MOE_T_FP16 = 2, MOE_T_FP32 = 3 } moe_dtype;
+typedef enum { MOE_MM_FORWARD = 1, MOE_MM_DX = 2, MOE_MM_DW = 3, MOE_MM_INT8 = 4 } moe_mm_op;
+
+/* Scratch bytes of one product: op as in moe_mm_op (MOE_MM_FORWARD is
+ * moe_grouped_mm, MOE_MM_INT8 moe_int8_mm with E = 1 and R = M, and
+ * moe_grouped_int8_mm).  Host only; 0 on sizes that the call refuses. */
+size_t moe_mm_scratch_bytes(int op, int E, int R, int N, int K);
+
+/*
+ * moe_grouped_mm -- out[r, n] = sum_k x[row(r), k] * w[e, n, k] for the rows r
+ * of group e.
+ *   dtype      MOE_T_BF16 or MOE_T_FP16: type of x and w
+ *   x          [x_rows, K];  w [E, N, K]
+ *   out_dtype  dtype or MOE_T_FP32;  out [R, N]
+ */
+int moe_grouped_mm(int dtype, const void *x, long long x_rows, const int32_t *rows, const void *w,
+                   const int32_t *first, int E, int R, int N, int K, int out_dtype, void *out, void *scratch,
+                   size_t scratch_bytes, void *stream);
+
+/* moe_grouped_mm_dx -- the gradient for the product rows:
+ * dx[r, k] = sum_n dy[r, n] * w[e, n, k]; dy [R, N], dx [R, K].  With `rows`
+ * in the forward product, a row of x receives the sum over its product rows,
+ * which is the caller's (moe_group_routes' inverse lists them). */
+int moe_grouped_mm_dx(int dtype, const void *dy, const void *w, const int32_t *first, int E, int R, int N, int K,
+                      int out_dtype, void *dx, void *scratch, size_t scratch_bytes, void *stream);
+
+/* moe_grouped_mm_dw -- the gradient for the weights:
+ * dw[e, n, k] = sum over the rows r of group e of dy[r, n] * x[row(r), k];
+ * dw [E, N, K], zeros for an empty group.  accumulate (fp32 dw only) adds to
+ * what dw holds instead. */
+int moe_grouped_mm_dw(int dtype, const void *dy, const void *x, long long x_rows, const int32_t *rows,
+                      const int32_t *first, int E, int R, int N, int K, int out_dtype, int accumulate, void *dw,
+                      void *scratch, size_t scratch_bytes, void *stream);
+
+/*
+ * moe_quant_int8 -- rows of bf16 or fp16 to 8-bit integers with one scale a row:
+ * scales[r] = fp32(max_k |x[r, k]| / 127), q[r, k] = x[r, k] / scales[r] rounded
+ * to the nearest integer, ties to even (of the exact quotient).  A row of zeros
+ * has scale 0 and codes 0; a row that holds an infinity or NaN has scale NaN and
+ * codes 0, so that its products are NaN.  cols % 16 == 0.  Quantises tokens'
+ * rows before moe_int8_mm, and weights [N, K] (or [E * N, K]) a channel.
+ */
+int moe_quant_int8(int dtype, const void *x, int rows, int cols, int8_t *q, float *scales, void *stream);
+
+/*
+ * moe_int8_mm -- out[m, n] = x_scales[m] * w_scales[n] * sum_k x[m, k] * w[n, k]
+ * over 8-bit integers x [M, K] and w [N, K], the sum exact in 32 bits (K up to
+ * 131056).  out_dtype MOE_T_BF16, MOE_T_FP16 or MOE_T_FP32.
+ * moe_grouped_int8_mm -- the same over groups: w [E, N, K], w_scales [E, N],
+ * x_scales [x_rows] by row of x.
+ */
+int moe_int8_mm(const int8_t *x, const float *x_scales, const int8_t *w, const float *w_scales, int M, int N, int K,
+                int out_dtype, void *out, void *scratch, size_t scratch_bytes, void *stream);
+int moe_grouped_int8_mm(const int8_t *x, const float *x_scales, long long x_rows, const int32_t *rows, const int8_t *w,
+                        const float *w_scales, const int32_t *first, int E, int R, int N, int K, int out_dtype,
+                        void *out, void *scratch, size_t scratch_bytes, void *stream);
+
+/*
+ * moe_group_routes -- the routes of a batch sorted by expert, for the products
+ * above: route r = t * top_k + j of token t, slot j, in ascending order inside
+ * an expert.  Ids outside [0, E) belong to no group.
+ *   topk_ids  device int32 [T, top_k]
+ *   first     device int32 [E+1]: offsets of the experts' rows
+ *   order     device int32 [T * top_k]: the route behind each sorted row, and
+ *             token its token (order / top_k); -1 from row first[E] on
+ *   inverse   device int32 [T, top_k]: the sorted row of each route, or -1
+ *   scratch   device buffer of moe_group_routes_scratch_bytes (0: may be NULL)
+ * top_k 1 .. 64, E 1 .. 1024, T * top_k up to 2^30; T = 0 writes first only.
+ * Stream-ordered, no allocation, no synchronisation (graph-capturable).
+ */
+size_t moe_group_routes_scratch_bytes(int T, int top_k, int E);
+int moe_group_routes(const int32_t *topk_ids, int T, int top_k, int E, int32_t *first, int32_t *order, int32_t *token,
+                     int32_t *inverse, void *scratch, size_t scratch_bytes, void *stream);
+
 /* ---- instrumentation ------------------------------------------------- */
 
 /* Stage timing for benchmarks: after this call, each moe_run under `plan`
