@@ -5,53 +5,6 @@
 
 namespace moe {
 
-// Group, first row and row count of row tile `tile` (tiles of BM rows, groups
-// in order); rows == 0 when the groups hold fewer tiles.  One wave reads 64
-// offsets at a time and scans their tile counts; every wave of a block does
-// the same work, so no barrier is needed.
-struct MmTile {
-  int e, row0, rows;
-};
-
-template <int BM>
-__device__ MmTile mm_tile(const MmArgs &a, int tile) {
-  MmTile t = {0, 0, 0};
-  if (!a.first) {
-    t.row0 = tile * BM;
-    t.rows = min(BM, a.R - t.row0);
-    return t;
-  }
-  const int lane = threadIdx.x & 63;
-  int run = 0;
-  for (int b = 0; b < a.E; b += 64) {
-    const int e = b + lane;
-    int lo = 0, hi = 0;
-    if (e < a.E) {
-      lo = min(max(a.first[e], 0), a.R);
-      hi = min(max(a.first[e + 1], lo), a.R);
-    }
-    const int c = (hi - lo + BM - 1) / BM;
-    int s = c;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(s, d);
-      if (lane >= d) s += v;
-    }
-    const int total = __shfl(s, 63);
-    if (tile < run + total) {
-      const unsigned long long m = __ballot(run + s > tile);
-      const int src = __ffsll(m) - 1;
-      const int before = run + __shfl(s - c, src);
-      t.e = b + src;
-      t.row0 = __shfl(lo, src) + (tile - before) * BM;
-      t.rows = max(0, min(BM, __shfl(hi, src) - t.row0));
-      return t;
-    }
-    run += total;
-  }
-  return t;
-}
-
 template <int TYPE>
 struct MmElem;
 template <>
@@ -79,134 +32,410 @@ struct MmElem<MM_I8> {
   }
 };
 
-__device__ __forceinline__ void mm_store(const MmArgs &a, long at, float v) {
+// Eight or four consecutive results (16- or 8-byte aligned in the output's type).
+__device__ __forceinline__ uint32_t mm_pack(int out_type, float lo, float hi) {
+  if (out_type == MM_BF16) return pack_bf16x2(lo, hi);
+  return __builtin_bit_cast(uint32_t, v2h{(_Float16)lo, (_Float16)hi});
+}
+
+__device__ __forceinline__ void mm_store4(const MmArgs &a, long at, const float *v) {
   if (a.out_type == MM_FP32) {
-    float *o = (float *)a.out + at;
-    *o = a.accumulate ? *o + v : v;
-  } else if (a.out_type == MM_BF16) {
-    ((uint16_t *)a.out)[at] = (uint16_t)pack_bf16x2(v, 0.f);
+    v4f *o = (v4f *)((float *)a.out + at);
+    v4f r = v4f{v[0], v[1], v[2], v[3]};
+    if (a.accumulate) r += *o;
+    *o = r;
   } else {
-    ((_Float16 *)a.out)[at] = (_Float16)v;
+    typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+    *(v2u *)((uint16_t *)a.out + at) = v2u{mm_pack(a.out_type, v[0], v[1]), mm_pack(a.out_type, v[2], v[3])};
   }
 }
 
-// 64 x 64 output tile per block of four waves (32 x 32 each, 16 x 16 MFMAs),
-// operands staged in LDS with the reduction contiguous.  P holds the output's
-// contiguous side, Q its rows.
-template <int OP, int TYPE>
-__global__ __launch_bounds__(256) void k_mm(MmArgs a) {
+__device__ __forceinline__ void mm_store8(const MmArgs &a, long at, const float *v) {
+  if (a.out_type == MM_FP32) {
+    mm_store4(a, at, v);
+    mm_store4(a, at + 4, v + 4);
+  } else {
+    typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+    *(v4u *)((uint16_t *)a.out + at) = v4u{mm_pack(a.out_type, v[0], v[1]), mm_pack(a.out_type, v[2], v[3]),
+                                           mm_pack(a.out_type, v[4], v[5]), mm_pack(a.out_type, v[6], v[7])};
+  }
+}
+
+// ------------------------------------------------------------ tile kernels
+
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+constexpr uint32_t kOutside = 0x80000000u;   // lane offset past every resource: loads zeros
+
+// A gathered row that names no row of x, and the part of a row past its end,
+// are read from here.
+__device__ const uint32_t g_mm_zeros[4] = {0, 0, 0, 0};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ Rsrc mm_rsrc(const uint8_t *base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)bytes, 0x00020000);
+}
+
+// Row range of group e.
+__device__ __forceinline__ void mm_group(const MmArgs &a, int e, int &lo, int &hi) {
+  if (!a.first) {
+    lo = 0;
+    hi = a.R;
+  } else {
+    lo = min(max(a.first[e], 0), a.R);
+    hi = min(max(a.first[e + 1], lo), a.R);
+  }
+}
+
+// Inclusive scan over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+struct MmTile {
+  int e, row0, rows, pt;   // group, first row, rows of the tile; column tile
+};
+
+// The output tile of this block, from the offsets on the GPU.  Row tiles of BQ
+// rows are numbered over the groups in order; a lane counts the tiles of
+// E / 64 consecutive groups, one scan gives the total, a second over the found
+// lane's groups the tile's own.  Blocks go to the eight XCDs in turn, so XCD i
+// takes the i-th eighth of the tiles that exist (not of the launch's upper
+// bound, whose surplus blocks would all land on the last XCD), and inside it
+// kMmGroup row tiles share each column tile of the weights before the next one
+// is read.  Every wave does the same work: no barrier.
+constexpr int kMmGroup = 4;
+
+template <int BQ>
+__device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile &t) {
+  const int lane = threadIdx.x & 63;
+  const int per = (a.E + 63) >> 6;
+  int cnt = 0;
+  for (int i = 0; i < per; i++) {
+    const int e = lane * per + i;
+    int lo = 0, hi = 0;
+    if (e < a.E) mm_group(a, e, lo, hi);
+    cnt += (hi - lo + BQ - 1) / BQ;
+  }
+  const int sum = wave_scan(cnt);
+  const int total = uniform(__shfl(sum, 63)), nt = total * ptiles;
+  const int chunk = (nt + 7) >> 3, b = (int)blockIdx.x;
+  const int id = (b & 7) * chunk + (b >> 3);
+  if ((b >> 3) >= chunk || id >= nt) return false;
+  const int grp = id / (kMmGroup * ptiles), rem = id - grp * kMmGroup * ptiles;
+  const int gcur = min(kMmGroup, total - grp * kMmGroup);
+  t.pt = rem / gcur;
+  const int rt = grp * kMmGroup + rem % gcur;
+  const int src = __ffsll(__ballot(sum > rt)) - 1;
+  const int before = __shfl(sum - cnt, src);
+  const int e = src * per + lane;
+  int lo = 0, hi = 0;
+  if (lane < per && e < a.E) mm_group(a, e, lo, hi);
+  const int c = (hi - lo + BQ - 1) / BQ, s2 = wave_scan(c);
+  const int at = __ffsll(__ballot(before + s2 > rt)) - 1;
+  const int k = rt - before - __shfl(s2 - c, at);
+  t.e = uniform(src * per + at);
+  t.row0 = uniform(__shfl(lo, at) + k * BQ);
+  t.rows = min(BQ, uniform(__shfl(hi, at)) - t.row0);
+  return t.rows > 0;
+}
+
+// Row of x behind product row r, or -1.
+__device__ __forceinline__ long mm_x_row(const MmArgs &a, int r) {
+  if (!a.rows) return r;
+  const int x = a.rows[r];
+  return x >= 0 && x < a.x_rows ? (long)x : -1l;
+}
+
+// LDS images of an operand tile, 128 bytes of the reduction (one step) by B
+// outer indices.  Reduction-contiguous operands: B rows of eight 16-byte
+// chunks, chunk c of row r at slot c ^ swz(r); transposed ones: 64 rows of B
+// 16-bit columns, chunk c of row z at c ^ 2 (z & 7).  Either way the 16 (or,
+// transposed, 32) lanes that read together touch every bank once.
+//   Q rows are read 16 consecutive ones a fragment: swz = (r >> 1) & 7.
+//   P rows are read as 4 runs of 4, 16 apart (below): bits 1, 4 and 5 of r.
+__device__ __forceinline__ int swz_q(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int swz_p(int r) { return ((r >> 1) & 1) | ((r >> 3) & 6); }
+
+// The MFMA's rows are the output's contiguous dimension (P: weights, or x for
+// the weight gradient), its columns the output's rows (Q), so a lane's four
+// results are contiguous.  With a reduction-contiguous P, row a of fragment j
+// of a 64-row group is row 16 (a / 4) + 4 j + a % 4: a lane then holds 16
+// consecutive outputs over the four fragments, stored 16 bytes at a time.
+template <int OP, int TYPE, int BQ, int BP, int WQ, int WP, bool GATHER, int MINW>
+__global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   typedef MmElem<TYPE> M;
-  typedef typename M::t T;
-  constexpr int ZB = 64 / sizeof(T);        // reduction elements per step: 64 bytes
-  constexpr int C = 16 / sizeof(T);         // elements per 16-byte chunk
-  __shared__ __align__(16) T lp[64][ZB + C], lq[64][ZB + C];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  constexpr int ES = sizeof(typename M::t), NW = WQ * WP;
+  constexpr bool TQ_T = OP == MM_DW, TP_T = OP != MM_FORWARD;   // transposed operands
+  constexpr int TQ = BQ / WQ, TP = BP / WP, NQ = TQ / 16, NP = TP / 16;
+  constexpr int CQ = BQ / 8 / NW, CP = BP / 8 / NW;             // loads of 1 KB a wave and step
+  constexpr int kStage = (BQ + BP) * 128;
+  static_assert(TP % 64 == 0 && TQ % 16 == 0 && CQ >= 1 && CP >= 1, "tile shape");
+  static_assert(!TQ_T || (BQ % 128 == 0 && TQ % 64 == 0), "transposed Q");
+  static_assert(!TP_T || BP % 128 == 0, "transposed P");
+  __shared__ __align__(1024) uint8_t lds[2 * kStage];
+
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  const int pn = OP == MM_FORWARD ? a.N : a.K;                  // output columns
+  const int ptiles = (pn + BP - 1) / BP;
   MmTile t;
-  int q0, qn, p0 = (int)blockIdx.x * 64, pn, zn;
+  int q0 = 0, qn, zn;                                           // output rows of the tile, reduction
   if (OP == MM_DW) {
-    t.e = blockIdx.z;
-    const int lo = min(max(a.first ? a.first[t.e] : 0, 0), a.R);
-    t.row0 = lo;
-    t.rows = (a.first ? min(max(a.first[t.e + 1], lo), a.R) : a.R) - lo;
-    q0 = blockIdx.y * 64;
-    qn = a.N;
-    pn = a.K;
+    // each group's tiles spread over the XCDs, so that a large group does not load one of them
+    const int tiles = ((a.N + BQ - 1) / BQ) * ptiles, per8 = (tiles + 7) >> 3;
+    const int b = (int)blockIdx.x >> 3, id = ((int)blockIdx.x & 7) * per8 + b % per8;
+    t.e = b / per8;
+    if (id >= tiles) return;
+    t.pt = id % ptiles;
+    q0 = (id / ptiles) * BQ;
+    int lo, hi;
+    mm_group(a, t.e, lo, hi);
+    t.row0 = uniform(lo);
+    t.rows = uniform(hi) - t.row0;
+    qn = min(BQ, a.N - q0);
     zn = t.rows;
   } else {
-    t = mm_tile<64>(a, blockIdx.y);
-    if (t.rows <= 0) return;
-    q0 = 0;
+    if (!mm_find_tile<BQ>(a, ptiles, t)) return;
     qn = t.rows;
-    pn = OP == MM_FORWARD ? a.N : a.K;
     zn = OP == MM_FORWARD ? a.K : a.N;
   }
-  const T *x = (const T *)a.x, *dy = (const T *)a.dy, *wt = (const T *)a.w + (long)t.e * a.N * a.K;
-  // 16 bytes of row i of x behind product row r, zeros where there is none
-  auto x_chunk = [&](int r, int col) -> v4i {
-    long xr = r;
-    if (a.rows) {
-      xr = a.rows[r];
-      if (xr < 0 || xr >= a.x_rows) return v4i{0, 0, 0, 0};
-    }
-    return *(const v4i *)(x + xr * a.K + col);
-  };
-  typename M::acc acc[2][2] = {};
-  for (int z0 = 0; z0 < zn; z0 += ZB) {
-    __syncthreads();
-    // Q
-    if (OP != MM_DW) {
-      const int row = tid >> 2, col = z0 + (tid & 3) * C;
-      v4i v = {0, 0, 0, 0};
-      if (row < qn && col < zn)
-        v = OP == MM_FORWARD ? x_chunk(t.row0 + row, col) : *(const v4i *)(dy + (long)(t.row0 + row) * a.N + col);
-      *(v4i *)&lq[row][(tid & 3) * C] = v;
+  const int p0 = t.pt * BP;
+  constexpr int ZS = (TQ_T || TP_T) ? 64 : 128 / ES;            // reduction elements a step
+  const int steps = (zn + ZS - 1) / ZS;
+  const int tail = (zn - (steps - 1) * ZS) * ES;                // bytes of the last step (contiguous operands)
+
+  // ---- loads of one step
+  const uint8_t *x = (const uint8_t *)a.x, *dy = (const uint8_t *)a.dy;
+  const uint8_t *wt = (const uint8_t *)a.w + (size_t)t.e * a.N * a.K * ES;
+  const uint32_t ldx = (uint32_t)a.K * ES, ldy = (uint32_t)a.N * ES;
+
+  uint32_t vq[CQ], vp[CP];
+  int cq[CQ], cp[CP];                    // chunk's byte within the step (contiguous operands)
+  const uint8_t *gx[GATHER && OP == MM_FORWARD ? CQ : 1];
+  int ginc[GATHER && OP == MM_FORWARD ? CQ : 1], gidx[GATHER && OP == MM_DW ? CP : 1];
+#pragma unroll
+  for (int i = 0; i < CQ; i++) {
+    if (!TQ_T) {
+      const int r = (i * NW + w) * 8 + (lane >> 3);
+      cq[i] = ((lane & 7) ^ swz_q(r)) * 16;
+      vq[i] = (uint32_t)r * (OP == MM_FORWARD ? ldx : ldy) + cq[i];
+      if constexpr (GATHER && OP == MM_FORWARD) {
+        const long xr = r < qn ? mm_x_row(a, t.row0 + r) : -1;
+        gx[i] = xr < 0 ? (const uint8_t *)g_mm_zeros : x + xr * ldx + cq[i];
+        ginc[i] = xr < 0 ? 0 : 128;
+      }
     } else {
-      const int z = tid >> 3, col = q0 + (tid & 7) * 8;
-      v4i v = {0, 0, 0, 0};
-      if (z0 + z < zn && col < qn) v = *(const v4i *)(dy + (long)(t.row0 + z0 + z) * a.N + col);
-      for (int i = 0; i < 8; i++) lq[(tid & 7) * 8 + i][z] = (T)((uint32_t)v[i >> 1] >> (16 * (i & 1)));
+      constexpr int LR = BQ / 8;         // lanes a row
+      const int z = (i * NW + w) * (64 / LR) + lane / LR;
+      vq[i] = (uint32_t)z * ldy + (uint32_t)(q0 * 2 + (((lane % LR) ^ (2 * (z & 7))) * 16));
     }
-    // P
-    if (OP == MM_FORWARD) {
-      const int row = p0 + (tid >> 2), col = z0 + (tid & 3) * C;
-      v4i v = {0, 0, 0, 0};
-      if (row < pn && col < zn) v = *(const v4i *)(wt + (long)row * a.K + col);
-      *(v4i *)&lp[tid >> 2][(tid & 3) * C] = v;
-    } else {
-      const int z = tid >> 3, col = p0 + (tid & 7) * 8;
-      v4i v = {0, 0, 0, 0};
-      if (z0 + z < zn && col < pn)
-        v = OP == MM_DX ? *(const v4i *)(wt + (long)(z0 + z) * a.K + col) : x_chunk(t.row0 + z0 + z, col);
-      for (int i = 0; i < 8; i++) lp[(tid & 7) * 8 + i][z] = (T)((uint32_t)v[i >> 1] >> (16 * (i & 1)));
-    }
-    __syncthreads();
-    v4i fp[2], fq[2];
-    for (int i = 0; i < 2; i++) {
-      fp[i] = *(const v4i *)&lp[32 * (w & 1) + 16 * i + (lane & 15)][(lane >> 4) * C];
-      fq[i] = *(const v4i *)&lq[32 * (w >> 1) + 16 * i + (lane & 15)][(lane >> 4) * C];
-    }
-    for (int i = 0; i < 2; i++)
-      for (int j = 0; j < 2; j++) acc[i][j] = M::mma(fp[i], fq[j], acc[i][j]);
   }
-  for (int i = 0; i < 2; i++)
-    for (int j = 0; j < 2; j++) {
-      const int q = q0 + 32 * (w >> 1) + 16 * j + (lane & 15), p = p0 + 32 * (w & 1) + 16 * i + 4 * (lane >> 4);
-      if (q >= qn) continue;
-      const long row = OP == MM_DW ? (long)t.e * a.N + q : t.row0 + q;
-      for (int k = 0; k < 4; k++) {
-        if (p + k >= pn) continue;
-        float v = (float)acc[i][j][k];
-        if (TYPE == MM_I8) {
-          long xr = row;
-          if (a.rows) {
-            xr = a.rows[row];
-            if (xr < 0 || xr >= a.x_rows) xr = -1;
-          }
-          v = xr < 0 ? 0.f : v * a.x_scales[xr] * a.w_scales[(long)t.e * a.N + p + k];
-        }
-        mm_store(a, row * pn + p + k, v);
+#pragma unroll
+  for (int i = 0; i < CP; i++) {
+    if (!TP_T) {
+      const int r = (i * NW + w) * 8 + (lane >> 3);
+      cp[i] = ((lane & 7) ^ swz_p(r)) * 16;
+      vp[i] = (uint32_t)r * ldx + cp[i];
+    } else {
+      constexpr int LR = BP / 8;
+      const int z = (i * NW + w) * (64 / LR) + lane / LR;
+      const uint32_t col = (uint32_t)(p0 * 2 + (((lane % LR) ^ (2 * (z & 7))) * 16));
+      vp[i] = (uint32_t)z * ldx + col;
+      cp[i] = (int)col;
+    }
+  }
+  const Rsrc rq = OP == MM_FORWARD  ? mm_rsrc(x + (GATHER ? 0 : (size_t)t.row0 * ldx), (uint32_t)qn * ldx)
+                  : OP == MM_DX     ? mm_rsrc(dy + (size_t)t.row0 * ldy, (uint32_t)qn * ldy)
+                                    : mm_rsrc(dy, 0);
+  const Rsrc rp = OP == MM_FORWARD ? mm_rsrc(wt + (size_t)p0 * ldx, (uint32_t)min(BP, pn - p0) * ldx) : mm_rsrc(wt, 0);
+
+  auto gather_rows = [&](int s) {        // weight gradient: rows of x behind the rows of step s
+    if constexpr (GATHER && OP == MM_DW) {
+#pragma unroll
+      for (int i = 0; i < CP; i++) {
+        const int z = s * 64 + (i * NW + w) * (64 / (BP / 8)) + lane / (BP / 8);
+        gidx[i] = z < zn ? a.rows[t.row0 + z] : -1;
       }
     }
+  };
+  auto load = [&](int s, int buf) {
+    uint8_t *lq = lds + buf * kStage, *lp = lq + BQ * 128;
+    const bool last = s == steps - 1;
+    // reduction rows left for transposed operands: rows past them load zeros
+    const uint32_t zleft = (uint32_t)min(ZS, zn - s * ZS);
+    const Rsrc sq = TQ_T ? mm_rsrc(dy + (size_t)(t.row0 + s * 64) * ldy, zleft * ldy) : rq;
+    const Rsrc sp = OP == MM_DX   ? mm_rsrc(wt + (size_t)(s * 64) * ldx, zleft * ldx)
+                    : OP == MM_DW ? mm_rsrc(x + (size_t)(t.row0 + s * 64) * ldx, zleft * ldx)
+                                  : rp;
+#pragma unroll
+    for (int i = 0; i < CQ; i++) {
+      lds_void *dst = (lds_void *)(lq + (i * NW + w) * 1024);
+      if constexpr (GATHER && OP == MM_FORWARD) {
+        const uint8_t *g = last && cq[i] >= tail ? (const uint8_t *)g_mm_zeros : gx[i];
+        __builtin_amdgcn_global_load_lds(g, dst, 16, 0, 0);
+        gx[i] += ginc[i];
+      } else {
+        const uint32_t v = !TQ_T && last && cq[i] >= tail ? kOutside : vq[i];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(sq, dst, 16, (int)v, TQ_T ? 0 : s * 128, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < CP; i++) {
+      lds_void *dst = (lds_void *)(lp + (i * NW + w) * 1024);
+      if constexpr (GATHER && OP == MM_DW) {
+        const bool ok = gidx[i] >= 0 && gidx[i] < a.x_rows && (uint32_t)cp[i] < ldx;
+        const uint8_t *g = ok ? x + (size_t)gidx[i] * ldx + cp[i] : (const uint8_t *)g_mm_zeros;
+        __builtin_amdgcn_global_load_lds(g, dst, 16, 0, 0);
+      } else {
+        const uint32_t v = !TP_T && last && cp[i] >= tail ? kOutside : vp[i];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(sp, dst, 16, (int)v, TP_T ? 0 : s * 128, 0, 0);
+      }
+    }
+  };
+
+  // ---- fragments of one half step (64 bytes of the reduction)
+  const int wq = w / WP, wp = w % WP, g = lane >> 4, l16 = lane & 15;
+  // transposed: rows 8 g + l16 / 4 (+ 4 for the second half of a fragment's k) of the half's 32
+  const int tz = 8 * g + (l16 >> 2), tsw = 2 * (l16 >> 2);
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4s lds_v4s;
+  auto frag_t = [&](const uint8_t *tile, int rb, int col, int h) -> v4i {
+    // col: first of the fragment's 16 columns
+    const int c = (col >> 3) + ((l16 & 3) >> 1);
+    const uint8_t *p = tile + (32 * h + tz) * rb + 8 * (l16 & 1);
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + ((c ^ tsw) * 16)));
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + 4 * rb + ((c ^ tsw ^ 8) * 16)));
+    return __builtin_bit_cast(v4i, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto frag_q = [&](const uint8_t *tile, int j, int h) -> v4i {
+    if (TQ_T) return frag_t(tile, BQ * 2, wq * TQ + 16 * j, h);
+    const int r = wq * TQ + 16 * j + l16;
+    return *(const v4i *)(tile + r * 128 + (((4 * h + g) ^ swz_q(r)) * 16));
+  };
+  auto frag_p = [&](const uint8_t *tile, int j, int h) -> v4i {
+    if (TP_T) return frag_t(tile, BP * 2, wp * TP + 16 * j, h);
+    const int r = wp * TP + (j >> 2) * 64 + (l16 >> 2) * 16 + (j & 3) * 4 + (l16 & 3);
+    return *(const v4i *)(tile + r * 128 + (((4 * h + g) ^ swz_p(r)) * 16));
+  };
+
+  typename M::acc acc[NP][NQ];
+#pragma unroll
+  for (int i = 0; i < NP; i++)
+#pragma unroll
+    for (int j = 0; j < NQ; j++) acc[i][j] = typename M::acc{0, 0, 0, 0};
+
+  if (steps > 0) {
+    gather_rows(0);
+    load(0, 0);
+    gather_rows(1);
+  }
+  for (int s = 0; s < steps; s++) {
+    // this step's tiles are in LDS once every wave's loads have landed; the
+    // other buffer is free once every wave has read its fragments of the step before
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_barrier();
+    const uint8_t *lq = lds + (s & 1) * kStage, *lp = lq + BQ * 128;
+    v4i fq[2][NQ], fp[2][NP];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+      for (int j = 0; j < NP; j++) fp[h][j] = frag_p(lp, j, h);
+#pragma unroll
+      for (int j = 0; j < NQ; j++) fq[h][j] = frag_q(lq, j, h);
+    }
+    if (s + 1 < steps) {
+      load(s + 1, (s + 1) & 1);
+      gather_rows(s + 2);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int j = 0; j < NQ; j++)
+#pragma unroll
+        for (int i = 0; i < NP; i++) acc[i][j] = M::mma(fp[h][i], fq[h][j], acc[i][j]);
+  }
+
+  // ---- outputs
+#pragma unroll
+  for (int j = 0; j < NQ; j++) {
+    const int q = wq * TQ + 16 * j + l16;
+    if (q >= qn) continue;
+    const long row = OP == MM_DW ? (long)t.e * a.N + q0 + q : (long)t.row0 + q;
+    float xs = 0.f;
+    if (TYPE == MM_I8) {
+      const long xr = mm_x_row(a, (int)row);
+      xs = xr < 0 ? 0.f : a.x_scales[xr];
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < NP; i0 += 4) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int k = 0; k < 4; k++) v[4 * i + k] = (float)acc[i0 + i][j][k];
+      const int pc = p0 + wp * TP + 16 * i0;
+      if (!TP_T) {                       // 16 consecutive columns
+        const int p = pc + 16 * g;
+        if (TYPE == MM_I8) {
+          const float *ws = a.w_scales + (size_t)t.e * a.N;
+#pragma unroll
+          for (int k = 0; k < 16; k++) v[k] *= xs * (p + k < pn ? ws[p + k] : 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; k += 8)
+          if (p + k < pn) mm_store8(a, row * pn + p + k, v + k);
+      } else {                           // four runs of 4 columns, 16 apart
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int p = pc + 16 * i + 4 * g;
+          if (p < pn) mm_store4(a, row * pn + p, v + 4 * i);
+        }
+      }
+    }
+  }
 }
 
-template <int OP, int TYPE>
-static hipError_t launch_mm_simple(const MmArgs &a, hipStream_t s) {
-  const int pn = OP == MM_FORWARD ? a.N : a.K;
-  const int tiles = a.first ? (a.R + 63) / 64 + (a.E < a.R ? a.E : a.R) : (a.R + 63) / 64;
-  const dim3 grid((pn + 63) / 64, OP == MM_DW ? (a.N + 63) / 64 : tiles, OP == MM_DW ? a.E : 1);
-  hipLaunchKernelGGL((k_mm<OP, TYPE>), grid, dim3(256), 0, s, a);
+template <int OP, int TYPE, int BQ, int BP, int WQ, int WP, int MINW>
+static hipError_t launch_tile(const MmArgs &a, hipStream_t s) {
+  const long pn = OP == MM_FORWARD ? a.N : a.K, ptiles = (pn + BP - 1) / BP;
+  long blocks;
+  if (OP == MM_DW) blocks = 8l * a.E * (((a.N + BQ - 1) / BQ * ptiles + 7) / 8);
+  else blocks = (((a.R + BQ - 1) / BQ + (a.first ? (a.E < a.R ? a.E : a.R) : 0)) * ptiles + 7) / 8 * 8;
+  if (blocks > INT32_MAX / (64 * WQ * WP)) return hipErrorInvalidValue;
+  if (OP != MM_DX && a.rows)
+    hipLaunchKernelGGL((k_mm_tile<OP, TYPE, BQ, BP, WQ, WP, true, MINW>), dim3((unsigned)blocks), dim3(64 * WQ * WP), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_mm_tile<OP, TYPE, BQ, BP, WQ, WP, false, MINW>), dim3((unsigned)blocks), dim3(64 * WQ * WP), 0, s, a);
   return hipGetLastError();
 }
 
+template <int TYPE>
+static hipError_t launch_forward(const MmArgs &a, hipStream_t s) {
+  const long avg = a.R / a.E;
+  if (avg >= 160) return launch_tile<MM_FORWARD, TYPE, 256, 256, 2, 4, 2>(a, s);
+  if (avg >= 96) return launch_tile<MM_FORWARD, TYPE, 128, 256, 2, 4, 2>(a, s);
+  return launch_tile<MM_FORWARD, TYPE, 64, 256, 1, 4, 2>(a, s);
+}
+
+template <int TYPE>
+static hipError_t launch_16bit(const MmArgs &a, hipStream_t s) {
+  if (a.op == MM_FORWARD) return launch_forward<TYPE>(a, s);
+  if (a.op == MM_DW) return launch_tile<MM_DW, TYPE, 256, 256, 2, 4, 2>(a, s);
+  const long avg = a.R / a.E;
+  if (avg >= 160) return launch_tile<MM_DX, TYPE, 256, 256, 2, 4, 2>(a, s);
+  return launch_tile<MM_DX, TYPE, 64, 256, 1, 4, 2>(a, s);
+}
+
 hipError_t launch_mm(const MmArgs &a, hipStream_t s) {
-  if (a.type == MM_I8) return launch_mm_simple<MM_FORWARD, MM_I8>(a, s);
-  if (a.type == MM_BF16)
-    return a.op == MM_FORWARD ? launch_mm_simple<MM_FORWARD, MM_BF16>(a, s)
-           : a.op == MM_DX    ? launch_mm_simple<MM_DX, MM_BF16>(a, s)
-                              : launch_mm_simple<MM_DW, MM_BF16>(a, s);
-  return a.op == MM_FORWARD ? launch_mm_simple<MM_FORWARD, MM_FP16>(a, s)
-         : a.op == MM_DX    ? launch_mm_simple<MM_DX, MM_FP16>(a, s)
-                            : launch_mm_simple<MM_DW, MM_FP16>(a, s);
+  return a.type == MM_I8     ? launch_forward<MM_I8>(a, s)
+         : a.type == MM_BF16 ? launch_16bit<MM_BF16>(a, s)
+                             : launch_16bit<MM_FP16>(a, s);
 }
 
 }  // namespace moe
