@@ -355,7 +355,7 @@ def _codes():
 
 def _operands(named):
     """Checks (name, tensor, dtypes, shape) operands: types and shapes first, then that all are
-    contiguous on one GPU. Optional tensors are left out by the caller."""
+    contiguous on one GPU, whose device index it returns. Optional tensors are left out by the caller."""
     for name, t, dtypes, shape in named:
         if t is None:
             raise ValueError(f"{name} is required")
@@ -363,14 +363,14 @@ def _operands(named):
             raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    dev = named[0][1].device
+    dev = named[0][1].get_device()
     for name, t, _, _ in named:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError(f"{name} must be a device tensor")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {dev}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {named[0][1].device}")
     return dev
 
 
@@ -383,27 +383,30 @@ def _use(stream, t):
 
 
 def _launch(dev, fn, *args):
-    """fn(*args, stream) on the operands' device and that device's current stream."""
+    """fn(*args, stream) on device dev and its current stream (by its handle: building a Stream
+    object takes longer than the launch)."""
     import torch
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if rc != MOE_OK:
+        _check(rc)
 
 
-def _mm_scratch(op, E, R, N, K, scratch, dev):
+def _mm_scratch(op, E, R, N, K, scratch, like):
     """(pointer, bytes, tensor) of a product's scratch: the caller's tensor, or one made here when it needs any."""
     import torch
     if scratch is not None:
         _need(scratch, "scratch", torch.uint8)
-        if scratch.device != dev:
-            raise ValueError(f"scratch is on {scratch.device}, the operands on {dev}")
+        if scratch.device != like.device:
+            raise ValueError(f"scratch is on {scratch.device}, the operands on {like.device}")
         return scratch.data_ptr(), scratch.numel(), scratch
     need = _lib.load().moe_mm_scratch_bytes(op, E, R, N, K)
     if not need:
         return None, 0, None
-    scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+    scratch = torch.empty(need, dtype=torch.uint8, device=like.device)
     return scratch.data_ptr(), need, scratch
 
 
@@ -412,13 +415,12 @@ def mm_scratch_bytes(op: int, E: int, R: int, N: int, K: int) -> int:
     return _lib.load().moe_mm_scratch_bytes(op, E, R, N, K)
 
 
-def _out_like(out, out_dtype, default, allowed, shape, dev, named, name="out"):
-    """The output tensor (made here unless given) and its moe_dtype."""
-    import torch
+def _out_dtype(out, out_dtype, default, allowed, shape, named):
+    """The output's type; an output that is given joins the operands to check."""
     if out is not None:
         if out_dtype is not None and out.dtype != out_dtype:
-            raise TypeError(f"{name}: expected {out_dtype}, got {out.dtype}")
-        named.append((name, out, allowed, shape))
+            raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
+        named.append(("out", out, allowed, shape))
         return out.dtype
     dt = default if out_dtype is None else out_dtype
     if dt not in allowed:
@@ -450,11 +452,11 @@ def grouped_mm(x, w, first, rows=None, out=None, out_dtype=None, scratch=None, s
     named = [("x", x, kinds, x.shape), ("w", w, (x.dtype,), (E, N, K)), ("first", first, (torch.int32,), (E + 1,))]
     if rows is not None:
         named.append(("rows", rows, (torch.int32,), (R,)))
-    dt = _out_like(out, out_dtype, x.dtype, (x.dtype, torch.float32), (R, N), x.device, named)
+    dt = _out_dtype(out, out_dtype, x.dtype, (x.dtype, torch.float32), (R, N), named)
     dev = _operands(named)
     if out is None:
-        out = torch.empty((R, N), dtype=dt, device=dev)
-    sp, sb, keep = _mm_scratch(MM_FORWARD, E, R, N, K, scratch, dev)
+        out = torch.empty((R, N), dtype=dt, device=x.device)
+    sp, sb, keep = _mm_scratch(MM_FORWARD, E, R, N, K, scratch, x)
     _launch(dev, _lib.load().moe_grouped_mm, _codes()[x.dtype], x.data_ptr(), T, _ptr(rows), w.data_ptr(),
             first.data_ptr(), E, R, N, K, _codes()[dt], out.data_ptr(), sp, sb)
     return out
@@ -473,11 +475,11 @@ def grouped_mm_dx(dy, w, first, out=None, out_dtype=None, scratch=None, stream=N
     E, _, K = _dims(w, "w", 3)
     kinds = (torch.bfloat16, torch.float16)
     named = [("dy", dy, kinds, dy.shape), ("w", w, (dy.dtype,), (E, N, K)), ("first", first, (torch.int32,), (E + 1,))]
-    dt = _out_like(out, out_dtype, dy.dtype, (dy.dtype, torch.float32), (R, K), dy.device, named)
+    dt = _out_dtype(out, out_dtype, dy.dtype, (dy.dtype, torch.float32), (R, K), named)
     dev = _operands(named)
     if out is None:
-        out = torch.empty((R, K), dtype=dt, device=dev)
-    sp, sb, keep = _mm_scratch(MM_DX, E, R, N, K, scratch, dev)
+        out = torch.empty((R, K), dtype=dt, device=dy.device)
+    sp, sb, keep = _mm_scratch(MM_DX, E, R, N, K, scratch, dy)
     _launch(dev, _lib.load().moe_grouped_mm_dx, _codes()[dy.dtype], dy.data_ptr(), w.data_ptr(),
             first.data_ptr(), E, R, N, K, _codes()[dt], out.data_ptr(), sp, sb)
     return out
@@ -505,11 +507,11 @@ def grouped_mm_dw(dy, x, first, rows=None, out=None, out_dtype=None, accumulate:
     named = [("dy", dy, kinds, dy.shape), ("x", x, (dy.dtype,), x.shape), ("first", first, (torch.int32,), (E + 1,))]
     if rows is not None:
         named.append(("rows", rows, (torch.int32,), (R,)))
-    dt = _out_like(out, out_dtype, dy.dtype, (dy.dtype, torch.float32), (E, N, K), dy.device, named)
+    dt = _out_dtype(out, out_dtype, dy.dtype, (dy.dtype, torch.float32), (E, N, K), named)
     dev = _operands(named)
     if out is None:
-        out = torch.empty((E, N, K), dtype=dt, device=dev)
-    sp, sb, keep = _mm_scratch(MM_DW, E, R, N, K, scratch, dev)
+        out = torch.empty((E, N, K), dtype=dt, device=dy.device)
+    sp, sb, keep = _mm_scratch(MM_DW, E, R, N, K, scratch, dy)
     _launch(dev, _lib.load().moe_grouped_mm_dw, _codes()[dy.dtype], dy.data_ptr(), x.data_ptr(), T, _ptr(rows),
             first.data_ptr(), E, R, N, K, _codes()[dt], int(bool(accumulate)), out.data_ptr(), sp, sb)
     return out
@@ -530,9 +532,9 @@ def quant_int8(x, out=None, scales=None, stream=None):
         named.append(("scales", scales, (torch.float32,), shape[:1]))
     dev = _operands(named)
     if out is None:
-        out = torch.empty(shape, dtype=torch.int8, device=dev)
+        out = torch.empty(shape, dtype=torch.int8, device=x.device)
     if scales is None:
-        scales = torch.empty(shape[0], dtype=torch.float32, device=dev)
+        scales = torch.empty(shape[0], dtype=torch.float32, device=x.device)
     _launch(dev, _lib.load().moe_quant_int8, _codes()[x.dtype], x.data_ptr(), shape[0], shape[1],
             out.data_ptr(), scales.data_ptr())
     return out, scales
@@ -552,11 +554,11 @@ def int8_mm(x, x_scales, w, w_scales, out=None, out_dtype=None, scratch=None, st
     N, _ = _dims(w, "w", 2)
     named = [("x", x, (torch.int8,), x.shape), ("x_scales", x_scales, (torch.float32,), (M,)),
              ("w", w, (torch.int8,), (N, K)), ("w_scales", w_scales, (torch.float32,), (N,))]
-    dt = _out_like(out, out_dtype, torch.bfloat16, tuple(_codes()), (M, N), x.device, named)
+    dt = _out_dtype(out, out_dtype, torch.bfloat16, tuple(_codes()), (M, N), named)
     dev = _operands(named)
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=dev)
-    sp, sb, keep = _mm_scratch(MM_INT8, 1, M, N, K, scratch, dev)
+        out = torch.empty((M, N), dtype=dt, device=x.device)
+    sp, sb, keep = _mm_scratch(MM_INT8, 1, M, N, K, scratch, x)
     _launch(dev, _lib.load().moe_int8_mm, x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
             M, N, K, _codes()[dt], out.data_ptr(), sp, sb)
     return out
@@ -577,11 +579,11 @@ def grouped_int8_mm(x, x_scales, w, w_scales, first, rows=None, out=None, out_dt
              ("first", first, (torch.int32,), (E + 1,))]
     if rows is not None:
         named.append(("rows", rows, (torch.int32,), (R,)))
-    dt = _out_like(out, out_dtype, torch.bfloat16, tuple(_codes()), (R, N), x.device, named)
+    dt = _out_dtype(out, out_dtype, torch.bfloat16, tuple(_codes()), (R, N), named)
     dev = _operands(named)
     if out is None:
-        out = torch.empty((R, N), dtype=dt, device=dev)
-    sp, sb, keep = _mm_scratch(MM_INT8, E, R, N, K, scratch, dev)
+        out = torch.empty((R, N), dtype=dt, device=x.device)
+    sp, sb, keep = _mm_scratch(MM_INT8, E, R, N, K, scratch, x)
     _launch(dev, _lib.load().moe_grouped_int8_mm, x.data_ptr(), x_scales.data_ptr(), T, _ptr(rows), w.data_ptr(),
             w_scales.data_ptr(), first.data_ptr(), E, R, N, K, _codes()[dt], out.data_ptr(), sp, sb)
     return out
@@ -601,15 +603,15 @@ def group_routes(topk_ids, num_experts: int, scratch=None, stream=None):
     dev = _operands([("topk_ids", topk_ids, (torch.int32,), topk_ids.shape)])
     E = int(num_experts)
     L = _lib.load()
-    first = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
-    order, token, inverse = torch.empty((3, T * k), dtype=torch.int32, device=dev).unbind(0)
+    first = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=topk_ids.device)
+    order, token, inverse = torch.empty((3, T * k), dtype=torch.int32, device=topk_ids.device).unbind(0)
     need = L.moe_group_routes_scratch_bytes(T, k, E)
     if scratch is None:
-        scratch = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        scratch = torch.empty(need, dtype=torch.uint8, device=topk_ids.device) if need else None
     else:
         _need(scratch, "scratch", torch.uint8)
-        if scratch.device != dev:
-            raise ValueError(f"scratch is on {scratch.device}, the operands on {dev}")
+        if scratch.device != topk_ids.device:
+            raise ValueError(f"scratch is on {scratch.device}, the operands on {topk_ids.device}")
     _launch(dev, L.moe_group_routes, topk_ids.data_ptr(), T, k, E, first.data_ptr(), order.data_ptr(),
             token.data_ptr(), inverse.data_ptr(), _ptr(scratch), 0 if scratch is None else scratch.numel())
     return first, order, token, inverse.view(T, k)

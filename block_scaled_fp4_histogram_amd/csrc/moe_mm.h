@@ -32,14 +32,25 @@ hipError_t launch_mm(const MmArgs &a, hipStream_t s);
 // Row quantiser: scale = fp32(amax / 127), codes = x / scale to nearest even.
 hipError_t launch_quant_int8(int type, const void *x, long rows, int cols, int8_t *q, float *scales, hipStream_t s);
 
-constexpr int kGroupChunk = 1024;    // routes one block of the grouping kernels takes
+constexpr int kGroupThreads = 1024;  // routes a block of the grouping kernels takes a round
+constexpr int kGroupFew = 256;       // most routes of the kernel without counting
+constexpr int kGroupMaxBlocks = 256; // most blocks of the counting kernels; more routes take more rounds
 
 struct GroupArgs {
   const int32_t *ids;
-  int R, topk, E, chunks;
+  int R, topk, E;
+  int blocks, rounds;                // of the two-launch form (R > 4 * kGroupThreads)
   int32_t *first, *order, *token, *inverse;
-  int32_t *hist, *rank;              // scratch of more than one chunk: [chunks][E] counts, per-route rank
+  int32_t *hist, *rank;              // its scratch: [blocks][E] counts, per-route rank
 };
+
+// Blocks and rounds of R routes in the two-launch form.
+constexpr int group_rounds(long R) {
+  return (int)((R + (long)kGroupThreads * kGroupMaxBlocks - 1) / ((long)kGroupThreads * kGroupMaxBlocks));
+}
+constexpr int group_blocks(long R) {
+  return (int)((R + (long)kGroupThreads * group_rounds(R) - 1) / ((long)kGroupThreads * group_rounds(R)));
+}
 
 hipError_t launch_group(const GroupArgs &a, hipStream_t s);
 

@@ -33,32 +33,47 @@ struct MmElem<MM_I8> {
 };
 
 // Eight or four consecutive results (16- or 8-byte aligned in the output's type).
-__device__ __forceinline__ uint32_t mm_pack(int out_type, float lo, float hi) {
-  if (out_type == MM_BF16) return pack_bf16x2(lo, hi);
+template <int OUT>
+__device__ __forceinline__ uint32_t mm_pack(float lo, float hi) {
+  if (OUT == MM_BF16) return pack_bf16x2(lo, hi);
   return __builtin_bit_cast(uint32_t, v2h{(_Float16)lo, (_Float16)hi});
 }
 
+template <int OUT>
 __device__ __forceinline__ void mm_store4(const MmArgs &a, long at, const float *v) {
-  if (a.out_type == MM_FP32) {
+  if (OUT == MM_FP32) {
     v4f *o = (v4f *)((float *)a.out + at);
     v4f r = v4f{v[0], v[1], v[2], v[3]};
     if (a.accumulate) r += *o;
     *o = r;
   } else {
     typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-    *(v2u *)((uint16_t *)a.out + at) = v2u{mm_pack(a.out_type, v[0], v[1]), mm_pack(a.out_type, v[2], v[3])};
+    *(v2u *)((uint16_t *)a.out + at) = v2u{mm_pack<OUT>(v[0], v[1]), mm_pack<OUT>(v[2], v[3])};
   }
 }
 
+template <int OUT>
 __device__ __forceinline__ void mm_store8(const MmArgs &a, long at, const float *v) {
-  if (a.out_type == MM_FP32) {
-    mm_store4(a, at, v);
-    mm_store4(a, at + 4, v + 4);
+  if (OUT == MM_FP32) {
+    mm_store4<OUT>(a, at, v);
+    mm_store4<OUT>(a, at + 4, v + 4);
   } else {
     typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-    *(v4u *)((uint16_t *)a.out + at) = v4u{mm_pack(a.out_type, v[0], v[1]), mm_pack(a.out_type, v[2], v[3]),
-                                           mm_pack(a.out_type, v[4], v[5]), mm_pack(a.out_type, v[6], v[7])};
+    *(v4u *)((uint16_t *)a.out + at) = v4u{mm_pack<OUT>(v[0], v[1]), mm_pack<OUT>(v[2], v[3]), mm_pack<OUT>(v[4], v[5]),
+                                           mm_pack<OUT>(v[6], v[7])};
   }
+}
+
+// f(integral constant of the output type): the branch on it stands outside the stores.
+template <int V>
+struct MmConst {
+  static constexpr int value = V;
+};
+template <typename F>
+__device__ __forceinline__ void mm_by_output(int out_type, F f) {
+  if (out_type == MM_FP32) f(MmConst<MM_FP32>{});
+  else if (out_type == MM_BF16) f(MmConst<MM_BF16>{});
+  else f(MmConst<MM_FP16>{});
 }
 
 // ------------------------------------------------------------ tile kernels
@@ -115,6 +130,18 @@ constexpr int kMmGroup = 4;
 template <int BQ>
 __device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile &t) {
   const int lane = threadIdx.x & 63;
+  if (!a.first) {                        // one group: the same order without the scans
+    const int total = (a.R + BQ - 1) / BQ, nt = total * ptiles, chunk = (nt + 7) >> 3;
+    const int id = ((int)blockIdx.x & 7) * chunk + ((int)blockIdx.x >> 3);
+    if (((int)blockIdx.x >> 3) >= chunk || id >= nt) return false;
+    const int grp = id / (kMmGroup * ptiles), rem = id - grp * kMmGroup * ptiles;
+    const int gcur = min(kMmGroup, total - grp * kMmGroup);
+    t.e = 0;
+    t.pt = rem / gcur;
+    t.row0 = (grp * kMmGroup + rem % gcur) * BQ;
+    t.rows = min(BQ, a.R - t.row0);
+    return true;
+  }
   const int per = (a.E + 63) >> 6;
   int cnt = 0;
   for (int i = 0; i < per; i++) {
@@ -362,43 +389,46 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   }
 
   // ---- outputs
+  mm_by_output(a.out_type, [&](auto out) {
+    constexpr int OUT = decltype(out)::value;
 #pragma unroll
-  for (int j = 0; j < NQ; j++) {
-    const int q = wq * TQ + 16 * j + l16;
-    if (q >= qn) continue;
-    const long row = OP == MM_DW ? (long)t.e * a.N + q0 + q : (long)t.row0 + q;
-    float xs = 0.f;
-    if (TYPE == MM_I8) {
-      const long xr = mm_x_row(a, (int)row);
-      xs = xr < 0 ? 0.f : a.x_scales[xr];
-    }
+    for (int j = 0; j < NQ; j++) {
+      const int q = wq * TQ + 16 * j + l16;
+      if (q >= qn) continue;
+      const long row = OP == MM_DW ? (long)t.e * a.N + q0 + q : (long)t.row0 + q;
+      float xs = 0.f;
+      if (TYPE == MM_I8) {
+        const long xr = mm_x_row(a, (int)row);
+        xs = xr < 0 ? 0.f : a.x_scales[xr];
+      }
 #pragma unroll
-    for (int i0 = 0; i0 < NP; i0 += 4) {
-      float v[16];
+      for (int i0 = 0; i0 < NP; i0 += 4) {
+        float v[16];
 #pragma unroll
-      for (int i = 0; i < 4; i++)
+        for (int i = 0; i < 4; i++)
 #pragma unroll
-        for (int k = 0; k < 4; k++) v[4 * i + k] = (float)acc[i0 + i][j][k];
-      const int pc = p0 + wp * TP + 16 * i0;
-      if (!TP_T) {                       // 16 consecutive columns
-        const int p = pc + 16 * g;
-        if (TYPE == MM_I8) {
-          const float *ws = a.w_scales + (size_t)t.e * a.N;
+          for (int k = 0; k < 4; k++) v[4 * i + k] = (float)acc[i0 + i][j][k];
+        const int pc = p0 + wp * TP + 16 * i0;
+        if (!TP_T) {                       // 16 consecutive columns
+          const int p = pc + 16 * g;
+          if (TYPE == MM_I8) {
+            const float *ws = a.w_scales + (size_t)t.e * a.N;
 #pragma unroll
-          for (int k = 0; k < 16; k++) v[k] *= xs * (p + k < pn ? ws[p + k] : 0.f);
-        }
+            for (int k = 0; k < 16; k++) v[k] *= xs * (p + k < pn ? ws[p + k] : 0.f);
+          }
 #pragma unroll
-        for (int k = 0; k < 16; k += 8)
-          if (p + k < pn) mm_store8(a, row * pn + p + k, v + k);
-      } else {                           // four runs of 4 columns, 16 apart
+          for (int k = 0; k < 16; k += 8)
+            if (p + k < pn) mm_store8<OUT>(a, row * pn + p + k, v + k);
+        } else {                           // four runs of 4 columns, 16 apart
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int p = pc + 16 * i + 4 * g;
-          if (p < pn) mm_store4(a, row * pn + p, v + 4 * i);
+          for (int i = 0; i < 4; i++) {
+            const int p = pc + 16 * i + 4 * g;
+            if (p < pn) mm_store4<OUT>(a, row * pn + p, v + 4 * i);
+          }
         }
       }
     }
-  }
+  });
 }
 
 template <int OP, int TYPE, int BQ, int BP, int WQ, int WP, int MINW>
@@ -415,9 +445,142 @@ static hipError_t launch_tile(const MmArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ------------------------------------------------------------ few rows a group
+//
+// Weights streamed once: a block takes up to 16 rows of a group and 16
+// channels, its waves the 128-byte columns of the reduction in turn.  Each wave
+// runs a ring of kStreamSlots columns of its own in LDS, loaded straight from
+// memory in whole 128-byte lines (8 rows a load), so it needs no barrier until
+// the waves' sums meet in wave order.  Loading MFMA operands into registers
+// instead touches 16 rows in every 16 lanes: 33 MB of int8 weights in 13.1 us
+// against 7.7 us this way (4.3 TB/s), 48 experts' bf16 rows (0.79 GB) in 133 us
+// against 129 us (5.8 TB/s).  Four waves of two slots leave four blocks a CU:
+// deeper rings or more waves measured 130 to 154 us and 8.6 to 13 us.
+constexpr int kStreamSlots = 2, kStreamWaves = 4;
+
+// The 16 x 16 MFMA operands of one column: weights at LDS offset pw, rows of x
+// at px, both halves of the reduction.  Read and waited for in one statement,
+// so the loads in flight to the other slots are not waited for.
+__device__ __forceinline__ void stream_read(uint32_t pw0, uint32_t pw1, uint32_t px0, uint32_t px1, v4i *w, v4i *x) {
+  asm volatile(
+      "ds_read_b128 %0, %4\n"
+      "ds_read_b128 %1, %5\n"
+      "ds_read_b128 %2, %6\n"
+      "ds_read_b128 %3, %7\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(w[0]), "=&v"(w[1]), "=&v"(x[0]), "=&v"(x[1])
+      : "v"(pw0), "v"(pw1), "v"(px0), "v"(px1)
+      : "memory");
+}
+
+template <int TYPE, bool GATHER>
+__global__ __launch_bounds__(64 * kStreamWaves) void k_mm_stream(MmArgs a) {
+  typedef MmElem<TYPE> M;
+  typedef typename M::acc Acc;
+  constexpr int ES = sizeof(typename M::t), D = kStreamSlots, NW = kStreamWaves;
+  constexpr int kSlot = 4096;            // 16 weight rows, 16 rows of x
+  constexpr int RS = 16 + 4;             // a row of sums, padded so that rows start on other banks
+  __shared__ __align__(1024) uint8_t ring[NW][D][kSlot];
+  __shared__ Acc sum[NW * 16 * RS / 4];
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  MmTile t;
+  if (!mm_find_tile<16>(a, (a.N + 15) >> 4, t)) return;
+  const int p0 = t.pt * 16, l16 = lane & 15, g = lane >> 4;
+  const uint32_t ld = (uint32_t)a.K * ES;
+  const int units = (int)((ld + 127) >> 7);
+  const Rsrc wb = mm_rsrc((const uint8_t *)a.w + ((size_t)t.e * a.N + p0) * ld, (uint32_t)min(16, a.N - p0) * ld);
+  // loads: row 8 i + lane / 8, its chunk swizzled as in the tile kernels
+  uint32_t vw[2], ck[2];
+  const uint8_t *xp[2];
+  bool live[2];
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const int r = 8 * i + (lane >> 3);
+    ck[i] = (uint32_t)((lane & 7) ^ swz_q(r)) * 16;
+    vw[i] = (uint32_t)r * ld + ck[i];
+    const long xr = r < t.rows ? (GATHER ? mm_x_row(a, t.row0 + r) : (long)t.row0 + r) : -1;
+    live[i] = xr >= 0;
+    xp[i] = (const uint8_t *)a.x + (live[i] ? (size_t)xr * ld : 0) + ck[i];
+  }
+  // this thread's outputs after the join: four channels of one row, and their scales
+  const int oq = threadIdx.x >> 2, op = (threadIdx.x & 3) * 4;
+  const bool writes = oq < t.rows && p0 + op < a.N;
+  float xs = 0.f;
+  v4f ws = {0.f, 0.f, 0.f, 0.f};
+  if (TYPE == MM_I8 && writes) {
+    const long xr = mm_x_row(a, t.row0 + oq);
+    if (xr >= 0) xs = a.x_scales[xr];
+#pragma unroll
+    for (int k = 0; k < 4; k++) ws[k] = a.w_scales[(size_t)t.e * a.N + p0 + op + k];
+  }
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_void *)&ring[w][0][0];
+  const uint32_t rd0 = base + l16 * 128 + ((g ^ swz_q(l16)) * 16), rd1 = base + l16 * 128 + (((4 + g) ^ swz_q(l16)) * 16);
+  Acc acc = {0, 0, 0, 0};
+  const int n = (units - w + NW - 1) / NW;   // columns of this wave
+
+  // XI: loads of eight rows of x a column
+  auto body = [&](auto xi) {
+    constexpr int XI = decltype(xi)::value, CNT = 2 + XI;
+    auto load = [&](int s) {
+      const uint32_t k = (uint32_t)(s * NW + w) * 128;
+      uint8_t *dst = &ring[w][s % D][0];
+#pragma unroll
+      for (int i = 0; i < 2; i++)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wb, (lds_void *)(dst + i * 1024), 16,
+                                                 (int)(k + ck[i] < ld ? vw[i] : kOutside), (int)k, 0, 0);
+#pragma unroll
+      for (int i = 0; i < XI; i++) {
+        const uint8_t *p = live[i] && k + ck[i] < ld ? xp[i] + k : (const uint8_t *)g_mm_zeros;
+        __builtin_amdgcn_global_load_lds(p, (lds_void *)(dst + 2048 + i * 1024), 16, 0, 0);
+      }
+    };
+    for (int s = 0; s < min(n, D - 1); s++) load(s);
+    for (int s = 0; s < n; s++) {
+      if (s + D - 1 < n) {
+        load(s + D - 1);                 // into the slot read in the step before
+        wait_vm<(D - 1) * CNT>();
+      } else {
+        wait_vm<0>();
+      }
+      const uint32_t o = (uint32_t)(s % D) * kSlot;
+      v4i fw[2], fx[2];
+      stream_read(rd0 + o, rd1 + o, rd0 + o + 2048, rd1 + o + 2048, fw, fx);
+      acc = M::mma(fw[0], fx[0], acc);
+      acc = M::mma(fw[1], fx[1], acc);
+    }
+  };
+  // rows past XI * 8 of x are not loaded: their MFMA columns hold what LDS held and are not stored
+  if (t.rows <= 8) body(MmConst<1>{});
+  else body(MmConst<2>{});
+  // sums of the waves: [wave][row][channel]
+  sum[((w * 16 + l16) * RS + 4 * g) >> 2] = acc;
+  __syncthreads();
+  mm_by_output(a.out_type, [&](auto out) {
+    constexpr int OUT = decltype(out)::value;
+    if (!writes) return;
+    Acc r = sum[(oq * RS + op) >> 2];
+#pragma unroll
+    for (int v = 1; v < NW; v++) r += sum[((v * 16 + oq) * RS + op) >> 2];
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) v[k] = TYPE == MM_I8 ? (float)r[k] * (xs * ws[k]) : (float)r[k];
+    mm_store4<OUT>(a, (long)(t.row0 + oq) * a.N + p0 + op, v);
+  });
+}
+
+template <int TYPE>
+static hipError_t launch_stream(const MmArgs &a, hipStream_t s) {
+  const long tiles = (a.R + 15) / 16 + (a.first ? (a.E < a.R ? a.E : a.R) : 0);
+  const long blocks = (tiles * ((a.N + 15) / 16) + 7) / 8 * 8;
+  if (a.rows) hipLaunchKernelGGL((k_mm_stream<TYPE, true>), dim3((unsigned)blocks), dim3(64 * kStreamWaves), 0, s, a);
+  else hipLaunchKernelGGL((k_mm_stream<TYPE, false>), dim3((unsigned)blocks), dim3(64 * kStreamWaves), 0, s, a);
+  return hipGetLastError();
+}
+
 template <int TYPE>
 static hipError_t launch_forward(const MmArgs &a, hipStream_t s) {
   const long avg = a.R / a.E;
+  if (a.R <= 8l * a.E || a.R <= 16) return launch_stream<TYPE>(a, s);
   if (avg >= 160) return launch_tile<MM_FORWARD, TYPE, 256, 256, 2, 4, 2>(a, s);
   if (avg >= 96) return launch_tile<MM_FORWARD, TYPE, 128, 256, 2, 4, 2>(a, s);
   return launch_tile<MM_FORWARD, TYPE, 64, 256, 1, 4, 2>(a, s);

@@ -168,8 +168,8 @@ int moe_int8_mm(const int8_t *x, const float *x_scales, const int8_t *w, const f
 
 size_t moe_group_routes_scratch_bytes(int T, int top_k, int E) {
   if (T < 0 || top_k < 1 || E < 1 || (long long)T * top_k > INT32_MAX) return 0;
-  const long long R = (long long)T * top_k, chunks = (R + moe::kGroupChunk - 1) / moe::kGroupChunk;
-  return chunks <= 1 ? 0 : (size_t)(4 * (chunks * E + R));
+  const long R = (long)T * top_k;
+  return R <= 4 * moe::kGroupThreads ? 0 : sizeof(int32_t) * ((size_t)moe::group_blocks(R) * E + R);
 }
 
 int moe_group_routes(const int32_t *topk_ids, int T, int top_k, int E, int32_t *first, int32_t *order, int32_t *token,
@@ -187,9 +187,9 @@ int moe_group_routes(const int32_t *topk_ids, int T, int top_k, int E, int32_t *
   if (scratch_bytes < need) return fail(MOE_ESCRATCH, "%s: scratch holds %zu bytes, %zu needed", fn, scratch_bytes, need);
   moe::GroupArgs a = {};
   a.ids = topk_ids, a.R = T * top_k, a.topk = top_k, a.E = E;
-  a.chunks = (a.R + moe::kGroupChunk - 1) / moe::kGroupChunk;
+  if (need) a.rounds = moe::group_rounds(a.R), a.blocks = moe::group_blocks(a.R);
   a.first = first, a.order = order, a.token = token, a.inverse = inverse;
-  a.hist = (int32_t *)scratch, a.rank = (int32_t *)scratch + (size_t)a.chunks * E;
+  a.hist = (int32_t *)scratch, a.rank = (int32_t *)scratch + (size_t)a.blocks * E;
   return launched(moe::launch_group(a, (hipStream_t)stream), fn);
 }
 
