@@ -341,16 +341,32 @@ def ep_remap(topk_ids, topk_weights, offset: int, num_local: int, out_ids=None, 
     return out_ids, out_weights
 
 
-_T_CODES = None
+class _Runtime:
+    """What the products' calls look up every time, gathered at the first one: a call on a few rows
+    costs little more than its launch, so attribute chains count (10.1 -> 9.1 us a call)."""
 
-
-def _codes():
-    """torch dtype -> moe_dtype of the types the products take."""
-    global _T_CODES
-    if _T_CODES is None:
+    def __init__(self):
         import torch
-        _T_CODES = {torch.bfloat16: T_BF16, torch.float16: T_FP16, torch.float32: T_FP32}
-    return _T_CODES
+        self.torch, self.lib = torch, _lib.load()
+        self.empty = torch.empty
+        self.current_device = torch.cuda.current_device
+        # the stream's handle: building a Stream object takes longer than the launch
+        self.current_stream = torch._C._cuda_getCurrentRawStream
+        self.codes = {torch.bfloat16: T_BF16, torch.float16: T_FP16, torch.float32: T_FP32}
+        self.any_float = tuple(self.codes)
+        self.half = (torch.bfloat16, torch.float16)
+        self.outs = {t: (t, torch.float32) for t in self.half}
+        self.i8, self.i32, self.f32 = (torch.int8,), (torch.int32,), (torch.float32,)
+
+
+_runtime = None
+
+
+def _rt():
+    global _runtime
+    if _runtime is None:
+        _runtime = _Runtime()
+    return _runtime
 
 
 def _operands(named):
@@ -367,46 +383,43 @@ def _operands(named):
     for name, t, _, _ in named:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise ValueError(f"{name} must be a device tensor")
-        if t.get_device() != dev:
+        if d != dev:
             raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {named[0][1].device}")
     return dev
 
 
 def _use(stream, t):
     """Makes `stream` current for a call on operand t, so that the tensors made there belong to it too."""
-    import torch
     if t is not None and t.device.type == "cuda" and stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, the operands on {t.device}")
-    return torch.cuda.stream(stream)
+    return _rt().torch.cuda.stream(stream)
 
 
-def _launch(dev, fn, *args):
-    """fn(*args, stream) on device dev and its current stream (by its handle: building a Stream
-    object takes longer than the launch)."""
-    import torch
-    if dev == torch.cuda.current_device():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+def _launch(rt, dev, fn, *args):
+    """fn(*args, stream) on device dev and its current stream."""
+    if dev == rt.current_device():
+        rc = fn(*args, rt.current_stream(dev))
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+        with rt.torch.cuda.device(dev):
+            rc = fn(*args, rt.current_stream(dev))
     if rc != MOE_OK:
         _check(rc)
 
 
-def _mm_scratch(op, E, R, N, K, scratch, like):
+def _mm_scratch(rt, op, E, R, N, K, scratch, like):
     """(pointer, bytes, tensor) of a product's scratch: the caller's tensor, or one made here when it needs any."""
-    import torch
     if scratch is not None:
-        _need(scratch, "scratch", torch.uint8)
+        _need(scratch, "scratch", rt.torch.uint8)
         if scratch.device != like.device:
             raise ValueError(f"scratch is on {scratch.device}, the operands on {like.device}")
         return scratch.data_ptr(), scratch.numel(), scratch
-    need = _lib.load().moe_mm_scratch_bytes(op, E, R, N, K)
+    need = rt.lib.moe_mm_scratch_bytes(op, E, R, N, K)
     if not need:
         return None, 0, None
-    scratch = torch.empty(need, dtype=torch.uint8, device=like.device)
+    scratch = rt.empty(need, dtype=rt.torch.uint8, device=like.device)
     return scratch.data_ptr(), need, scratch
 
 
@@ -434,6 +447,13 @@ def _dims(t, name, dim):
     return t.shape
 
 
+def _half(rt, t, name):
+    """Types an output may have beside the bf16 or fp16 operand t."""
+    if t.dtype not in rt.half:
+        raise TypeError(f"{name}: expected {' or '.join(map(str, rt.half))}, got {t.dtype}")
+    return rt.outs[t.dtype]
+
+
 def grouped_mm(x, w, first, rows=None, out=None, out_dtype=None, scratch=None, stream=None):
     """Products over ragged groups (moe_grouped_mm): out[r] = x[row(r)] @ w[e].T for the rows r of
     group e, first[e] <= r < first[e + 1].
@@ -441,24 +461,25 @@ def grouped_mm(x, w, first, rows=None, out=None, out_dtype=None, scratch=None, s
     x [T, K] and w [E, N, K] bf16 or fp16, first int32 [E + 1]; rows int32 [R] names the row of x
     behind each product row (None: R = T, row r itself; a number outside [0, T): a row of zeros).
     out [R, N] in x's type or fp32; rows in no group keep what out held (unset in a new tensor)."""
-    import torch
     if stream is not None:
         with _use(stream, x):
             return grouped_mm(x, w, first, rows, out, out_dtype, scratch)
+    rt = _rt()
     T, K = _dims(x, "x", 2)
     E, N, _ = _dims(w, "w", 3)
-    R = T if rows is None else _dims(rows, "rows", 1)[0]
-    kinds = (torch.bfloat16, torch.float16)
-    named = [("x", x, kinds, x.shape), ("w", w, (x.dtype,), (E, N, K)), ("first", first, (torch.int32,), (E + 1,))]
+    outs = _half(rt, x, "x")
+    named = [("x", x, outs, x.shape), ("w", w, (x.dtype,), (E, N, K)), ("first", first, rt.i32, (E + 1,))]
+    R = T
     if rows is not None:
-        named.append(("rows", rows, (torch.int32,), (R,)))
-    dt = _out_dtype(out, out_dtype, x.dtype, (x.dtype, torch.float32), (R, N), named)
+        R, = _dims(rows, "rows", 1)
+        named.append(("rows", rows, rt.i32, (R,)))
+    dt = _out_dtype(out, out_dtype, x.dtype, outs, (R, N), named)
     dev = _operands(named)
     if out is None:
-        out = torch.empty((R, N), dtype=dt, device=x.device)
-    sp, sb, keep = _mm_scratch(MM_FORWARD, E, R, N, K, scratch, x)
-    _launch(dev, _lib.load().moe_grouped_mm, _codes()[x.dtype], x.data_ptr(), T, _ptr(rows), w.data_ptr(),
-            first.data_ptr(), E, R, N, K, _codes()[dt], out.data_ptr(), sp, sb)
+        out = rt.empty((R, N), dtype=dt, device=x.device)
+    sp, sb, keep = _mm_scratch(rt, MM_FORWARD, E, R, N, K, scratch, x)
+    _launch(rt, dev, rt.lib.moe_grouped_mm, rt.codes[x.dtype], x.data_ptr(), T, None if rows is None else rows.data_ptr(),
+            w.data_ptr(), first.data_ptr(), E, R, N, K, rt.codes[dt], out.data_ptr(), sp, sb)
     return out
 
 
@@ -467,21 +488,21 @@ def grouped_mm_dx(dy, w, first, out=None, out_dtype=None, scratch=None, stream=N
 
     dy [R, N], w [E, N, K] bf16 or fp16; out [R, K] in dy's type or fp32. With `rows` in the forward
     product, a token's gradient is the sum of dx over its rows (group_routes' inverse lists them)."""
-    import torch
     if stream is not None:
         with _use(stream, dy):
             return grouped_mm_dx(dy, w, first, out, out_dtype, scratch)
+    rt = _rt()
     R, N = _dims(dy, "dy", 2)
     E, _, K = _dims(w, "w", 3)
-    kinds = (torch.bfloat16, torch.float16)
-    named = [("dy", dy, kinds, dy.shape), ("w", w, (dy.dtype,), (E, N, K)), ("first", first, (torch.int32,), (E + 1,))]
-    dt = _out_dtype(out, out_dtype, dy.dtype, (dy.dtype, torch.float32), (R, K), named)
+    outs = _half(rt, dy, "dy")
+    named = [("dy", dy, outs, dy.shape), ("w", w, (dy.dtype,), (E, N, K)), ("first", first, rt.i32, (E + 1,))]
+    dt = _out_dtype(out, out_dtype, dy.dtype, outs, (R, K), named)
     dev = _operands(named)
     if out is None:
-        out = torch.empty((R, K), dtype=dt, device=dy.device)
-    sp, sb, keep = _mm_scratch(MM_DX, E, R, N, K, scratch, dy)
-    _launch(dev, _lib.load().moe_grouped_mm_dx, _codes()[dy.dtype], dy.data_ptr(), w.data_ptr(),
-            first.data_ptr(), E, R, N, K, _codes()[dt], out.data_ptr(), sp, sb)
+        out = rt.empty((R, K), dtype=dt, device=dy.device)
+    sp, sb, keep = _mm_scratch(rt, MM_DX, E, R, N, K, scratch, dy)
+    _launch(rt, dev, rt.lib.moe_grouped_mm_dx, rt.codes[dy.dtype], dy.data_ptr(), w.data_ptr(), first.data_ptr(), E, R, N,
+            K, rt.codes[dt], out.data_ptr(), sp, sb)
     return out
 
 
@@ -492,10 +513,10 @@ def grouped_mm_dw(dy, x, first, rows=None, out=None, out_dtype=None, accumulate:
 
     dy [R, N], x [T, K] bf16 or fp16, rows as in grouped_mm; out [E, N, K] in dy's type or fp32.
     accumulate adds to out (fp32, required then)."""
-    import torch
     if stream is not None:
         with _use(stream, dy):
             return grouped_mm_dw(dy, x, first, rows, out, out_dtype, accumulate, scratch)
+    rt = _rt()
     R, N = _dims(dy, "dy", 2)
     T, K = _dims(x, "x", 2)
     E = _dims(first, "first", 1)[0] - 1
@@ -503,40 +524,41 @@ def grouped_mm_dw(dy, x, first, rows=None, out=None, out_dtype=None, accumulate:
         raise ValueError(f"x: expected {R} rows as dy, got {T}")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    kinds = (torch.bfloat16, torch.float16)
-    named = [("dy", dy, kinds, dy.shape), ("x", x, (dy.dtype,), x.shape), ("first", first, (torch.int32,), (E + 1,))]
+    outs = _half(rt, dy, "dy")
+    named = [("dy", dy, outs, dy.shape), ("x", x, (dy.dtype,), x.shape), ("first", first, rt.i32, (E + 1,))]
     if rows is not None:
-        named.append(("rows", rows, (torch.int32,), (R,)))
-    dt = _out_dtype(out, out_dtype, dy.dtype, (dy.dtype, torch.float32), (E, N, K), named)
+        named.append(("rows", rows, rt.i32, (R,)))
+    dt = _out_dtype(out, out_dtype, dy.dtype, outs, (E, N, K), named)
     dev = _operands(named)
     if out is None:
-        out = torch.empty((E, N, K), dtype=dt, device=dy.device)
-    sp, sb, keep = _mm_scratch(MM_DW, E, R, N, K, scratch, dy)
-    _launch(dev, _lib.load().moe_grouped_mm_dw, _codes()[dy.dtype], dy.data_ptr(), x.data_ptr(), T, _ptr(rows),
-            first.data_ptr(), E, R, N, K, _codes()[dt], int(bool(accumulate)), out.data_ptr(), sp, sb)
+        out = rt.empty((E, N, K), dtype=dt, device=dy.device)
+    sp, sb, keep = _mm_scratch(rt, MM_DW, E, R, N, K, scratch, dy)
+    _launch(rt, dev, rt.lib.moe_grouped_mm_dw, rt.codes[dy.dtype], dy.data_ptr(), x.data_ptr(), T,
+            None if rows is None else rows.data_ptr(), first.data_ptr(), E, R, N, K, rt.codes[dt], int(bool(accumulate)),
+            out.data_ptr(), sp, sb)
     return out
 
 
 def quant_int8(x, out=None, scales=None, stream=None):
     """Rows of a bf16 or fp16 [rows, cols] tensor to 8-bit integers with one fp32 scale a row
     (moe_quant_int8): (codes int8 [rows, cols], scales [rows])."""
-    import torch
     if stream is not None:
         with _use(stream, x):
             return quant_int8(x, out, scales)
+    rt = _rt()
     shape = _dims(x, "x", 2)
-    named = [("x", x, (torch.bfloat16, torch.float16), shape)]
+    named = [("x", x, rt.half, shape)]
     if out is not None:
-        named.append(("out", out, (torch.int8,), shape))
+        named.append(("out", out, rt.i8, shape))
     if scales is not None:
-        named.append(("scales", scales, (torch.float32,), shape[:1]))
+        named.append(("scales", scales, rt.f32, shape[:1]))
     dev = _operands(named)
     if out is None:
-        out = torch.empty(shape, dtype=torch.int8, device=x.device)
+        out = rt.empty(shape, dtype=rt.torch.int8, device=x.device)
     if scales is None:
-        scales = torch.empty(shape[0], dtype=torch.float32, device=x.device)
-    _launch(dev, _lib.load().moe_quant_int8, _codes()[x.dtype], x.data_ptr(), shape[0], shape[1],
-            out.data_ptr(), scales.data_ptr())
+        scales = rt.empty(shape[:1], dtype=rt.torch.float32, device=x.device)
+    _launch(rt, dev, rt.lib.moe_quant_int8, rt.codes[x.dtype], x.data_ptr(), shape[0], shape[1], out.data_ptr(),
+            scales.data_ptr())
     return out, scales
 
 
@@ -546,46 +568,47 @@ def int8_mm(x, x_scales, w, w_scales, out=None, out_dtype=None, scratch=None, st
 
     x int8 [M, K], x_scales fp32 [M], w int8 [N, K], w_scales fp32 [N]; out [M, N] bf16 (default),
     fp16 or fp32."""
-    import torch
     if stream is not None:
         with _use(stream, x):
             return int8_mm(x, x_scales, w, w_scales, out, out_dtype, scratch)
+    rt = _rt()
     M, K = _dims(x, "x", 2)
     N, _ = _dims(w, "w", 2)
-    named = [("x", x, (torch.int8,), x.shape), ("x_scales", x_scales, (torch.float32,), (M,)),
-             ("w", w, (torch.int8,), (N, K)), ("w_scales", w_scales, (torch.float32,), (N,))]
-    dt = _out_dtype(out, out_dtype, torch.bfloat16, tuple(_codes()), (M, N), named)
+    named = [("x", x, rt.i8, x.shape), ("x_scales", x_scales, rt.f32, (M,)), ("w", w, rt.i8, (N, K)),
+             ("w_scales", w_scales, rt.f32, (N,))]
+    dt = _out_dtype(out, out_dtype, rt.torch.bfloat16, rt.any_float, (M, N), named)
     dev = _operands(named)
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=x.device)
-    sp, sb, keep = _mm_scratch(MM_INT8, 1, M, N, K, scratch, x)
-    _launch(dev, _lib.load().moe_int8_mm, x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
-            M, N, K, _codes()[dt], out.data_ptr(), sp, sb)
+        out = rt.empty((M, N), dtype=dt, device=x.device)
+    sp, sb, keep = _mm_scratch(rt, MM_INT8, 1, M, N, K, scratch, x)
+    _launch(rt, dev, rt.lib.moe_int8_mm, x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), M, N, K,
+            rt.codes[dt], out.data_ptr(), sp, sb)
     return out
 
 
 def grouped_int8_mm(x, x_scales, w, w_scales, first, rows=None, out=None, out_dtype=None, scratch=None, stream=None):
     """int8_mm over ragged groups (moe_grouped_int8_mm): w int8 [E, N, K], w_scales fp32 [E, N], first and
     rows as in grouped_mm; x_scales belongs to the rows of x. out [R, N] bf16 (default), fp16 or fp32."""
-    import torch
     if stream is not None:
         with _use(stream, x):
             return grouped_int8_mm(x, x_scales, w, w_scales, first, rows, out, out_dtype, scratch)
+    rt = _rt()
     T, K = _dims(x, "x", 2)
     E, N, _ = _dims(w, "w", 3)
-    R = T if rows is None else _dims(rows, "rows", 1)[0]
-    named = [("x", x, (torch.int8,), x.shape), ("x_scales", x_scales, (torch.float32,), (T,)),
-             ("w", w, (torch.int8,), (E, N, K)), ("w_scales", w_scales, (torch.float32,), (E, N)),
-             ("first", first, (torch.int32,), (E + 1,))]
+    named = [("x", x, rt.i8, x.shape), ("x_scales", x_scales, rt.f32, (T,)), ("w", w, rt.i8, (E, N, K)),
+             ("w_scales", w_scales, rt.f32, (E, N)), ("first", first, rt.i32, (E + 1,))]
+    R = T
     if rows is not None:
-        named.append(("rows", rows, (torch.int32,), (R,)))
-    dt = _out_dtype(out, out_dtype, torch.bfloat16, tuple(_codes()), (R, N), named)
+        R, = _dims(rows, "rows", 1)
+        named.append(("rows", rows, rt.i32, (R,)))
+    dt = _out_dtype(out, out_dtype, rt.torch.bfloat16, rt.any_float, (R, N), named)
     dev = _operands(named)
     if out is None:
-        out = torch.empty((R, N), dtype=dt, device=x.device)
-    sp, sb, keep = _mm_scratch(MM_INT8, E, R, N, K, scratch, x)
-    _launch(dev, _lib.load().moe_grouped_int8_mm, x.data_ptr(), x_scales.data_ptr(), T, _ptr(rows), w.data_ptr(),
-            w_scales.data_ptr(), first.data_ptr(), E, R, N, K, _codes()[dt], out.data_ptr(), sp, sb)
+        out = rt.empty((R, N), dtype=dt, device=x.device)
+    sp, sb, keep = _mm_scratch(rt, MM_INT8, E, R, N, K, scratch, x)
+    _launch(rt, dev, rt.lib.moe_grouped_int8_mm, x.data_ptr(), x_scales.data_ptr(), T,
+            None if rows is None else rows.data_ptr(), w.data_ptr(), w_scales.data_ptr(), first.data_ptr(), E, R, N, K,
+            rt.codes[dt], out.data_ptr(), sp, sb)
     return out
 
 
@@ -594,27 +617,31 @@ def group_routes(topk_ids, num_experts: int, scratch=None, stream=None):
 
     topk_ids int32 [T, k]; ids outside [0, num_experts) belong to no group. Returns int32 device tensors
     (first [E + 1], order [T * k], token [T * k], inverse [T, k]): the groups' offsets, the route and
-    the token behind each sorted row (-1 past first[E]), and the sorted row of each route (or -1)."""
-    import torch
+    the token behind each sorted row (-1 past first[E]), and the sorted row of each route (or -1). They
+    share one allocation."""
     if stream is not None:
         with _use(stream, topk_ids):
             return group_routes(topk_ids, num_experts, scratch)
-    T, k = _dims(topk_ids, "topk_ids", 2)
-    dev = _operands([("topk_ids", topk_ids, (torch.int32,), topk_ids.shape)])
-    E = int(num_experts)
-    L = _lib.load()
-    first = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=topk_ids.device)
-    order, token, inverse = torch.empty((3, T * k), dtype=torch.int32, device=topk_ids.device).unbind(0)
-    need = L.moe_group_routes_scratch_bytes(T, k, E)
-    if scratch is None:
-        scratch = torch.empty(need, dtype=torch.uint8, device=topk_ids.device) if need else None
-    else:
-        _need(scratch, "scratch", torch.uint8)
+    rt = _rt()
+    T, k = shape = _dims(topk_ids, "topk_ids", 2)
+    dev = _operands([("topk_ids", topk_ids, rt.i32, shape)])
+    E, R = int(num_experts), T * k
+    if E < 1:
+        raise ValueError(f"num_experts must be positive, got {E}")
+    first, order, token, inverse = rt.empty(E + 1 + 3 * R, dtype=rt.torch.int32, device=topk_ids.device).split(
+        [E + 1, R, R, R])
+    need = rt.lib.moe_group_routes_scratch_bytes(T, k, E)
+    if scratch is not None:
+        _need(scratch, "scratch", rt.torch.uint8)
         if scratch.device != topk_ids.device:
             raise ValueError(f"scratch is on {scratch.device}, the operands on {topk_ids.device}")
-    _launch(dev, L.moe_group_routes, topk_ids.data_ptr(), T, k, E, first.data_ptr(), order.data_ptr(),
-            token.data_ptr(), inverse.data_ptr(), _ptr(scratch), 0 if scratch is None else scratch.numel())
-    return first, order, token, inverse.view(T, k)
+    elif need:
+        scratch = rt.empty(need, dtype=rt.torch.uint8, device=topk_ids.device)
+    p = first.data_ptr()
+    _launch(rt, dev, rt.lib.moe_group_routes, topk_ids.data_ptr(), T, k, E, p, p + 4 * (E + 1), p + 4 * (E + 1 + R),
+            p + 4 * (E + 1 + 2 * R), None if scratch is None else scratch.data_ptr(),
+            0 if scratch is None else scratch.numel())
+    return first, order, token, inverse.view(shape)
 
 
 def debug_route(plan: Plan, tiers: Sequence, topk_ids, scratch=None, stream=None):

@@ -173,6 +173,30 @@ __device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile
   return t.rows > 0;
 }
 
+// Exchanges, among the four lanes l, l + 16, l + 32, l + 48, element 4 i + k of
+// lane group g with element 4 g + k of lane group i: two rounds of row swaps.
+__device__ __forceinline__ void swap_columns(float *v) {
+  typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) r[i] = __float_as_uint(v[4 * i + k]);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {        // upper half of element i with the lower half of i + 2
+      const v2u t = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane32_swap(r[i], r[i + 2], false, false));
+      r[i] = t[0], r[i + 2] = t[1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {     // odd rows of 16 of element i with the even ones of i + 1
+      const v2u t = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane16_swap(r[i], r[i + 1], false, false));
+      r[i] = t[0], r[i + 1] = t[1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[4 * i + k] = __uint_as_float(r[i]);
+  }
+}
+
 // Row of x behind product row r, or -1.
 __device__ __forceinline__ long mm_x_row(const MmArgs &a, int r) {
   if (!a.rows) return r;
@@ -203,10 +227,11 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   constexpr int TQ = BQ / WQ, TP = BP / WP, NQ = TQ / 16, NP = TP / 16;
   constexpr int CQ = BQ / 8 / NW, CP = BP / 8 / NW;             // loads of 1 KB a wave and step
   constexpr int kStage = (BQ + BP) * 128;
+  constexpr bool HALF = OP == MM_DW;
   static_assert(TP % 64 == 0 && TQ % 16 == 0 && CQ >= 1 && CP >= 1, "tile shape");
   static_assert(!TQ_T || (BQ % 128 == 0 && TQ % 64 == 0), "transposed Q");
   static_assert(!TP_T || BP % 128 == 0, "transposed P");
-  __shared__ __align__(1024) uint8_t lds[2 * kStage];
+  __shared__ __align__(1024) uint8_t lds[kStage];
 
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const int pn = OP == MM_FORWARD ? a.N : a.K;                  // output columns
@@ -235,93 +260,91 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   const int p0 = t.pt * BP;
   constexpr int ZS = (TQ_T || TP_T) ? 64 : 128 / ES;            // reduction elements a step
   const int steps = (zn + ZS - 1) / ZS;
-  const int tail = (zn - (steps - 1) * ZS) * ES;                // bytes of the last step (contiguous operands)
 
   // ---- loads of one step
   const uint8_t *x = (const uint8_t *)a.x, *dy = (const uint8_t *)a.dy;
   const uint8_t *wt = (const uint8_t *)a.w + (size_t)t.e * a.N * a.K * ES;
   const uint32_t ldx = (uint32_t)a.K * ES, ldy = (uint32_t)a.N * ES;
 
-  uint32_t vq[CQ], vp[CP];
-  int cq[CQ], cp[CP];                    // chunk's byte within the step (contiguous operands)
-  const uint8_t *gx[GATHER && OP == MM_FORWARD ? CQ : 1];
-  int ginc[GATHER && OP == MM_FORWARD ? CQ : 1], gidx[GATHER && OP == MM_DW ? CP : 1];
-#pragma unroll
-  for (int i = 0; i < CQ; i++) {
-    if (!TQ_T) {
-      const int r = (i * NW + w) * 8 + (lane >> 3);
-      cq[i] = ((lane & 7) ^ swz_q(r)) * 16;
-      vq[i] = (uint32_t)r * (OP == MM_FORWARD ? ldx : ldy) + cq[i];
-      if constexpr (GATHER && OP == MM_FORWARD) {
-        const long xr = r < qn ? mm_x_row(a, t.row0 + r) : -1;
-        gx[i] = xr < 0 ? (const uint8_t *)g_mm_zeros : x + xr * ldx + cq[i];
-        ginc[i] = xr < 0 ? 0 : 128;
-      }
-    } else {
-      constexpr int LR = BQ / 8;         // lanes a row
-      const int z = (i * NW + w) * (64 / LR) + lane / LR;
-      vq[i] = (uint32_t)z * ldy + (uint32_t)(q0 * 2 + (((lane % LR) ^ (2 * (z & 7))) * 16));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < CP; i++) {
-    if (!TP_T) {
-      const int r = (i * NW + w) * 8 + (lane >> 3);
-      cp[i] = ((lane & 7) ^ swz_p(r)) * 16;
-      vp[i] = (uint32_t)r * ldx + cp[i];
-    } else {
-      constexpr int LR = BP / 8;
-      const int z = (i * NW + w) * (64 / LR) + lane / LR;
-      const uint32_t col = (uint32_t)(p0 * 2 + (((lane % LR) ^ (2 * (z & 7))) * 16));
-      vp[i] = (uint32_t)z * ldx + col;
-      cp[i] = (int)col;
-    }
-  }
+  // A wave's loads of an operand are the same lanes of rows a fixed step apart,
+  // so one offset a lane does for all of them.  Contiguous operands: load i holds
+  // rows (i NW + w) 8 + lane / 8; transposed ones, LR lanes a row: rows
+  // (i NW + w) 64 / LR + lane / LR.
+  constexpr int LRQ = BQ / 8, LRP = BP / 8;
+  constexpr int DQ = TQ_T ? NW * 64 / LRQ : NW * 8, DP = TP_T ? NW * 64 / LRP : NW * 8;   // rows between loads
+  static_assert(TQ_T ? DQ % 8 == 0 : DQ % 16 == 0, "the swizzle repeats over a wave's loads of Q");
+  static_assert(TP_T ? DP % 8 == 0 : DP % 32 == 0, "... and of P, but for bit 5 (below)");
+  const int rq0 = TQ_T ? w * (64 / LRQ) + lane / LRQ : w * 8 + (lane >> 3);
+  const int rp0 = TP_T ? w * (64 / LRP) + lane / LRP : w * 8 + (lane >> 3);
+  // contiguous: the chunk's byte in the step; transposed: its byte in the row
+  const uint32_t cq = TQ_T ? q0 * 2 + (((lane % LRQ) ^ (2 * (rq0 & 7))) * 16) : ((lane & 7) ^ swz_q(rq0)) * 16;
+  const uint32_t cp = TP_T ? p0 * 2 + (((lane % LRP) ^ (2 * (rp0 & 7))) * 16) : ((lane & 7) ^ swz_p(rp0)) * 16;
+  const uint32_t ldq = OP == MM_FORWARD ? ldx : ldy;
+  const uint32_t vq = (uint32_t)rq0 * ldq + cq, vp = (uint32_t)rp0 * ldx + cp;
   const Rsrc rq = OP == MM_FORWARD  ? mm_rsrc(x + (GATHER ? 0 : (size_t)t.row0 * ldx), (uint32_t)qn * ldx)
                   : OP == MM_DX     ? mm_rsrc(dy + (size_t)t.row0 * ldy, (uint32_t)qn * ldy)
                                     : mm_rsrc(dy, 0);
   const Rsrc rp = OP == MM_FORWARD ? mm_rsrc(wt + (size_t)p0 * ldx, (uint32_t)min(BP, pn - p0) * ldx) : mm_rsrc(wt, 0);
-
-  auto gather_rows = [&](int s) {        // weight gradient: rows of x behind the rows of step s
-    if constexpr (GATHER && OP == MM_DW) {
+  // forward gather: each load's row of x
+  constexpr bool GF = GATHER && OP == MM_FORWARD, GW = GATHER && OP == MM_DW;
+  const uint8_t *gx[GF ? CQ : 1];
+  bool glive[GF ? CQ : 1];
+  if constexpr (GF) {
+#pragma unroll
+    for (int i = 0; i < CQ; i++) {
+      const int r = rq0 + i * DQ;
+      const long xr = r < qn ? mm_x_row(a, t.row0 + r) : -1;
+      glive[i] = xr >= 0;
+      gx[i] = glive[i] ? x + xr * ldx + cq : (const uint8_t *)g_mm_zeros;
+    }
+  }
+  // weight gradient gather: rows of x behind this lane's rows of step s, read one
+  // step before they are loaded
+  int gidx[GW ? CP : 1];
+  const bool gcol = cp < ldx;                       // columns past the row's end are not stored
+  auto gather_rows = [&](int s) {
+    if constexpr (GW) {
 #pragma unroll
       for (int i = 0; i < CP; i++) {
-        const int z = s * 64 + (i * NW + w) * (64 / (BP / 8)) + lane / (BP / 8);
+        const int z = s * ZS + rp0 + i * DP;
         gidx[i] = z < zn ? a.rows[t.row0 + z] : -1;
       }
     }
   };
-  auto load = [&](int s, int buf) {
-    uint8_t *lq = lds + buf * kStage, *lp = lq + BQ * 128;
-    const bool last = s == steps - 1;
+  auto load = [&](int s) {
+    uint8_t *lq = lds + w * 1024, *lp = lq + BQ * 128;
+    const int left = zn * ES - s * 128;             // contiguous operands: bytes from this step on
     // reduction rows left for transposed operands: rows past them load zeros
     const uint32_t zleft = (uint32_t)min(ZS, zn - s * ZS);
-    const Rsrc sq = TQ_T ? mm_rsrc(dy + (size_t)(t.row0 + s * 64) * ldy, zleft * ldy) : rq;
-    const Rsrc sp = OP == MM_DX   ? mm_rsrc(wt + (size_t)(s * 64) * ldx, zleft * ldx)
-                    : OP == MM_DW ? mm_rsrc(x + (size_t)(t.row0 + s * 64) * ldx, zleft * ldx)
+    const Rsrc sq = TQ_T ? mm_rsrc(dy + (size_t)(t.row0 + s * ZS) * ldy, zleft * ldy) : rq;
+    const Rsrc sp = OP == MM_DX   ? mm_rsrc(wt + (size_t)(s * ZS) * ldx, zleft * ldx)
+                    : OP == MM_DW ? mm_rsrc(x + (size_t)(t.row0 + s * ZS) * ldx, zleft * ldx)
                                   : rp;
 #pragma unroll
     for (int i = 0; i < CQ; i++) {
-      lds_void *dst = (lds_void *)(lq + (i * NW + w) * 1024);
-      if constexpr (GATHER && OP == MM_FORWARD) {
-        const uint8_t *g = last && cq[i] >= tail ? (const uint8_t *)g_mm_zeros : gx[i];
-        __builtin_amdgcn_global_load_lds(g, dst, 16, 0, 0);
-        gx[i] += ginc[i];
+      lds_void *dst = (lds_void *)(lq + i * NW * 1024);
+      if constexpr (GF) {
+        const uint8_t *g = gx[i] + (glive[i] ? s * 128 : 0);
+        __builtin_amdgcn_global_load_lds((int)cq < left ? g : (const uint8_t *)g_mm_zeros, dst, 16, 0, 0);
       } else {
-        const uint32_t v = !TQ_T && last && cq[i] >= tail ? kOutside : vq[i];
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(sq, dst, 16, (int)v, TQ_T ? 0 : s * 128, 0, 0);
+        const uint32_t v = vq + (uint32_t)(i * DQ) * ldq;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(sq, dst, 16, (int)(TQ_T || (int)cq < left ? v : kOutside),
+                                                 TQ_T ? 0 : s * 128, 0, 0);
       }
     }
 #pragma unroll
     for (int i = 0; i < CP; i++) {
-      lds_void *dst = (lds_void *)(lp + (i * NW + w) * 1024);
-      if constexpr (GATHER && OP == MM_DW) {
-        const bool ok = gidx[i] >= 0 && gidx[i] < a.x_rows && (uint32_t)cp[i] < ldx;
-        const uint8_t *g = ok ? x + (size_t)gidx[i] * ldx + cp[i] : (const uint8_t *)g_mm_zeros;
+      lds_void *dst = (lds_void *)(lp + i * NW * 1024);
+      if constexpr (GW) {
+        const bool ok = gcol && gidx[i] >= 0 && gidx[i] < a.x_rows;
+        const uint8_t *g = ok ? x + ((size_t)(uint32_t)gidx[i] * ldx + cp) : (const uint8_t *)g_mm_zeros;
         __builtin_amdgcn_global_load_lds(g, dst, 16, 0, 0);
       } else {
-        const uint32_t v = !TP_T && last && cp[i] >= tail ? kOutside : vp[i];
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(sp, dst, 16, (int)v, TP_T ? 0 : s * 128, 0, 0);
+        // rows 32 further have bit 5 of their number, so bit 2 of their swizzle, flipped
+        const uint32_t flip = !TP_T && DP == 32 && (i & 1) ? 64 : 0, c = cp ^ flip;
+        const uint32_t v = vp - cp + c + (uint32_t)(i * DP) * ldx;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(sp, dst, 16, (int)(TP_T || (int)c < left ? v : kOutside),
+                                                 TP_T ? 0 : s * 128, 0, 0);
       }
     }
   };
@@ -357,74 +380,100 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
 #pragma unroll
     for (int j = 0; j < NQ; j++) acc[i][j] = typename M::acc{0, 0, 0, 0};
 
+  // One stage of LDS: the next step's tiles are loaded once every wave has this
+  // one's fragments in registers, and the other blocks of the CU (two or three,
+  // by registers and LDS) multiply while they arrive and while this one stores.
+  // A second stage in its place leaves room for fewer or smaller blocks:
+  // 16382 x 4096 x 4096 in 585 us (256 x 256, eight waves, one block a CU, which
+  // spends a tenth of a tile on its start and end) against 576 us (256 x 128,
+  // two blocks); 32 experts' row gradient 315 -> 271 us.
+  // The weight gradient's transposed reads take more registers, so its first
+  // half multiplies before the second is read (256 x 128: 380 us, spilled 643 us).
   if (steps > 0) {
     gather_rows(0);
-    load(0, 0);
+    load(0);
     gather_rows(1);
   }
   for (int s = 0; s < steps; s++) {
-    // this step's tiles are in LDS once every wave's loads have landed; the
-    // other buffer is free once every wave has read its fragments of the step before
-    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_waitcnt(0);       // this step's tiles have landed, for every wave
     __builtin_amdgcn_s_barrier();
-    const uint8_t *lq = lds + (s & 1) * kStage, *lp = lq + BQ * 128;
+    const uint8_t *lq = lds, *lp = lq + BQ * 128;
     v4i fq[2][NQ], fp[2][NP];
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
+    auto read = [&](int h) {
 #pragma unroll
       for (int j = 0; j < NP; j++) fp[h][j] = frag_p(lp, j, h);
 #pragma unroll
       for (int j = 0; j < NQ; j++) fq[h][j] = frag_q(lq, j, h);
-    }
-    if (s + 1 < steps) {
-      load(s + 1, (s + 1) & 1);
-      gather_rows(s + 2);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; h++)
+    };
+    auto mul = [&](int h) {
 #pragma unroll
       for (int j = 0; j < NQ; j++)
 #pragma unroll
         for (int i = 0; i < NP; i++) acc[i][j] = M::mma(fp[h][i], fq[h][j], acc[i][j]);
+    };
+    read(0);
+    if (HALF) {
+      mul(0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    read(1);
+    if (s + 1 < steps) {
+      wait_lgkm0();                      // the stage is free once every wave has read it
+      __builtin_amdgcn_s_barrier();
+      load(s + 1);
+      gather_rows(s + 2);
+    }
+    if (!HALF) mul(0);
+    mul(1);
   }
 
   // ---- outputs
-  mm_by_output(a.out_type, [&](auto out) {
-    constexpr int OUT = decltype(out)::value;
+  const long orow = OP == MM_DW ? (long)t.e * a.N + q0 : (long)t.row0;   // row 0 of the tile
+  float xs[TYPE == MM_I8 ? NQ : 1];
+  if constexpr (TYPE == MM_I8) {
 #pragma unroll
     for (int j = 0; j < NQ; j++) {
       const int q = wq * TQ + 16 * j + l16;
-      if (q >= qn) continue;
-      const long row = OP == MM_DW ? (long)t.e * a.N + q0 + q : (long)t.row0 + q;
-      float xs = 0.f;
-      if (TYPE == MM_I8) {
-        const long xr = mm_x_row(a, (int)row);
-        xs = xr < 0 ? 0.f : a.x_scales[xr];
+      const long xr = q < qn ? mm_x_row(a, t.row0 + q) : -1;
+      xs[j] = xr < 0 ? 0.f : a.x_scales[xr];
+    }
+  }
+  mm_by_output(a.out_type, [&](auto out) {
+    constexpr int OUT = decltype(out)::value;
+#pragma unroll
+    for (int i0 = 0; i0 < NP; i0 += 4) {
+      const int pc = p0 + wp * TP + 16 * i0, p = pc + 16 * g;
+      float ws[TYPE == MM_I8 ? 16 : 1];
+      if constexpr (TYPE == MM_I8) {
+#pragma unroll
+        for (int k = 0; k < 16; k++) ws[k] = p + k < pn ? a.w_scales[(size_t)t.e * a.N + p + k] : 0.f;
       }
 #pragma unroll
-      for (int i0 = 0; i0 < NP; i0 += 4) {
+      for (int j = 0; j < NQ; j++) {
+        const int q = wq * TQ + 16 * j + l16;
+        if (q >= qn) continue;
         float v[16];
 #pragma unroll
         for (int i = 0; i < 4; i++)
 #pragma unroll
           for (int k = 0; k < 4; k++) v[4 * i + k] = (float)acc[i0 + i][j][k];
-        const int pc = p0 + wp * TP + 16 * i0;
-        if (!TP_T) {                       // 16 consecutive columns
-          const int p = pc + 16 * g;
-          if (TYPE == MM_I8) {
-            const float *ws = a.w_scales + (size_t)t.e * a.N;
+        if constexpr (TYPE == MM_I8) {
 #pragma unroll
-            for (int k = 0; k < 16; k++) v[k] *= xs * (p + k < pn ? ws[p + k] : 0.f);
-          }
+          for (int k = 0; k < 16; k++) v[k] *= xs[j] * ws[k];
+        }
+        // 16 bits: 16 consecutive columns a lane, 32 bits: columns 16 i + 4 g + k with lane
+        // group g, so that four lanes' 16 bytes meet; the lane groups trade for the other
+        // of the two (64-byte pieces a lane cost the weight gradient 432 us for 381 us)
+        if (TP_T == (OUT != MM_FP32)) swap_columns(v);
+        const long at = (orow + q) * pn;
+        if (OUT == MM_FP32) {
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            if (pc + 16 * i + 4 * g < pn) mm_store4<OUT>(a, at + pc + 16 * i + 4 * g, v + 4 * i);
+        } else {
 #pragma unroll
           for (int k = 0; k < 16; k += 8)
-            if (p + k < pn) mm_store8<OUT>(a, row * pn + p + k, v + k);
-        } else {                           // four runs of 4 columns, 16 apart
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const int p = pc + 16 * i + 4 * g;
-            if (p < pn) mm_store4<OUT>(a, row * pn + p, v + 4 * i);
-          }
+            if (p + k < pn) mm_store8<OUT>(a, at + p + k, v + k);
         }
       }
     }
@@ -577,22 +626,53 @@ static hipError_t launch_stream(const MmArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Tile shapes, all of four waves: 256 x 128 and 128 x 256 two blocks a CU,
+// 128 x 128 three, 64 x 128 four.
+enum MmShape { MM_256x128, MM_128x256, MM_128x128, MM_64x128 };
+
+// The shape whose full rounds of blocks over the 256 CUs cover the least output,
+// weighed by what a shape reaches when it fills the chip (measured on 16382 x
+// 4096 x 4096: 576, 598, 636 and TODO us).  Row tiles are estimated for groups
+// of even size, half a tile a group lost.
+static MmShape mm_shape(long R, long E, long pn) {
+  static const struct { int bq, bp, occ; float weight; } shapes[] = {
+      {256, 128, 2, 1.0f}, {128, 256, 2, 1.04f}, {128, 128, 3, 1.1f}, {64, 128, 4, 1.4f}};
+  int best = 0;
+  float least = 0.f;
+  for (int i = 0; i < 4; i++) {
+    const auto &s = shapes[i];
+    const long groups = E < R ? E : R;
+    const long rows = E == 1 ? (R + s.bq - 1) / s.bq : (R + groups * (s.bq / 2)) / s.bq;
+    const long tiles = (rows > groups ? rows : groups) * ((pn + s.bp - 1) / s.bp), slots = 256l * s.occ;
+    const float cost = (float)((tiles + slots - 1) / slots * s.occ) * (float)(s.bq * s.bp) * s.weight;
+    if (i == 0 || cost < least) best = i, least = cost;
+  }
+  return (MmShape)best;
+}
+
+template <int OP, int TYPE>
+static hipError_t launch_rows(const MmArgs &a, hipStream_t s) {
+  switch (mm_shape(a.R, a.E, OP == MM_FORWARD ? a.N : a.K)) {
+    case MM_256x128: return launch_tile<OP, TYPE, 256, 128, 2, 2, 2>(a, s);
+    case MM_128x256: return launch_tile<OP, TYPE, 128, 256, 2, 2, 2>(a, s);
+    case MM_128x128: return launch_tile<OP, TYPE, 128, 128, 2, 2, 3>(a, s);
+    default: return launch_tile<OP, TYPE, 64, 128, 2, 2, 4>(a, s);
+  }
+}
+
 template <int TYPE>
 static hipError_t launch_forward(const MmArgs &a, hipStream_t s) {
-  const long avg = a.R / a.E;
   if (a.R <= 8l * a.E || a.R <= 16) return launch_stream<TYPE>(a, s);
-  if (avg >= 160) return launch_tile<MM_FORWARD, TYPE, 256, 256, 2, 4, 2>(a, s);
-  if (avg >= 96) return launch_tile<MM_FORWARD, TYPE, 128, 256, 2, 4, 2>(a, s);
-  return launch_tile<MM_FORWARD, TYPE, 64, 256, 1, 4, 2>(a, s);
+  return launch_rows<MM_FORWARD, TYPE>(a, s);
 }
 
 template <int TYPE>
 static hipError_t launch_16bit(const MmArgs &a, hipStream_t s) {
   if (a.op == MM_FORWARD) return launch_forward<TYPE>(a, s);
-  if (a.op == MM_DW) return launch_tile<MM_DW, TYPE, 256, 256, 2, 4, 2>(a, s);
-  const long avg = a.R / a.E;
-  if (avg >= 160) return launch_tile<MM_DX, TYPE, 256, 256, 2, 4, 2>(a, s);
-  return launch_tile<MM_DX, TYPE, 64, 256, 1, 4, 2>(a, s);
+  if (a.op == MM_DX) return launch_rows<MM_DX, TYPE>(a, s);
+  // short sums write more than they read: smaller tiles, more blocks to store
+  if (a.R < 128l * a.E || (long)a.E * a.N * a.K < 512l * 256 * 128) return launch_tile<MM_DW, TYPE, 128, 128, 2, 2, 3>(a, s);
+  return launch_tile<MM_DW, TYPE, 256, 128, 2, 2, 2>(a, s);
 }
 
 hipError_t launch_mm(const MmArgs &a, hipStream_t s) {
