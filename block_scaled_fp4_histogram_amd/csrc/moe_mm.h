@@ -25,7 +25,18 @@ struct MmArgs {
   int E, R, N, K;
   const float *x_scales, *w_scales;  // MM_I8: per row of x, per channel [E, N]
   void *out;                         // [R, N], [R, K] or [E, N, K]
+  float *part;                       // scratch of a split reduction: [splits] of out in 32 bits
+  int splits;                        // set by launch_mm
 };
+
+// How a product of these sizes runs: by streaming or in tiles of a shape, with
+// the reduction in how many parts, and the scratch bytes those take.  Host only,
+// from the sizes alone.
+struct MmPlan {
+  int stream, shape, splits;
+  size_t scratch;
+};
+MmPlan mm_plan(int op, int type, long E, long R, long N, long K);
 
 hipError_t launch_mm(const MmArgs &a, hipStream_t s);
 

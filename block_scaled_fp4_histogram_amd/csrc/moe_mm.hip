@@ -69,9 +69,11 @@ template <int V>
 struct MmConst {
   static constexpr int value = V;
 };
+constexpr int MM_PART = 5;   // 32-bit sums of one part of the reduction, as they are
 template <typename F>
 __device__ __forceinline__ void mm_by_output(int out_type, F f) {
-  if (out_type == MM_FP32) f(MmConst<MM_FP32>{});
+  if (out_type == MM_PART) f(MmConst<MM_PART>{});
+  else if (out_type == MM_FP32) f(MmConst<MM_FP32>{});
   else if (out_type == MM_BF16) f(MmConst<MM_BF16>{});
   else f(MmConst<MM_FP16>{});
 }
@@ -259,7 +261,9 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   }
   const int p0 = t.pt * BP;
   constexpr int ZS = (TQ_T || TP_T) ? 64 : 128 / ES;            // reduction elements a step
-  const int steps = (zn + ZS - 1) / ZS;
+  // with a split reduction, this block's share of the steps
+  const int all = (zn + ZS - 1) / ZS, share = a.splits > 1 ? (all + a.splits - 1) / a.splits : all;
+  const int begin = (int)blockIdx.y * share, steps = min(all, begin + share);
 
   // ---- loads of one step
   const uint8_t *x = (const uint8_t *)a.x, *dy = (const uint8_t *)a.dy;
@@ -287,15 +291,12 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   const Rsrc rp = OP == MM_FORWARD ? mm_rsrc(wt + (size_t)p0 * ldx, (uint32_t)min(BP, pn - p0) * ldx) : mm_rsrc(wt, 0);
   // forward gather: each load's row of x
   constexpr bool GF = GATHER && OP == MM_FORWARD, GW = GATHER && OP == MM_DW;
-  const uint8_t *gx[GF ? CQ : 1];
-  bool glive[GF ? CQ : 1];
+  int grow[GF ? CQ : 1];
   if constexpr (GF) {
 #pragma unroll
     for (int i = 0; i < CQ; i++) {
       const int r = rq0 + i * DQ;
-      const long xr = r < qn ? mm_x_row(a, t.row0 + r) : -1;
-      glive[i] = xr >= 0;
-      gx[i] = glive[i] ? x + xr * ldx + cq : (const uint8_t *)g_mm_zeros;
+      grow[i] = r < qn ? (int)mm_x_row(a, t.row0 + r) : -1;
     }
   }
   // weight gradient gather: rows of x behind this lane's rows of step s, read one
@@ -324,8 +325,9 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     for (int i = 0; i < CQ; i++) {
       lds_void *dst = (lds_void *)(lq + i * NW * 1024);
       if constexpr (GF) {
-        const uint8_t *g = gx[i] + (glive[i] ? s * 128 : 0);
-        __builtin_amdgcn_global_load_lds((int)cq < left ? g : (const uint8_t *)g_mm_zeros, dst, 16, 0, 0);
+        const bool ok = grow[i] >= 0 && (int)cq < left;
+        const uint8_t *g = ok ? x + ((size_t)(uint32_t)grow[i] * ldx + (cq + s * 128)) : (const uint8_t *)g_mm_zeros;
+        __builtin_amdgcn_global_load_lds(g, dst, 16, 0, 0);
       } else {
         const uint32_t v = vq + (uint32_t)(i * DQ) * ldq;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(sq, dst, 16, (int)(TQ_T || (int)cq < left ? v : kOutside),
@@ -389,12 +391,12 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   // two blocks); 32 experts' row gradient 315 -> 271 us.
   // The weight gradient's transposed reads take more registers, so its first
   // half multiplies before the second is read (256 x 128: 380 us, spilled 643 us).
-  if (steps > 0) {
-    gather_rows(0);
-    load(0);
-    gather_rows(1);
+  if (begin < steps) {
+    gather_rows(begin);
+    load(begin);
+    gather_rows(begin + 1);
   }
-  for (int s = 0; s < steps; s++) {
+  for (int s = begin; s < steps; s++) {
     __builtin_amdgcn_s_waitcnt(0);       // this step's tiles have landed, for every wave
     __builtin_amdgcn_s_barrier();
     const uint8_t *lq = lds, *lp = lq + BQ * 128;
@@ -438,8 +440,9 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       xs[j] = xr < 0 ? 0.f : a.x_scales[xr];
     }
   }
-  mm_by_output(a.out_type, [&](auto out) {
+  mm_by_output(a.splits > 1 ? MM_PART : a.out_type, [&](auto out) {
     constexpr int OUT = decltype(out)::value;
+    constexpr bool WIDE = OUT == MM_FP32 || OUT == MM_PART;
 #pragma unroll
     for (int i0 = 0; i0 < NP; i0 += 4) {
       const int pc = p0 + wp * TP + 16 * i0, p = pc + 16 * g;
@@ -456,17 +459,27 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; i++)
 #pragma unroll
-          for (int k = 0; k < 4; k++) v[4 * i + k] = (float)acc[i0 + i][j][k];
-        if constexpr (TYPE == MM_I8) {
+          for (int k = 0; k < 4; k++) {
+            const auto e = acc[i0 + i][j][k];
+            v[4 * i + k] = OUT == MM_PART ? __builtin_bit_cast(float, e) : (float)e;
+          }
+        if constexpr (TYPE == MM_I8 && OUT != MM_PART) {
 #pragma unroll
           for (int k = 0; k < 16; k++) v[k] *= xs[j] * ws[k];
         }
         // 16 bits: 16 consecutive columns a lane, 32 bits: columns 16 i + 4 g + k with lane
         // group g, so that four lanes' 16 bytes meet; the lane groups trade for the other
         // of the two (64-byte pieces a lane cost the weight gradient 432 us for 381 us)
-        if (TP_T == (OUT != MM_FP32)) swap_columns(v);
+        if (TP_T == !WIDE) swap_columns(v);
         const long at = (orow + q) * pn;
-        if (OUT == MM_FP32) {
+        if (OUT == MM_PART) {
+          const long outs = OP == MM_DW ? (long)a.E * a.N : (long)a.R;
+          float *o = a.part + ((long)blockIdx.y * outs * pn + at);
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            if (pc + 16 * i + 4 * g < pn)
+              *(v4f *)(o + pc + 16 * i + 4 * g) = v4f{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+        } else if (OUT == MM_FP32) {
 #pragma unroll
           for (int i = 0; i < 4; i++)
             if (pc + 16 * i + 4 * g < pn) mm_store4<OUT>(a, at + pc + 16 * i + 4 * g, v + 4 * i);
@@ -480,6 +493,56 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   });
 }
 
+// Joins the parts of a split reduction, in their order: a block per output row,
+// eight columns a thread at a time.  A row of the groups' rows finds its group
+// by comparing all offsets; rows in no group are left alone.
+template <int TYPE>
+__global__ __launch_bounds__(256) void k_mm_join(MmArgs a) {
+  typedef typename MmElem<TYPE>::acc Acc;
+  const int pn = a.op == MM_FORWARD ? a.N : a.K;
+  const long row = blockIdx.x, outs = a.op == MM_DW ? (long)a.E * a.N : (long)a.R;
+  int e = 0;
+  if (a.op != MM_DW && a.first) {
+    const int lane = threadIdx.x & 63;
+    e = -1;
+    for (int b = 0; b < a.E; b += 64) {
+      int lo = 0, hi = 0;
+      if (b + lane < a.E) mm_group(a, b + lane, lo, hi);
+      const unsigned long long m = __ballot(row >= lo && row < hi);
+      if (m) {
+        e = b + __ffsll(m) - 1;
+        break;
+      }
+    }
+    if (e < 0) return;
+  }
+  float xs = 0.f;
+  if (TYPE == MM_I8) {
+    const long xr = mm_x_row(a, (int)row);
+    if (xr >= 0) xs = a.x_scales[xr];
+  }
+  mm_by_output(a.out_type, [&](auto out) {
+    constexpr int OUT = decltype(out)::value;
+    if constexpr (OUT != MM_PART) {
+      for (int p = threadIdx.x * 8; p < pn; p += 256 * 8) {
+        Acc s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        for (int i = 0; i < a.splits; i++) {
+          const Acc *part = (const Acc *)(a.part + ((long)i * outs + row) * pn + p);
+          s[0] += part[0];
+          s[1] += part[1];
+        }
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          v[k] = (float)s[k >> 2][k & 3];
+          if (TYPE == MM_I8) v[k] *= xs * a.w_scales[(size_t)e * a.N + p + k];
+        }
+        mm_store8<OUT>(a, row * pn + p, v);
+      }
+    }
+  });
+}
+
 template <int OP, int TYPE, int BQ, int BP, int WQ, int WP, int MINW>
 static hipError_t launch_tile(const MmArgs &a, hipStream_t s) {
   const long pn = OP == MM_FORWARD ? a.N : a.K, ptiles = (pn + BP - 1) / BP;
@@ -487,10 +550,13 @@ static hipError_t launch_tile(const MmArgs &a, hipStream_t s) {
   if (OP == MM_DW) blocks = 8l * a.E * (((a.N + BQ - 1) / BQ * ptiles + 7) / 8);
   else blocks = (((a.R + BQ - 1) / BQ + (a.first ? (a.E < a.R ? a.E : a.R) : 0)) * ptiles + 7) / 8 * 8;
   if (blocks > INT32_MAX / (64 * WQ * WP)) return hipErrorInvalidValue;
-  if (OP != MM_DX && a.rows)
-    hipLaunchKernelGGL((k_mm_tile<OP, TYPE, BQ, BP, WQ, WP, true, MINW>), dim3((unsigned)blocks), dim3(64 * WQ * WP), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_mm_tile<OP, TYPE, BQ, BP, WQ, WP, false, MINW>), dim3((unsigned)blocks), dim3(64 * WQ * WP), 0, s, a);
+  const dim3 grid((unsigned)blocks, (unsigned)a.splits), threads(64 * WQ * WP);
+  if (OP != MM_DX && a.rows) hipLaunchKernelGGL((k_mm_tile<OP, TYPE, BQ, BP, WQ, WP, true, MINW>), grid, threads, 0, s, a);
+  else hipLaunchKernelGGL((k_mm_tile<OP, TYPE, BQ, BP, WQ, WP, false, MINW>), grid, threads, 0, s, a);
+  if (a.splits > 1) {
+    const long outs = OP == MM_DW ? (long)a.E * a.N : (long)a.R;
+    hipLaunchKernelGGL(k_mm_join<TYPE>, dim3((unsigned)outs), dim3(256), 0, s, a);
+  }
   return hipGetLastError();
 }
 
@@ -626,59 +692,91 @@ static hipError_t launch_stream(const MmArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tile shapes, all of four waves: 256 x 128 and 128 x 256 two blocks a CU,
-// 128 x 128 three, 64 x 128 four.
-enum MmShape { MM_256x128, MM_128x256, MM_128x128, MM_64x128 };
+// ------------------------------------------------------------ the choice
+//
+// Tile shapes, all of four waves, and the blocks of each that a CU holds; weight:
+// what covering an output element costs beside 256 x 128 once the chip is full
+// (16382 x 4096 x 4096: 576, 598 and 636 us for the first three).
+enum { kShapes = 4 };
+static const struct { int bq, bp, occ; float weight; } kMmShapes[kShapes] = {
+    {256, 128, 2, 1.0f}, {128, 256, 2, 1.04f}, {128, 128, 3, 1.2f}, {64, 128, 4, 1.5f}};
 
-// The shape whose full rounds of blocks over the 256 CUs cover the least output,
-// weighed by what a shape reaches when it fills the chip (measured on 16382 x
-// 4096 x 4096: 576, 598, 636 and TODO us).  Row tiles are estimated for groups
-// of even size, half a tile a group lost.
-static MmShape mm_shape(long R, long E, long pn) {
-  static const struct { int bq, bp, occ; float weight; } shapes[] = {
-      {256, 128, 2, 1.0f}, {128, 256, 2, 1.04f}, {128, 128, 3, 1.1f}, {64, 128, 4, 1.4f}};
-  int best = 0;
-  float least = 0.f;
-  for (int i = 0; i < 4; i++) {
-    const auto &s = shapes[i];
-    const long groups = E < R ? E : R;
-    const long rows = E == 1 ? (R + s.bq - 1) / s.bq : (R + groups * (s.bq / 2)) / s.bq;
-    const long tiles = (rows > groups ? rows : groups) * ((pn + s.bp - 1) / s.bp), slots = 256l * s.occ;
-    const float cost = (float)((tiles + slots - 1) / slots * s.occ) * (float)(s.bq * s.bp) * s.weight;
-    if (i == 0 || cost < least) best = i, least = cost;
+MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
+  MmPlan m = {0, 0, 1, 0};
+  const long item = type == MM_I8 ? 1 : 2, groups = E < R ? E : R;
+  const long pn = op == MM_FORWARD ? N : K, qn = op == MM_DW ? N : R, outs = op == MM_DW ? E * N : R;
+  // Few rows a group: the weights pass once, and 16 of their rows a block.  Short
+  // reductions leave its waves without work (125 groups of 5 rows, K = 64: 74 us,
+  // TODO us in tiles); many rows read the weights again for every 16, which only
+  // pays while tiles would leave most of the chip idle.
+  if (op == MM_FORWARD && K * item >= 512) {
+    const long tiles16 = ((R + 15) / 16 + (E > 1 ? groups : 0)) * ((N + 15) / 16);
+    if (R <= 8 * E || R <= 16 || (R <= 64 * E && tiles16 <= 2048)) {
+      m.stream = 1;
+      return m;
+    }
   }
-  return (MmShape)best;
+  // The shape whose full rounds of blocks cover the least output.  Row tiles are
+  // estimated for groups of even size, half a tile a group lost.
+  long tiles = 0;
+  float least = 0.f;
+  for (int i = 0; i < kShapes; i++) {
+    const auto &s = kMmShapes[i];
+    if (op == MM_DW && i != 0 && i != 2) continue;
+    long rows = (qn + s.bq - 1) / s.bq;
+    if (op == MM_DW) rows *= E;
+    else if (E > 1) rows = (R + groups * (s.bq / 2)) / s.bq > groups ? (R + groups * (s.bq / 2)) / s.bq : groups;
+    const long n = rows * ((pn + s.bp - 1) / s.bp), slots = 256l * s.occ;
+    const float cost = (float)((n + slots - 1) / slots * s.occ) * (float)(s.bq * s.bp) * s.weight;
+    if (!tiles || cost < least) m.shape = i, least = cost, tiles = n;
+  }
+  // short weight gradients write more than they read: more blocks to store
+  if (op == MM_DW && R < 128 * E) m.shape = 2;
+  // Too few tiles for the chip: the reduction is split, and the parts joined in
+  // order by a second launch.
+  const long steps = op == MM_FORWARD ? K * item / 128 : op == MM_DX ? N / 64 : R / E / 64;
+  const long slots = 256l * kMmShapes[m.shape].occ;
+  if (tiles * 2 <= slots && steps >= 32) {
+    long splits = slots / tiles;
+    if (splits > steps / 8) splits = steps / 8;
+    if (splits > 16) splits = 16;
+    if (splits > 1) {
+      m.splits = (int)splits;
+      m.scratch = (size_t)splits * outs * pn * 4;
+    }
+  }
+  return m;
 }
 
 template <int OP, int TYPE>
-static hipError_t launch_rows(const MmArgs &a, hipStream_t s) {
-  switch (mm_shape(a.R, a.E, OP == MM_FORWARD ? a.N : a.K)) {
-    case MM_256x128: return launch_tile<OP, TYPE, 256, 128, 2, 2, 2>(a, s);
-    case MM_128x256: return launch_tile<OP, TYPE, 128, 256, 2, 2, 2>(a, s);
-    case MM_128x128: return launch_tile<OP, TYPE, 128, 128, 2, 2, 3>(a, s);
+static hipError_t launch_rows(const MmArgs &a, int shape, hipStream_t s) {
+  switch (shape) {
+    case 0: return launch_tile<OP, TYPE, 256, 128, 2, 2, 2>(a, s);
+    case 1: return launch_tile<OP, TYPE, 128, 256, 2, 2, 2>(a, s);
+    case 2: return launch_tile<OP, TYPE, 128, 128, 2, 2, 3>(a, s);
     default: return launch_tile<OP, TYPE, 64, 128, 2, 2, 4>(a, s);
   }
 }
 
 template <int TYPE>
-static hipError_t launch_forward(const MmArgs &a, hipStream_t s) {
-  if (a.R <= 8l * a.E || a.R <= 16) return launch_stream<TYPE>(a, s);
-  return launch_rows<MM_FORWARD, TYPE>(a, s);
+static hipError_t launch_forward(const MmArgs &a, const MmPlan &m, hipStream_t s) {
+  return m.stream ? launch_stream<TYPE>(a, s) : launch_rows<MM_FORWARD, TYPE>(a, m.shape, s);
 }
 
 template <int TYPE>
-static hipError_t launch_16bit(const MmArgs &a, hipStream_t s) {
-  if (a.op == MM_FORWARD) return launch_forward<TYPE>(a, s);
-  if (a.op == MM_DX) return launch_rows<MM_DX, TYPE>(a, s);
-  // short sums write more than they read: smaller tiles, more blocks to store
-  if (a.R < 128l * a.E || (long)a.E * a.N * a.K < 512l * 256 * 128) return launch_tile<MM_DW, TYPE, 128, 128, 2, 2, 3>(a, s);
-  return launch_tile<MM_DW, TYPE, 256, 128, 2, 2, 2>(a, s);
+static hipError_t launch_16bit(const MmArgs &a, const MmPlan &m, hipStream_t s) {
+  if (a.op == MM_FORWARD) return launch_forward<TYPE>(a, m, s);
+  if (a.op == MM_DX) return launch_rows<MM_DX, TYPE>(a, m.shape, s);
+  return m.shape == 2 ? launch_tile<MM_DW, TYPE, 128, 128, 2, 2, 3>(a, s) : launch_tile<MM_DW, TYPE, 256, 128, 2, 2, 2>(a, s);
 }
 
-hipError_t launch_mm(const MmArgs &a, hipStream_t s) {
-  return a.type == MM_I8     ? launch_forward<MM_I8>(a, s)
-         : a.type == MM_BF16 ? launch_16bit<MM_BF16>(a, s)
-                             : launch_16bit<MM_FP16>(a, s);
+hipError_t launch_mm(const MmArgs &args, hipStream_t s) {
+  const MmPlan m = mm_plan(args.op, args.type, args.E, args.R, args.N, args.K);
+  MmArgs a = args;
+  a.splits = m.splits;
+  return a.type == MM_I8     ? launch_forward<MM_I8>(a, m, s)
+         : a.type == MM_BF16 ? launch_16bit<MM_BF16>(a, m, s)
+                             : launch_16bit<MM_FP16>(a, m, s);
 }
 
 }  // namespace moe

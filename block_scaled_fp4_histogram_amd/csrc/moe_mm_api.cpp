@@ -59,6 +59,13 @@ int check_rows(const char *fn, const int32_t *rows, long long x_rows, int R) {
   return MOE_OK;
 }
 
+int check_scratch(const char *fn, int op, int E, int R, int N, int K, const void *scratch, size_t bytes) {
+  const size_t need = moe_mm_scratch_bytes(op, E, R, N, K);
+  if (need && (!scratch || !aligned(scratch, 16))) return fail(MOE_EINVAL, "%s: null or misaligned scratch (16 bytes)", fn);
+  if (bytes < need) return fail(MOE_ESCRATCH, "%s: scratch holds %zu bytes, %zu needed", fn, bytes, need);
+  return MOE_OK;
+}
+
 }  // namespace
 
 #define TRY(expr)              \
@@ -70,8 +77,10 @@ int check_rows(const char *fn, const int32_t *rows, long long x_rows, int R) {
 extern "C" {
 
 size_t moe_mm_scratch_bytes(int op, int E, int R, int N, int K) {
-  (void)op, (void)E, (void)R, (void)N, (void)K;
-  return 0;
+  const bool i8 = op == MOE_MM_INT8;
+  if (op < MOE_MM_FORWARD || op > MOE_MM_INT8 || check_shape("moe_mm_scratch_bytes", i8 ? 16 : 8, nullptr, E, R, N, K) != MOE_OK)
+    return 0;
+  return R == 0 ? 0 : moe::mm_plan(i8 ? MOE_MM_FORWARD : op, i8 ? moe::MM_I8 : moe::MM_BF16, E, R, N, K).scratch;
 }
 
 int moe_grouped_mm(int dtype, const void *x, long long x_rows, const int32_t *rows, const void *w,
@@ -85,7 +94,9 @@ int moe_grouped_mm(int dtype, const void *x, long long x_rows, const int32_t *ro
   if (!first) return fail(MOE_EINVAL, "%s: null first", fn);
   const void *p[] = {x, w, out};
   TRY(check_ptrs(fn, p, 3));
+  TRY(check_scratch(fn, MOE_MM_FORWARD, E, R, N, K, scratch, scratch_bytes));
   moe::MmArgs a = {};
+  a.part = (float *)scratch;
   a.op = moe::MM_FORWARD, a.type = dtype, a.out_type = out_dtype;
   a.x = x, a.x_rows = (long)x_rows, a.rows = rows, a.w = w, a.first = first;
   a.E = E, a.R = R, a.N = N, a.K = K, a.out = out;
@@ -101,7 +112,9 @@ int moe_grouped_mm_dx(int dtype, const void *dy, const void *w, const int32_t *f
   if (!first) return fail(MOE_EINVAL, "%s: null first", fn);
   const void *p[] = {dy, w, dx};
   TRY(check_ptrs(fn, p, 3));
+  TRY(check_scratch(fn, MOE_MM_DX, E, R, N, K, scratch, scratch_bytes));
   moe::MmArgs a = {};
+  a.part = (float *)scratch;
   a.op = moe::MM_DX, a.type = dtype, a.out_type = out_dtype;
   a.dy = dy, a.w = w, a.first = first;
   a.E = E, a.R = R, a.N = N, a.K = K, a.out = dx;
@@ -119,7 +132,9 @@ int moe_grouped_mm_dw(int dtype, const void *dy, const void *x, long long x_rows
   if (!first) return fail(MOE_EINVAL, "%s: null first", fn);
   const void *p[] = {dw, dy, x};   // without rows dy and x are not read
   TRY(check_ptrs(fn, p, R ? 3 : 1));
+  TRY(check_scratch(fn, MOE_MM_DW, E, R, N, K, scratch, scratch_bytes));
   moe::MmArgs a = {};
+  a.part = (float *)scratch;
   a.op = moe::MM_DW, a.type = dtype, a.out_type = out_dtype, a.accumulate = accumulate;
   a.dy = dy, a.x = x, a.x_rows = (long)x_rows, a.rows = rows, a.first = first;
   a.E = E, a.R = R, a.N = N, a.K = K, a.out = dw;
@@ -153,7 +168,9 @@ int moe_grouped_int8_mm(const int8_t *x, const float *x_scales, long long x_rows
   TRY(check_ptrs(fn, p, 3));
   if (!x_scales || !w_scales || !aligned(x_scales, 4) || !aligned(w_scales, 4))
     return fail(MOE_EINVAL, "%s: null or misaligned scales", fn);
+  TRY(check_scratch(fn, MOE_MM_INT8, E, R, N, K, scratch, scratch_bytes));
   moe::MmArgs a = {};
+  a.part = (float *)scratch;
   a.op = moe::MM_FORWARD, a.type = moe::MM_I8, a.out_type = out_dtype;
   a.x = x, a.x_rows = (long)x_rows, a.rows = rows, a.x_scales = x_scales, a.w = w, a.w_scales = w_scales;
   a.first = first, a.E = E, a.R = R, a.N = N, a.K = K, a.out = out;
