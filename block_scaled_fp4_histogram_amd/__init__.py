@@ -341,86 +341,34 @@ def ep_remap(topk_ids, topk_weights, offset: int, num_local: int, out_ids=None, 
     return out_ids, out_weights
 
 
-class _Runtime:
-    """What the products' calls look up every time, gathered at the first one: a call on a few rows
-    costs little more than its launch, so attribute chains count (10.1 -> 9.1 us a call)."""
+_binding = None
 
-    def __init__(self):
+
+def _bind():
+    """The compiled torch binding of the products (csrc/moe_torch.cpp), given the library's addresses
+    once. Raises ImportError when it has not been built."""
+    global _binding
+    if _binding is None:
         import torch
-        self.torch, self.lib = torch, _lib.load()
-        self.empty = torch.empty
-        self.current_device = torch.cuda.current_device
-        # the stream's handle: building a Stream object takes longer than the launch
-        self.current_stream = torch._C._cuda_getCurrentRawStream
-        self.codes = {torch.bfloat16: T_BF16, torch.float16: T_FP16, torch.float32: T_FP32}
-        self.any_float = tuple(self.codes)
-        self.half = (torch.bfloat16, torch.float16)
-        self.outs = {t: (t, torch.float32) for t in self.half}
-        self.i8, self.i32, self.f32 = (torch.int8,), (torch.int32,), (torch.float32,)
-
-
-_runtime = None
-
-
-def _rt():
-    global _runtime
-    if _runtime is None:
-        _runtime = _Runtime()
-    return _runtime
-
-
-def _operands(named):
-    """Checks (name, tensor, dtypes, shape) operands: types and shapes first, then that all are
-    contiguous on one GPU, whose device index it returns. Optional tensors are left out by the caller."""
-    for name, t, dtypes, shape in named:
-        if t is None:
-            raise ValueError(f"{name} is required")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    dev = named[0][1].get_device()
-    for name, t, _, _ in named:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        d = t.get_device()
-        if d < 0:
-            raise ValueError(f"{name} must be a device tensor")
-        if d != dev:
-            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {named[0][1].device}")
-    return dev
+        L = _lib.load()
+        try:
+            from . import _products as b
+        except ImportError as e:
+            raise ImportError("block_scaled_fp4_histogram_amd/_products.so is missing or was built for another torch: "
+                              "build it with block_scaled_fp4_histogram_amd/build.py (or __graft_entry__.build())") from e
+        names = [n for n in _lib.SIGNATURES if n.startswith(("moe_grouped", "moe_mm", "moe_quant", "moe_int8", "moe_group_",
+                                                             "moe_last_error"))]
+        b.bind({n: C.cast(getattr(L, n), C.c_void_p).value for n in names}, MoeError, torch._C._cuda_getCurrentRawStream)
+        _binding = b
+    return _binding
 
 
 def _use(stream, t):
     """Makes `stream` current for a call on operand t, so that the tensors made there belong to it too."""
+    import torch
     if t is not None and t.device.type == "cuda" and stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, the operands on {t.device}")
-    return _rt().torch.cuda.stream(stream)
-
-
-def _launch(rt, dev, fn, *args):
-    """fn(*args, stream) on device dev and its current stream."""
-    if dev == rt.current_device():
-        rc = fn(*args, rt.current_stream(dev))
-    else:
-        with rt.torch.cuda.device(dev):
-            rc = fn(*args, rt.current_stream(dev))
-    if rc != MOE_OK:
-        _check(rc)
-
-
-def _mm_scratch(rt, op, E, R, N, K, scratch, like):
-    """(pointer, bytes, tensor) of a product's scratch: the caller's tensor, or one made here when it needs any."""
-    if scratch is not None:
-        _need(scratch, "scratch", rt.torch.uint8)
-        if scratch.device != like.device:
-            raise ValueError(f"scratch is on {scratch.device}, the operands on {like.device}")
-        return scratch.data_ptr(), scratch.numel(), scratch
-    need = rt.lib.moe_mm_scratch_bytes(op, E, R, N, K)
-    if not need:
-        return None, 0, None
-    scratch = rt.empty(need, dtype=rt.torch.uint8, device=like.device)
-    return scratch.data_ptr(), need, scratch
+    return torch.cuda.stream(stream)
 
 
 def mm_scratch_bytes(op: int, E: int, R: int, N: int, K: int) -> int:
@@ -428,30 +376,8 @@ def mm_scratch_bytes(op: int, E: int, R: int, N: int, K: int) -> int:
     return _lib.load().moe_mm_scratch_bytes(op, E, R, N, K)
 
 
-def _out_dtype(out, out_dtype, default, allowed, shape, named):
-    """The output's type; an output that is given joins the operands to check."""
-    if out is not None:
-        if out_dtype is not None and out.dtype != out_dtype:
-            raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
-        named.append(("out", out, allowed, shape))
-        return out.dtype
-    dt = default if out_dtype is None else out_dtype
-    if dt not in allowed:
-        raise TypeError(f"out_dtype: expected {' or '.join(map(str, allowed))}, got {dt}")
-    return dt
-
-
-def _dims(t, name, dim):
-    if t is None or t.dim() != dim:
-        raise ValueError(f"{name} must be a tensor of {dim} dimensions")
-    return t.shape
-
-
-def _half(rt, t, name):
-    """Types an output may have beside the bf16 or fp16 operand t."""
-    if t.dtype not in rt.half:
-        raise TypeError(f"{name}: expected {' or '.join(map(str, rt.half))}, got {t.dtype}")
-    return rt.outs[t.dtype]
+# The products below check types, shapes, contiguity and device of every tensor, make the outputs and the
+# scratch that are not given, and run on `stream` or on the current stream of the operands' device.
 
 
 def grouped_mm(x, w, first, rows=None, out=None, out_dtype=None, scratch=None, stream=None):
@@ -464,23 +390,7 @@ def grouped_mm(x, w, first, rows=None, out=None, out_dtype=None, scratch=None, s
     if stream is not None:
         with _use(stream, x):
             return grouped_mm(x, w, first, rows, out, out_dtype, scratch)
-    rt = _rt()
-    T, K = _dims(x, "x", 2)
-    E, N, _ = _dims(w, "w", 3)
-    outs = _half(rt, x, "x")
-    named = [("x", x, outs, x.shape), ("w", w, (x.dtype,), (E, N, K)), ("first", first, rt.i32, (E + 1,))]
-    R = T
-    if rows is not None:
-        R, = _dims(rows, "rows", 1)
-        named.append(("rows", rows, rt.i32, (R,)))
-    dt = _out_dtype(out, out_dtype, x.dtype, outs, (R, N), named)
-    dev = _operands(named)
-    if out is None:
-        out = rt.empty((R, N), dtype=dt, device=x.device)
-    sp, sb, keep = _mm_scratch(rt, MM_FORWARD, E, R, N, K, scratch, x)
-    _launch(rt, dev, rt.lib.moe_grouped_mm, rt.codes[x.dtype], x.data_ptr(), T, None if rows is None else rows.data_ptr(),
-            w.data_ptr(), first.data_ptr(), E, R, N, K, rt.codes[dt], out.data_ptr(), sp, sb)
-    return out
+    return (_binding or _bind()).grouped_mm(x, w, first, rows, out, out_dtype, scratch)
 
 
 def grouped_mm_dx(dy, w, first, out=None, out_dtype=None, scratch=None, stream=None):
@@ -491,19 +401,7 @@ def grouped_mm_dx(dy, w, first, out=None, out_dtype=None, scratch=None, stream=N
     if stream is not None:
         with _use(stream, dy):
             return grouped_mm_dx(dy, w, first, out, out_dtype, scratch)
-    rt = _rt()
-    R, N = _dims(dy, "dy", 2)
-    E, _, K = _dims(w, "w", 3)
-    outs = _half(rt, dy, "dy")
-    named = [("dy", dy, outs, dy.shape), ("w", w, (dy.dtype,), (E, N, K)), ("first", first, rt.i32, (E + 1,))]
-    dt = _out_dtype(out, out_dtype, dy.dtype, outs, (R, K), named)
-    dev = _operands(named)
-    if out is None:
-        out = rt.empty((R, K), dtype=dt, device=dy.device)
-    sp, sb, keep = _mm_scratch(rt, MM_DX, E, R, N, K, scratch, dy)
-    _launch(rt, dev, rt.lib.moe_grouped_mm_dx, rt.codes[dy.dtype], dy.data_ptr(), w.data_ptr(), first.data_ptr(), E, R, N,
-            K, rt.codes[dt], out.data_ptr(), sp, sb)
-    return out
+    return (_binding or _bind()).grouped_mm_dx(dy, w, first, out, out_dtype, scratch)
 
 
 def grouped_mm_dw(dy, x, first, rows=None, out=None, out_dtype=None, accumulate: bool = False, scratch=None,
@@ -516,27 +414,7 @@ def grouped_mm_dw(dy, x, first, rows=None, out=None, out_dtype=None, accumulate:
     if stream is not None:
         with _use(stream, dy):
             return grouped_mm_dw(dy, x, first, rows, out, out_dtype, accumulate, scratch)
-    rt = _rt()
-    R, N = _dims(dy, "dy", 2)
-    T, K = _dims(x, "x", 2)
-    E = _dims(first, "first", 1)[0] - 1
-    if rows is None and T != R:
-        raise ValueError(f"x: expected {R} rows as dy, got {T}")
-    if accumulate and out is None:
-        raise ValueError("accumulate needs out")
-    outs = _half(rt, dy, "dy")
-    named = [("dy", dy, outs, dy.shape), ("x", x, (dy.dtype,), x.shape), ("first", first, rt.i32, (E + 1,))]
-    if rows is not None:
-        named.append(("rows", rows, rt.i32, (R,)))
-    dt = _out_dtype(out, out_dtype, dy.dtype, outs, (E, N, K), named)
-    dev = _operands(named)
-    if out is None:
-        out = rt.empty((E, N, K), dtype=dt, device=dy.device)
-    sp, sb, keep = _mm_scratch(rt, MM_DW, E, R, N, K, scratch, dy)
-    _launch(rt, dev, rt.lib.moe_grouped_mm_dw, rt.codes[dy.dtype], dy.data_ptr(), x.data_ptr(), T,
-            None if rows is None else rows.data_ptr(), first.data_ptr(), E, R, N, K, rt.codes[dt], int(bool(accumulate)),
-            out.data_ptr(), sp, sb)
-    return out
+    return (_binding or _bind()).grouped_mm_dw(dy, x, first, rows, out, out_dtype, accumulate, scratch)
 
 
 def quant_int8(x, out=None, scales=None, stream=None):
@@ -545,21 +423,7 @@ def quant_int8(x, out=None, scales=None, stream=None):
     if stream is not None:
         with _use(stream, x):
             return quant_int8(x, out, scales)
-    rt = _rt()
-    shape = _dims(x, "x", 2)
-    named = [("x", x, rt.half, shape)]
-    if out is not None:
-        named.append(("out", out, rt.i8, shape))
-    if scales is not None:
-        named.append(("scales", scales, rt.f32, shape[:1]))
-    dev = _operands(named)
-    if out is None:
-        out = rt.empty(shape, dtype=rt.torch.int8, device=x.device)
-    if scales is None:
-        scales = rt.empty(shape[:1], dtype=rt.torch.float32, device=x.device)
-    _launch(rt, dev, rt.lib.moe_quant_int8, rt.codes[x.dtype], x.data_ptr(), shape[0], shape[1], out.data_ptr(),
-            scales.data_ptr())
-    return out, scales
+    return (_binding or _bind()).quant_int8(x, out, scales)
 
 
 def int8_mm(x, x_scales, w, w_scales, out=None, out_dtype=None, scratch=None, stream=None):
@@ -571,19 +435,7 @@ def int8_mm(x, x_scales, w, w_scales, out=None, out_dtype=None, scratch=None, st
     if stream is not None:
         with _use(stream, x):
             return int8_mm(x, x_scales, w, w_scales, out, out_dtype, scratch)
-    rt = _rt()
-    M, K = _dims(x, "x", 2)
-    N, _ = _dims(w, "w", 2)
-    named = [("x", x, rt.i8, x.shape), ("x_scales", x_scales, rt.f32, (M,)), ("w", w, rt.i8, (N, K)),
-             ("w_scales", w_scales, rt.f32, (N,))]
-    dt = _out_dtype(out, out_dtype, rt.torch.bfloat16, rt.any_float, (M, N), named)
-    dev = _operands(named)
-    if out is None:
-        out = rt.empty((M, N), dtype=dt, device=x.device)
-    sp, sb, keep = _mm_scratch(rt, MM_INT8, 1, M, N, K, scratch, x)
-    _launch(rt, dev, rt.lib.moe_int8_mm, x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), M, N, K,
-            rt.codes[dt], out.data_ptr(), sp, sb)
-    return out
+    return (_binding or _bind()).int8_mm(x, x_scales, w, w_scales, out, out_dtype, scratch)
 
 
 def grouped_int8_mm(x, x_scales, w, w_scales, first, rows=None, out=None, out_dtype=None, scratch=None, stream=None):
@@ -592,24 +444,7 @@ def grouped_int8_mm(x, x_scales, w, w_scales, first, rows=None, out=None, out_dt
     if stream is not None:
         with _use(stream, x):
             return grouped_int8_mm(x, x_scales, w, w_scales, first, rows, out, out_dtype, scratch)
-    rt = _rt()
-    T, K = _dims(x, "x", 2)
-    E, N, _ = _dims(w, "w", 3)
-    named = [("x", x, rt.i8, x.shape), ("x_scales", x_scales, rt.f32, (T,)), ("w", w, rt.i8, (E, N, K)),
-             ("w_scales", w_scales, rt.f32, (E, N)), ("first", first, rt.i32, (E + 1,))]
-    R = T
-    if rows is not None:
-        R, = _dims(rows, "rows", 1)
-        named.append(("rows", rows, rt.i32, (R,)))
-    dt = _out_dtype(out, out_dtype, rt.torch.bfloat16, rt.any_float, (R, N), named)
-    dev = _operands(named)
-    if out is None:
-        out = rt.empty((R, N), dtype=dt, device=x.device)
-    sp, sb, keep = _mm_scratch(rt, MM_INT8, E, R, N, K, scratch, x)
-    _launch(rt, dev, rt.lib.moe_grouped_int8_mm, x.data_ptr(), x_scales.data_ptr(), T,
-            None if rows is None else rows.data_ptr(), w.data_ptr(), w_scales.data_ptr(), first.data_ptr(), E, R, N, K,
-            rt.codes[dt], out.data_ptr(), sp, sb)
-    return out
+    return (_binding or _bind()).grouped_int8_mm(x, x_scales, w, w_scales, first, rows, out, out_dtype, scratch)
 
 
 def group_routes(topk_ids, num_experts: int, scratch=None, stream=None):
@@ -622,26 +457,7 @@ def group_routes(topk_ids, num_experts: int, scratch=None, stream=None):
     if stream is not None:
         with _use(stream, topk_ids):
             return group_routes(topk_ids, num_experts, scratch)
-    rt = _rt()
-    T, k = shape = _dims(topk_ids, "topk_ids", 2)
-    dev = _operands([("topk_ids", topk_ids, rt.i32, shape)])
-    E, R = int(num_experts), T * k
-    if E < 1:
-        raise ValueError(f"num_experts must be positive, got {E}")
-    first, order, token, inverse = rt.empty(E + 1 + 3 * R, dtype=rt.torch.int32, device=topk_ids.device).split(
-        [E + 1, R, R, R])
-    need = rt.lib.moe_group_routes_scratch_bytes(T, k, E)
-    if scratch is not None:
-        _need(scratch, "scratch", rt.torch.uint8)
-        if scratch.device != topk_ids.device:
-            raise ValueError(f"scratch is on {scratch.device}, the operands on {topk_ids.device}")
-    elif need:
-        scratch = rt.empty(need, dtype=rt.torch.uint8, device=topk_ids.device)
-    p = first.data_ptr()
-    _launch(rt, dev, rt.lib.moe_group_routes, topk_ids.data_ptr(), T, k, E, p, p + 4 * (E + 1), p + 4 * (E + 1 + R),
-            p + 4 * (E + 1 + 2 * R), None if scratch is None else scratch.data_ptr(),
-            0 if scratch is None else scratch.numel())
-    return first, order, token, inverse.view(shape)
+    return (_binding or _bind()).group_routes(topk_ids, num_experts, scratch)
 
 
 def debug_route(plan: Plan, tiers: Sequence, topk_ids, scratch=None, stream=None):

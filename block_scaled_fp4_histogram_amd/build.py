@@ -1,4 +1,5 @@
-"""Builds the gfx950 library block_scaled_fp4_histogram_amd/libmoe_gfx950.so with hipcc."""
+"""Builds the gfx950 library block_scaled_fp4_histogram_amd/libmoe_gfx950.so with hipcc, and the torch
+binding of its products (_products.so) with the host compiler."""
 import os
 import subprocess
 import sys
@@ -27,6 +28,31 @@ FLAGS = [
 ]
 
 
+BINDING = os.path.join(PKG, "_products.so")
+
+
+def build_binding(verbose: bool = False) -> str:
+    """The torch binding of the products: host code only."""
+    import sysconfig
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include")]
+    for d in include_paths() + [sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "moe_torch.cpp"), "-o", BINDING + ".tmp"]
+    for d in library_paths():
+        cmd += ["-L", d]
+    cmd += ["-lc10", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the binding failed ({r.returncode}):\n{r.stderr}")
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False) -> str:
     cmd = [HIPCC] + FLAGS + SOURCES + ["-o", LIB + ".tmp"]
     if verbose:
@@ -39,6 +65,7 @@ def build(verbose: bool = False) -> str:
     if verbose and err:
         print(err, file=sys.stderr)
     os.replace(LIB + ".tmp", LIB)
+    build_binding(verbose)
     return LIB
 
 

@@ -229,7 +229,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   constexpr int TQ = BQ / WQ, TP = BP / WP, NQ = TQ / 16, NP = TP / 16;
   constexpr int CQ = BQ / 8 / NW, CP = BP / 8 / NW;             // loads of 1 KB a wave and step
   constexpr int kStage = (BQ + BP) * 128;
-  constexpr bool HALF = OP == MM_DW;
+  constexpr bool HALF = OP == MM_DW || GATHER;
   static_assert(TP % 64 == 0 && TQ % 16 == 0 && CQ >= 1 && CP >= 1, "tile shape");
   static_assert(!TQ_T || (BQ % 128 == 0 && TQ % 64 == 0), "transposed Q");
   static_assert(!TP_T || BP % 128 == 0, "transposed P");
