@@ -93,6 +93,13 @@ __device__ __forceinline__ Rsrc mm_rsrc(const uint8_t *base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)bytes, 0x00020000);
 }
 
+// A barrier that LDS accesses are not moved across; the waits are the caller's.
+__device__ __forceinline__ void mm_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Row range of group e.
 __device__ __forceinline__ void mm_group(const MmArgs &a, int e, int &lo, int &hi) {
   if (!a.first) {
@@ -209,12 +216,15 @@ __device__ __forceinline__ long mm_x_row(const MmArgs &a, int r) {
 // LDS images of an operand tile, 128 bytes of the reduction (one step) by B
 // outer indices.  Reduction-contiguous operands: B rows of eight 16-byte
 // chunks, chunk c of row r at slot c ^ swz(r); transposed ones: 64 rows of B
-// 16-bit columns, chunk c of row z at c ^ 2 (z & 7).  Either way the 16 (or,
+// 16-bit columns, chunk c of row z at c ^ 2 swz(z).  Either way the 16 (or,
 // transposed, 32) lanes that read together touch every bank once.
 //   Q rows are read 16 consecutive ones a fragment: swz = (r >> 1) & 7.
 //   P rows are read as 4 runs of 4, 16 apart (below): bits 1, 4 and 5 of r.
 __device__ __forceinline__ int swz_q(int r) { return (r >> 1) & 7; }
+//   Transposed rows are read 8 g .. 8 g + 3 by lane group g, and 4 further on
+//   next: bits 0, 1 and 3 of z.
 __device__ __forceinline__ int swz_p(int r) { return ((r >> 1) & 1) | ((r >> 3) & 6); }
+__device__ __forceinline__ int swz_t(int z) { return (z & 3) | ((z >> 1) & 4); }
 
 // The MFMA's rows are the output's contiguous dimension (P: weights, or x for
 // the weight gradient), its columns the output's rows (Q), so a lane's four
@@ -276,13 +286,16 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   // (i NW + w) 64 / LR + lane / LR.
   constexpr int LRQ = BQ / 8, LRP = BP / 8;
   constexpr int DQ = TQ_T ? NW * 64 / LRQ : NW * 8, DP = TP_T ? NW * 64 / LRP : NW * 8;   // rows between loads
-  static_assert(TQ_T ? DQ % 8 == 0 : DQ % 16 == 0, "the swizzle repeats over a wave's loads of Q");
-  static_assert(TP_T ? DP % 8 == 0 : DP % 32 == 0, "... and of P, but for bit 5 (below)");
+  // The swizzle repeats over a wave's loads, but for one bit of it that flips with
+  // every load where the rows between them reach only that bit: these bytes.
+  static_assert(TQ_T ? DQ % 8 == 0 : DQ % 16 == 0, "loads of Q");
+  static_assert(TP_T ? DP % 8 == 0 : DP % 32 == 0, "loads of P");
+  constexpr uint32_t FQ = TQ_T && DQ % 16 ? 128 : 0, FP = TP_T ? (DP % 16 ? 128 : 0) : (DP % 64 ? 64 : 0);
   const int rq0 = TQ_T ? w * (64 / LRQ) + lane / LRQ : w * 8 + (lane >> 3);
   const int rp0 = TP_T ? w * (64 / LRP) + lane / LRP : w * 8 + (lane >> 3);
   // contiguous: the chunk's byte in the step; transposed: its byte in the row
-  const uint32_t cq = TQ_T ? q0 * 2 + (((lane % LRQ) ^ (2 * (rq0 & 7))) * 16) : ((lane & 7) ^ swz_q(rq0)) * 16;
-  const uint32_t cp = TP_T ? p0 * 2 + (((lane % LRP) ^ (2 * (rp0 & 7))) * 16) : ((lane & 7) ^ swz_p(rp0)) * 16;
+  const uint32_t cq = TQ_T ? q0 * 2 + (((lane % LRQ) ^ (2 * swz_t(rq0))) * 16) : ((lane & 7) ^ swz_q(rq0)) * 16;
+  const uint32_t cp = TP_T ? p0 * 2 + (((lane % LRP) ^ (2 * swz_t(rp0))) * 16) : ((lane & 7) ^ swz_p(rp0)) * 16;
   const uint32_t ldq = OP == MM_FORWARD ? ldx : ldy;
   const uint32_t vq = (uint32_t)rq0 * ldq + cq, vp = (uint32_t)rp0 * ldx + cp;
   const Rsrc rq = OP == MM_FORWARD  ? mm_rsrc(x + (GATHER ? 0 : (size_t)t.row0 * ldx), (uint32_t)qn * ldx)
@@ -302,7 +315,6 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   // weight gradient gather: rows of x behind this lane's rows of step s, read one
   // step before they are loaded
   int gidx[GW ? CP : 1];
-  const bool gcol = cp < ldx;                       // columns past the row's end are not stored
   auto gather_rows = [&](int s) {
     if constexpr (GW) {
 #pragma unroll
@@ -329,7 +341,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
         const uint8_t *g = ok ? x + ((size_t)(uint32_t)grow[i] * ldx + (cq + s * 128)) : (const uint8_t *)g_mm_zeros;
         __builtin_amdgcn_global_load_lds(g, dst, 16, 0, 0);
       } else {
-        const uint32_t v = vq + (uint32_t)(i * DQ) * ldq;
+        const uint32_t v = vq - cq + (cq ^ (i & 1 ? FQ : 0)) + (uint32_t)(i * DQ) * ldq;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(sq, dst, 16, (int)(TQ_T || (int)cq < left ? v : kOutside),
                                                  TQ_T ? 0 : s * 128, 0, 0);
       }
@@ -338,12 +350,12 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     for (int i = 0; i < CP; i++) {
       lds_void *dst = (lds_void *)(lp + i * NW * 1024);
       if constexpr (GW) {
-        const bool ok = gcol && gidx[i] >= 0 && gidx[i] < a.x_rows;
-        const uint8_t *g = ok ? x + ((size_t)(uint32_t)gidx[i] * ldx + cp) : (const uint8_t *)g_mm_zeros;
+        const uint32_t c = cp ^ (i & 1 ? FP : 0);   // columns past the row's end are not stored
+        const bool ok = c < ldx && gidx[i] >= 0 && gidx[i] < a.x_rows;
+        const uint8_t *g = ok ? x + ((size_t)(uint32_t)gidx[i] * ldx + c) : (const uint8_t *)g_mm_zeros;
         __builtin_amdgcn_global_load_lds(g, dst, 16, 0, 0);
       } else {
-        // rows 32 further have bit 5 of their number, so bit 2 of their swizzle, flipped
-        const uint32_t flip = !TP_T && DP == 32 && (i & 1) ? 64 : 0, c = cp ^ flip;
+        const uint32_t c = cp ^ (i & 1 ? FP : 0);
         const uint32_t v = vp - cp + c + (uint32_t)(i * DP) * ldx;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(sp, dst, 16, (int)(TP_T || (int)c < left ? v : kOutside),
                                                  TP_T ? 0 : s * 128, 0, 0);
@@ -354,7 +366,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   // ---- fragments of one half step (64 bytes of the reduction)
   const int wq = w / WP, wp = w % WP, g = lane >> 4, l16 = lane & 15;
   // transposed: rows 8 g + l16 / 4 (+ 4 for the second half of a fragment's k) of the half's 32
-  const int tz = 8 * g + (l16 >> 2), tsw = 2 * (l16 >> 2);
+  const int tz = 8 * g + (l16 >> 2), tsw = 2 * swz_t(tz);
   typedef short v4s __attribute__((ext_vector_type(4)));
   typedef __attribute__((address_space(3))) v4s lds_v4s;
   auto frag_t = [&](const uint8_t *tile, int rb, int col, int h) -> v4i {
@@ -362,7 +374,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     const int c = (col >> 3) + ((l16 & 3) >> 1);
     const uint8_t *p = tile + (32 * h + tz) * rb + 8 * (l16 & 1);
     const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + ((c ^ tsw) * 16)));
-    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + 4 * rb + ((c ^ tsw ^ 8) * 16)));
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + 4 * rb + ((c ^ tsw) * 16)));
     return __builtin_bit_cast(v4i, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
   auto frag_q = [&](const uint8_t *tile, int j, int h) -> v4i {
@@ -398,7 +410,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   }
   for (int s = begin; s < steps; s++) {
     __builtin_amdgcn_s_waitcnt(0);       // this step's tiles have landed, for every wave
-    __builtin_amdgcn_s_barrier();
+    mm_barrier();
     const uint8_t *lq = lds, *lp = lq + BQ * 128;
     v4i fq[2][NQ], fp[2][NP];
     auto read = [&](int h) {
@@ -421,7 +433,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     read(1);
     if (s + 1 < steps) {
       wait_lgkm0();                      // the stage is free once every wave has read it
-      __builtin_amdgcn_s_barrier();
+      mm_barrier();
       load(s + 1);
       gather_rows(s + 2);
     }
@@ -711,7 +723,7 @@ MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
   // pays while tiles would leave most of the chip idle.
   if (op == MM_FORWARD && K * item >= 512) {
     const long tiles16 = ((R + 15) / 16 + (E > 1 ? groups : 0)) * ((N + 15) / 16);
-    if (R <= 8 * E || R <= 16 || (R <= 64 * E && tiles16 <= 2048)) {
+    if (tiles16 < 1l << 23 && (R <= 8 * E || R <= 16 || (R <= 64 * E && tiles16 <= 2048))) {
       m.stream = 1;
       return m;
     }

@@ -1,5 +1,7 @@
 // Row kernels next to the products, for gfx950: the 8-bit integer quantiser
 // and the grouping of routes by expert.
+#include <algorithm>
+
 #include "moe_device.h"
 #include "moe_mm.h"
 
@@ -84,33 +86,35 @@ __device__ __forceinline__ RowScale row_scale(uint32_t m) {
 // (8 rows of 7168: 3.5 us, 6.4 us with four chunks on 256 threads).  A row
 // with an infinity or NaN gets scale NaN and codes 0, so its products are NaN.
 template <int TYPE>
-__global__ __launch_bounds__(1024) void k_quant_int8(const uint16_t *x, int cols, int8_t *q, float *scales) {
+__global__ __launch_bounds__(1024) void k_quant_int8(const uint16_t *x, long rows, int cols, int8_t *q, float *scales) {
   __shared__ uint32_t red[16];
-  const size_t row = blockIdx.x;
-  const v4i *src = (const v4i *)(x + row * cols);
-  v2u *dst = (v2u *)(q + row * cols);
   const int n = cols / 8, tid = threadIdx.x, step = blockDim.x;
-  v2us mm = {0, 0};
-  v4i v = {0, 0, 0, 0};
-  for (int i = tid; i < n; i += step) {
-    v = src[i];
-    mm = quant_largest(mm, v);
-  }
-  uint32_t m = row16_max(max((uint32_t)mm[0], (uint32_t)mm[1]));
-  m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-  m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-  if (step > 64) {
-    if ((tid & 63) == 0) red[tid >> 6] = m;
-    __syncthreads();
-    m = row16_max((tid & 15) < (step >> 6) ? red[tid & 15] : 0);
-  }
-  const RowScale r = row_scale<TYPE>(m);
-  if (tid == 0) scales[row] = r.scale;
-  for (int i = tid; i < n; i += step) {
-    if (n > step) v = src[i];
-    uint32_t o[2];
-    quant_chunk<TYPE>(v, r.s, r.inv, r.up, o);
-    dst[i] = r.zero ? v2u{0, 0} : v2u{o[0], o[1]};
+  for (size_t row = blockIdx.x; row < (size_t)rows; row += gridDim.x) {
+    const v4i *src = (const v4i *)(x + row * cols);
+    v2u *dst = (v2u *)(q + row * cols);
+    v2us mm = {0, 0};
+    v4i v = {0, 0, 0, 0};
+    for (int i = tid; i < n; i += step) {
+      v = src[i];
+      mm = quant_largest(mm, v);
+    }
+    uint32_t m = row16_max(max((uint32_t)mm[0], (uint32_t)mm[1]));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+    if (step > 64) {
+      __syncthreads();                   // the row before is done with red
+      if ((tid & 63) == 0) red[tid >> 6] = m;
+      __syncthreads();
+      m = row16_max((tid & 15) < (step >> 6) ? red[tid & 15] : 0);
+    }
+    const RowScale r = row_scale<TYPE>(m);
+    if (tid == 0) scales[row] = r.scale;
+    for (int i = tid; i < n; i += step) {
+      if (n > step) v = src[i];
+      uint32_t o[2];
+      quant_chunk<TYPE>(v, r.s, r.inv, r.up, o);
+      dst[i] = r.zero ? v2u{0, 0} : v2u{o[0], o[1]};
+    }
   }
 }
 
@@ -119,44 +123,46 @@ __global__ __launch_bounds__(1024) void k_quant_int8(const uint16_t *x, int cols
 // with a block per row).
 template <int TYPE, int CH>
 __global__ __launch_bounds__(256) void k_quant_int8_rows(const uint16_t *x, long rows, int cols, int8_t *q, float *scales) {
-  const long row = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= rows) return;
   const int n = cols / 8, lane = threadIdx.x & 63;
-  const v4i *src = (const v4i *)(x + row * cols);
-  v2u *dst = (v2u *)(q + row * cols);
-  v4i v[CH];
+  for (long row = (long)blockIdx.x * 4 + (threadIdx.x >> 6); row < rows; row += (long)gridDim.x * 4) {
+    const v4i *src = (const v4i *)(x + row * cols);
+    v2u *dst = (v2u *)(q + row * cols);
+    v4i v[CH];
 #pragma unroll
-  for (int i = 0; i < CH; i++) v[i] = lane + 64 * i < n ? src[lane + 64 * i] : v4i{0, 0, 0, 0};
-  v2us mm = {0, 0};
+    for (int i = 0; i < CH; i++) v[i] = lane + 64 * i < n ? src[lane + 64 * i] : v4i{0, 0, 0, 0};
+    v2us mm = {0, 0};
 #pragma unroll
-  for (int i = 0; i < CH; i++) mm = quant_largest(mm, v[i]);
-  uint32_t m = row16_max(max((uint32_t)mm[0], (uint32_t)mm[1]));
-  m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-  m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-  const RowScale r = row_scale<TYPE>(m);
-  if (lane == 0) scales[row] = r.scale;
+    for (int i = 0; i < CH; i++) mm = quant_largest(mm, v[i]);
+    uint32_t m = row16_max(max((uint32_t)mm[0], (uint32_t)mm[1]));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+    const RowScale r = row_scale<TYPE>(m);
+    if (lane == 0) scales[row] = r.scale;
 #pragma unroll
-  for (int i = 0; i < CH; i++) {
-    if (lane + 64 * i >= n) break;
-    uint32_t o[2];
-    quant_chunk<TYPE>(v[i], r.s, r.inv, r.up, o);
-    dst[lane + 64 * i] = r.zero ? v2u{0, 0} : v2u{o[0], o[1]};
+    for (int i = 0; i < CH; i++) {
+      if (lane + 64 * i >= n) break;
+      uint32_t o[2];
+      quant_chunk<TYPE>(v[i], r.s, r.inv, r.up, o);
+      dst[lane + 64 * i] = r.zero ? v2u{0, 0} : v2u{o[0], o[1]};
+    }
   }
 }
+
+constexpr long kQuantBlocks = 1 << 18;   // a grid holds 2^32 threads at most: longer batches take further turns
 
 template <int TYPE>
 static hipError_t launch_quant(const uint16_t *x, long rows, int cols, int8_t *q, float *scales, hipStream_t s) {
   const int n = cols / 8;
   // enough rows for a wave each to fill the chip
   if (rows >= 1024 && n <= 1024) {
-    const dim3 g((unsigned)((rows + 3) / 4)), t(256);
+    const dim3 g((unsigned)std::min((rows + 3) / 4, kQuantBlocks)), t(256);
     if (n <= 128) hipLaunchKernelGGL((k_quant_int8_rows<TYPE, 2>), g, t, 0, s, x, rows, cols, q, scales);
     else if (n <= 256) hipLaunchKernelGGL((k_quant_int8_rows<TYPE, 4>), g, t, 0, s, x, rows, cols, q, scales);
     else if (n <= 512) hipLaunchKernelGGL((k_quant_int8_rows<TYPE, 8>), g, t, 0, s, x, rows, cols, q, scales);
     else hipLaunchKernelGGL((k_quant_int8_rows<TYPE, 16>), g, t, 0, s, x, rows, cols, q, scales);
   } else {
     const dim3 t(cols >= 8192 ? 1024 : (n + 63) / 64 * 64);
-    hipLaunchKernelGGL(k_quant_int8<TYPE>, dim3((unsigned)rows), t, 0, s, x, cols, q, scales);
+    hipLaunchKernelGGL(k_quant_int8<TYPE>, dim3((unsigned)std::min(rows, kQuantBlocks)), t, 0, s, x, rows, cols, q, scales);
   }
   return hipGetLastError();
 }

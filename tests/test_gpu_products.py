@@ -450,3 +450,110 @@ def test_offsets_beyond_32_bits():
     dw = M.grouped_mm_dw(x, out, first, rows=rows, out_dtype=FP32)   # gathered rows past 4 GiB
     ref, mag = ref_dw(x, out, first, rows)
     assert_product(dw, ref, mag, R)
+
+
+# sizes whose tiles would leave the chip idle: the reduction is split into parts joined by a second launch
+SPLIT = [([70, 0, 200, 31], 264, 4104, 72), ([600], 136, 2600, 2608)]   # counts, N, K of forward, N of dx
+
+
+@pytest.mark.parametrize("counts,N,K,Nx", SPLIT)
+@pytest.mark.parametrize("dtype,out_dtype,gathered", [(BF16, BF16, True), (FP16, FP32, False)])
+def test_split_reductions(counts, N, K, Nx, dtype, out_dtype, gathered):
+    R, E = sum(counts), len(counts)
+    assert M.mm_scratch_bytes(M.MM_FORWARD, E, R, N, K) > 0 and M.mm_scratch_bytes(M.MM_DX, E, R, 2608, N) > 0
+    x, w, _, first, rows = _case(counts, N, K, dtype, gathered, seed=21)
+    out = M.grouped_mm(x, w, first, rows=rows, out_dtype=out_dtype)
+    ref, mag, _ = ref_mm(x, w, first, rows, R)
+    assert_product(out, ref, mag, K, "forward")
+    _, w, dy, first, _ = _case(counts, 2608, N, dtype, False, seed=22)
+    dx = M.grouped_mm_dx(dy, w, first, out_dtype=out_dtype)
+    ref, mag, _ = ref_dx(dy, w, first)
+    assert_product(dx, ref, mag, 2608, "dx")
+
+
+@pytest.mark.parametrize("gathered", [False, True])
+def test_split_weight_gradient_accumulates(gathered):
+    counts, N, K = [5000, 0, 3001], 72, 136
+    R = sum(counts)
+    assert M.mm_scratch_bytes(M.MM_DW, 3, R, N, K) > 0
+    x, _, dy, first, rows = _case(counts, N, K, BF16, gathered, seed=23)
+    ref, mag = ref_dw(dy, x, first, rows)
+    assert_product(M.grouped_mm_dw(dy, x, first, rows=rows), ref, mag, max(counts))
+    base = torch.randn(3, N, K, device="cuda", generator=_gen(24))
+    out = base.clone()
+    M.grouped_mm_dw(dy, x, first, rows=rows, out=out, accumulate=True)
+    assert_product(out, ref + base.double(), mag + base.double().abs(), max(counts) + 1)
+    assert torch.equal(out[1], base[1])
+
+
+def test_split_products_leave_rows_outside_the_groups():
+    counts, start, tail, N, K = [40, 200], 7, 11, 72, 4096
+    R = start + sum(counts) + tail
+    assert M.mm_scratch_bytes(M.MM_FORWARD, 2, R, N, K) > 0
+    g = _gen(25)
+    first = offsets(counts, start).cuda()
+    x, w = _normal(g, R, K), _normal(g, 2, N, K)
+    out = torch.full((R, N), -3.0, dtype=BF16, device="cuda")
+    M.grouped_mm(x, w, first, out=out)
+    ref, mag, cov = ref_mm(x, w, first, None, R)
+    assert_product(out[cov], ref[cov], mag[cov], K)
+    assert bool((out[~cov] == -3).all()) and int((~cov).sum()) == start + tail
+
+
+@pytest.mark.parametrize("rows_given", [False, True])
+def test_split_int8_product(rows_given):
+    g = _gen(26)
+    counts, N, K = [90, 0, 140], 136, 8192
+    R = sum(counts)
+    assert M.mm_scratch_bytes(M.MM_INT8, 3, R, N, K) > 0
+    i8 = lambda *s: torch.randint(-128, 128, s, device="cuda", generator=g, dtype=torch.int8)  # noqa: E731
+    x, w = i8(R, K), i8(3, N, K)
+    xs, ws = torch.rand(R, device="cuda", generator=g), torch.rand(3, N, device="cuda", generator=g) / K
+    rows = torch.randperm(R, device="cuda", generator=g).to(torch.int32) if rows_given else None
+    first = offsets(counts).cuda()
+    for dt in (BF16, FP32):
+        out = M.grouped_int8_mm(x, xs, w, ws, first, rows=rows, out_dtype=dt)
+        assert_int8(out, ref_int8(x, xs, w, ws, first, rows, R)[0])
+
+
+def test_given_scratch_and_its_refusals():
+    counts, N, K = [70, 200], 264, 4104
+    x, w, _, first, _ = _case(counts, N, K, BF16, False, seed=27)
+    need = M.mm_scratch_bytes(M.MM_FORWARD, 2, sum(counts), N, K)
+    want = M.grouped_mm(x, w, first)
+    scratch = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert torch.equal(M.grouped_mm(x, w, first, scratch=scratch), want)
+    with pytest.raises(M.MoeError) as e:
+        M.grouped_mm(x, w, first, scratch=scratch[:need - 16])
+    assert e.value.code == M.MOE_ESCRATCH
+    with pytest.raises(M.MoeError) as e:
+        M.grouped_mm(x, w, first, scratch=torch.empty(need + 16, dtype=torch.uint8, device="cuda")[4:])
+    assert e.value.code == M.MOE_EINVAL
+    with pytest.raises(M.MoeError) as e:                       # contiguous, but not 16-byte aligned
+        M.grouped_mm(torch.empty(270 * K + 8, dtype=BF16, device="cuda")[1:270 * K + 1].view(270, K), w, first)
+    assert e.value.code == M.MOE_EINVAL
+
+
+def test_quantiser_on_more_rows_than_a_grid():
+    """More rows than one grid of either kernel takes: every row of the ends and the turns between."""
+    for rows, cols in ((1100000, 16), (300000, 8208)):
+        x = torch.randn(rows, 16, device="cuda", generator=_gen(rows)).to(BF16).repeat(1, cols // 16)
+        q, s = M.quant_int8(x)
+        for at in (0, 262100, rows - 70):
+            z = slice(at, at + 70)
+            rq, rs = ref_quant(x[z])
+            assert torch.equal(q[z], rq) and torch.equal(s[z], rs)
+        assert torch.equal(s, (x[:, :16].float().abs().amax(1).double() / 127).float())
+
+
+def test_two_products_at_once_on_two_streams():
+    """Overlapping calls with scratch of their own."""
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    x, w, _, first, _ = _case([70, 0, 200], 264, 4104, BF16, False, seed=28)
+    want = M.grouped_mm(x, w, first)
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        outs += [M.grouped_mm(x, w, first, stream=a), M.grouped_mm(x, w, first, stream=b)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
