@@ -39,13 +39,17 @@ __device__ __forceinline__ uint32_t mm_pack(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v2h{(_Float16)lo, (_Float16)hi});
 }
 
-template <int OUT>
+// NT: past the caches' keeping (the weight gradient of 32 groups of 1024 x 6144
+// in fp32: 368 -> 336 us; 16-bit rows, whose lines take two stores a lane, lose:
+// 64 groups of 7168 x 576, 120 -> 262 us).
+template <int OUT, bool NT = false>
 __device__ __forceinline__ void mm_store4(const MmArgs &a, long at, const float *v) {
   if (OUT == MM_FP32) {
     v4f *o = (v4f *)((float *)a.out + at);
     v4f r = v4f{v[0], v[1], v[2], v[3]};
     if (a.accumulate) r += *o;
-    *o = r;
+    if (NT) __builtin_nontemporal_store(r, o);
+    else *o = r;
   } else {
     typedef uint32_t v2u __attribute__((ext_vector_type(2)));
     *(v2u *)((uint16_t *)a.out + at) = v2u{mm_pack<OUT>(v[0], v[1]), mm_pack<OUT>(v[2], v[3])};
@@ -59,8 +63,9 @@ __device__ __forceinline__ void mm_store8(const MmArgs &a, long at, const float 
     mm_store4<OUT>(a, at + 4, v + 4);
   } else {
     typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-    *(v4u *)((uint16_t *)a.out + at) = v4u{mm_pack<OUT>(v[0], v[1]), mm_pack<OUT>(v[2], v[3]), mm_pack<OUT>(v[4], v[5]),
-                                           mm_pack<OUT>(v[6], v[7])};
+    const v4u r = v4u{mm_pack<OUT>(v[0], v[1]), mm_pack<OUT>(v[2], v[3]), mm_pack<OUT>(v[4], v[5]),
+                      mm_pack<OUT>(v[6], v[7])};
+    *(v4u *)((uint16_t *)a.out + at) = r;
   }
 }
 
@@ -134,7 +139,7 @@ struct MmTile {
 // bound, whose surplus blocks would all land on the last XCD), and inside it
 // kMmGroup row tiles share each column tile of the weights before the next one
 // is read.  Every wave does the same work: no barrier.
-constexpr int kMmGroup = 4;
+constexpr int kMmGroup = 8;
 
 template <int BQ>
 __device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile &t) {
@@ -454,7 +459,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   }
   mm_by_output(a.splits > 1 ? MM_PART : a.out_type, [&](auto out) {
     constexpr int OUT = decltype(out)::value;
-    constexpr bool WIDE = OUT == MM_FP32 || OUT == MM_PART;
+    constexpr bool WIDE = OUT == MM_FP32 || OUT == MM_PART, NT = OP == MM_DW && OUT == MM_FP32;
 #pragma unroll
     for (int i0 = 0; i0 < NP; i0 += 4) {
       const int pc = p0 + wp * TP + 16 * i0, p = pc + 16 * g;
@@ -494,7 +499,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
         } else if (OUT == MM_FP32) {
 #pragma unroll
           for (int i = 0; i < 4; i++)
-            if (pc + 16 * i + 4 * g < pn) mm_store4<OUT>(a, at + pc + 16 * i + 4 * g, v + 4 * i);
+            if (pc + 16 * i + 4 * g < pn) mm_store4<OUT, NT>(a, at + pc + 16 * i + 4 * g, v + 4 * i);
         } else {
 #pragma unroll
           for (int k = 0; k < 16; k += 8)
@@ -719,7 +724,7 @@ MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
   const long pn = op == MM_FORWARD ? N : K, qn = op == MM_DW ? N : R, outs = op == MM_DW ? E * N : R;
   // Few rows a group: the weights pass once, and 16 of their rows a block.  Short
   // reductions leave its waves without work (125 groups of 5 rows, K = 64: 74 us,
-  // TODO us in tiles); many rows read the weights again for every 16, which only
+  // 14 us in tiles); many rows read the weights again for every 16, which only
   // pays while tiles would leave most of the chip idle.
   if (op == MM_FORWARD && K * item >= 512) {
     const long tiles16 = ((R + 15) / 16 + (E > 1 ? groups : 0)) * ((N + 15) / 16);
