@@ -366,7 +366,7 @@ def _bind():
 def _use(stream, t):
     """Makes `stream` current for a call on operand t, so that the tensors made there belong to it too."""
     import torch
-    if t is not None and t.device.type == "cuda" and stream.device != t.device:
+    if torch.is_tensor(t) and t.device.type == "cuda" and stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, the operands on {t.device}")
     return torch.cuda.stream(stream)
 
@@ -377,7 +377,8 @@ def mm_scratch_bytes(op: int, E: int, R: int, N: int, K: int) -> int:
 
 
 # The products below check types, shapes, contiguity and device of every tensor, make the outputs and the
-# scratch that are not given, and run on `stream` or on the current stream of the operands' device.
+# scratch that are not given, and run on `stream` or on the current stream of the operands' device. autograd
+# does not record them: a training step calls the gradients itself.
 
 
 def grouped_mm(x, w, first, rows=None, out=None, out_dtype=None, scratch=None, stream=None):

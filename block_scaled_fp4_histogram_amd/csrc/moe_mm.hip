@@ -39,21 +39,26 @@ __device__ __forceinline__ uint32_t mm_pack(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v2h{(_Float16)lo, (_Float16)hi});
 }
 
-// NT: past the caches' keeping (the weight gradient of 32 groups of 1024 x 6144
-// in fp32: 368 -> 336 us; 16-bit rows, whose lines take two stores a lane, lose:
-// 64 groups of 7168 x 576, 120 -> 262 us).
-template <int OUT, bool NT = false>
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+// NT: past the caches' keeping.
+template <bool NT, typename V>
+__device__ __forceinline__ void mm_store(V *o, V v) {
+  if (NT) __builtin_nontemporal_store(v, o);
+  else *o = v;
+}
+
+template <bool NT = false>
+__device__ __forceinline__ void mm_store_f32(const MmArgs &a, long at, v4f r) {
+  v4f *o = (v4f *)((float *)a.out + at);
+  if (a.accumulate) r += *o;
+  mm_store<NT>(o, r);
+}
+
+template <int OUT>
 __device__ __forceinline__ void mm_store4(const MmArgs &a, long at, const float *v) {
-  if (OUT == MM_FP32) {
-    v4f *o = (v4f *)((float *)a.out + at);
-    v4f r = v4f{v[0], v[1], v[2], v[3]};
-    if (a.accumulate) r += *o;
-    if (NT) __builtin_nontemporal_store(r, o);
-    else *o = r;
-  } else {
-    typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-    *(v2u *)((uint16_t *)a.out + at) = v2u{mm_pack<OUT>(v[0], v[1]), mm_pack<OUT>(v[2], v[3])};
-  }
+  if (OUT == MM_FP32) mm_store_f32(a, at, v4f{v[0], v[1], v[2], v[3]});
+  else *(v2u *)((uint16_t *)a.out + at) = v2u{mm_pack<OUT>(v[0], v[1]), mm_pack<OUT>(v[2], v[3])};
 }
 
 template <int OUT>
@@ -168,7 +173,8 @@ __device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile
   const int total = uniform(__shfl(sum, 63)), nt = total * ptiles;
   const int chunk = (nt + 7) >> 3, b = (int)blockIdx.x;
   const int id = (b & 7) * chunk + (b >> 3);
-  if ((b >> 3) >= chunk || id >= nt) return false;
+  // (a total below zero: offsets that fall, whose groups overlap past 2^31 tiles)
+  if (total <= 0 || (b >> 3) >= chunk || id >= nt) return false;
   const int grp = id / (kMmGroup * ptiles), rem = id - grp * kMmGroup * ptiles;
   const int gcur = min(kMmGroup, total - grp * kMmGroup);
   t.pt = rem / gcur;
@@ -185,30 +191,6 @@ __device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile
   t.row0 = uniform(__shfl(lo, at) + k * BQ);
   t.rows = min(BQ, uniform(__shfl(hi, at)) - t.row0);
   return t.rows > 0;
-}
-
-// Exchanges, among the four lanes l, l + 16, l + 32, l + 48, element 4 i + k of
-// lane group g with element 4 g + k of lane group i: two rounds of row swaps.
-__device__ __forceinline__ void swap_columns(float *v) {
-  typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-#pragma unroll
-  for (int k = 0; k < 4; k++) {
-    uint32_t r[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) r[i] = __float_as_uint(v[4 * i + k]);
-#pragma unroll
-    for (int i = 0; i < 2; i++) {        // upper half of element i with the lower half of i + 2
-      const v2u t = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane32_swap(r[i], r[i + 2], false, false));
-      r[i] = t[0], r[i + 2] = t[1];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {     // odd rows of 16 of element i with the even ones of i + 1
-      const v2u t = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane16_swap(r[i], r[i + 1], false, false));
-      r[i] = t[0], r[i + 1] = t[1];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i++) v[4 * i + k] = __uint_as_float(r[i]);
-  }
 }
 
 // Row of x behind product row r, or -1.
@@ -248,6 +230,8 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   static_assert(TP % 64 == 0 && TQ % 16 == 0 && CQ >= 1 && CP >= 1, "tile shape");
   static_assert(!TQ_T || (BQ % 128 == 0 && TQ % 64 == 0), "transposed Q");
   static_assert(!TP_T || BP % 128 == 0, "transposed P");
+  constexpr int kOutStage = 16 * (64 * 4 + 16);                 // of one wave, for its outputs
+  static_assert(NW * kOutStage <= kStage, "outputs through LDS");
   __shared__ __align__(1024) uint8_t lds[kStage];
 
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
@@ -457,12 +441,29 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       xs[j] = xr < 0 ? 0.f : a.x_scales[xr];
     }
   }
+  // Sixteen rows of 64 columns at a time go through the wave's own part of LDS, so
+  // that a store writes whole rows of them (four of 256 bytes, eight of 128): 16
+  // bytes of each of 16 rows in every quarter wave, as the accumulators lie, cost
+  // a fp32 weight gradient of 64 x 7168 x 576 328 us for 195 us (5.4 TB/s), one in
+  // 16 bits 150 for 122.  Weight gradients, which are read much later, are stored
+  // past the caches: another 210 -> 195 us and 122 -> 87 us there; the other
+  // products' rows, which the next kernel reads, gain 0 to 3 % and stay.
+  mm_barrier();                          // every wave has read its last fragments
+  uint8_t *mine = lds + w * kOutStage;
+  auto fence = [] {                      // LDS accesses of a wave are in order: for the compiler only
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  };
   mm_by_output(a.splits > 1 ? MM_PART : a.out_type, [&](auto out) {
     constexpr int OUT = decltype(out)::value;
-    constexpr bool WIDE = OUT == MM_FP32 || OUT == MM_PART, NT = OP == MM_DW && OUT == MM_FP32;
+    constexpr bool WIDE = OUT == MM_FP32 || OUT == MM_PART, NT = OP == MM_DW && OUT != MM_PART;
+    constexpr int RB = WIDE ? 64 * 4 + 16 : 64 * 2 + 16;   // a row, and 16 bytes that spread the rows over the banks
+    constexpr int LR = WIDE ? 16 : 8, CW = 64 / LR;        // lanes a row, columns a lane
+    const long outs = OP == MM_DW ? (long)a.E * a.N : (long)a.R;
+    float *part = a.part + (OUT == MM_PART ? (long)blockIdx.y * outs * pn : 0);
 #pragma unroll
     for (int i0 = 0; i0 < NP; i0 += 4) {
-      const int pc = p0 + wp * TP + 16 * i0, p = pc + 16 * g;
+      const int pc = p0 + wp * TP + 16 * i0, p = pc + 16 * g, po = pc + CW * (lane % LR);
       float ws[TYPE == MM_I8 ? 16 : 1];
       if constexpr (TYPE == MM_I8) {
 #pragma unroll
@@ -470,40 +471,30 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < NQ; j++) {
-        const int q = wq * TQ + 16 * j + l16;
-        if (q >= qn) continue;
-        float v[16];
+        fence();
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < 4; i++) {
+          float v[4];
 #pragma unroll
           for (int k = 0; k < 4; k++) {
             const auto e = acc[i0 + i][j][k];
-            v[4 * i + k] = OUT == MM_PART ? __builtin_bit_cast(float, e) : (float)e;
+            v[k] = OUT == MM_PART ? __builtin_bit_cast(float, e) : (float)e;
+            if constexpr (TYPE == MM_I8 && OUT != MM_PART) v[k] *= xs[j] * ws[4 * i + k];
           }
-        if constexpr (TYPE == MM_I8 && OUT != MM_PART) {
-#pragma unroll
-          for (int k = 0; k < 16; k++) v[k] *= xs[j] * ws[k];
+          uint8_t *o = mine + l16 * RB + (TP_T ? 16 * i + 4 * g : 16 * g + 4 * i) * (WIDE ? 4 : 2);
+          if constexpr (WIDE) *(v4f *)o = v4f{v[0], v[1], v[2], v[3]};
+          else *(v2u *)o = v2u{mm_pack<OUT>(v[0], v[1]), mm_pack<OUT>(v[2], v[3])};
         }
-        // 16 bits: 16 consecutive columns a lane, 32 bits: columns 16 i + 4 g + k with lane
-        // group g, so that four lanes' 16 bytes meet; the lane groups trade for the other
-        // of the two (64-byte pieces a lane cost the weight gradient 432 us for 381 us)
-        if (TP_T == !WIDE) swap_columns(v);
-        const long at = (orow + q) * pn;
-        if (OUT == MM_PART) {
-          const long outs = OP == MM_DW ? (long)a.E * a.N : (long)a.R;
-          float *o = a.part + ((long)blockIdx.y * outs * pn + at);
+        fence();
 #pragma unroll
-          for (int i = 0; i < 4; i++)
-            if (pc + 16 * i + 4 * g < pn)
-              *(v4f *)(o + pc + 16 * i + 4 * g) = v4f{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-        } else if (OUT == MM_FP32) {
-#pragma unroll
-          for (int i = 0; i < 4; i++)
-            if (pc + 16 * i + 4 * g < pn) mm_store4<OUT, NT>(a, at + pc + 16 * i + 4 * g, v + 4 * i);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 16; k += 8)
-            if (p + k < pn) mm_store8<OUT>(a, at + p + k, v + k);
+        for (int r = 0; r < 16; r += 64 / LR) {
+          const int row = r + lane / LR, q = wq * TQ + 16 * j + row;
+          const v4i d = *(const v4i *)(mine + row * RB + (lane % LR) * 16);
+          if (q >= qn || po >= pn) continue;
+          const long at = (orow + q) * pn + po;
+          if constexpr (OUT == MM_PART) *(v4i *)(part + at) = d;
+          else if constexpr (OUT == MM_FP32) mm_store_f32<NT>(a, at, __builtin_bit_cast(v4f, d));
+          else mm_store<NT>((v4i *)((uint16_t *)a.out + at), d);
         }
       }
     }
@@ -722,13 +713,18 @@ MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
   MmPlan m = {0, 0, 1, 0};
   const long item = type == MM_I8 ? 1 : 2, groups = E < R ? E : R;
   const long pn = op == MM_FORWARD ? N : K, qn = op == MM_DW ? N : R, outs = op == MM_DW ? E * N : R;
-  // Few rows a group: the weights pass once, and 16 of their rows a block.  Short
-  // reductions leave its waves without work (125 groups of 5 rows, K = 64: 74 us,
-  // 14 us in tiles); many rows read the weights again for every 16, which only
-  // pays while tiles would leave most of the chip idle.
-  if (op == MM_FORWARD && K * item >= 512) {
+  // Few rows a group: the weights pass once, 16 of their rows a block.  Short rows
+  // make for blocks that mostly start and end (64 groups of 5 rows, N = 1024:
+  // K = 512 in 21.0 us, in tiles 16.2; K = 2048 in 53.0, in tiles 58.4), which
+  // costs nothing while tiles would leave most of the chip idle (64 groups of 8,
+  // N = 256, K = 512: 6.4, 8.5 us).  Up to there more rows stream too, though
+  // every 16 read the weights again (R = 64, N = 2048, K = 7168: 13.3, 17.6 us;
+  // R = 128, N = 512, K = 2048: 5.8, 12.3; 8 groups of 24, N = 2048, K = 7168:
+  // 68.2, 54.7).
+  if (op == MM_FORWARD) {
     const long tiles16 = ((R + 15) / 16 + (E > 1 ? groups : 0)) * ((N + 15) / 16);
-    if (tiles16 < 1l << 23 && (R <= 8 * E || R <= 16 || (R <= 64 * E && tiles16 <= 2048))) {
+    const bool few = (R <= 8 * E || R <= 16) && K * item >= 4096 && tiles16 < 1l << 23;
+    if (few || (R <= 64 * E && tiles16 <= 2048) || (R <= 128 && tiles16 <= 1024)) {
       m.stream = 1;
       return m;
     }
@@ -747,21 +743,27 @@ MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
     const float cost = (float)((n + slots - 1) / slots * s.occ) * (float)(s.bq * s.bp) * s.weight;
     if (!tiles || cost < least) m.shape = i, least = cost, tiles = n;
   }
-  // short weight gradients write more than they read: more blocks to store
-  if (op == MM_DW && R < 128 * E) m.shape = 2;
-  // Too few tiles for the chip: the reduction is split, and the parts joined in
-  // order by a second launch.
+  // Short weight gradients write more than they read, and more blocks store better
+  // (64 groups of 32 rows, 576 x 7168: 105 us, 118 in 256 x 128; 16 groups of 256,
+  // 2048 x 2048: 45, 50; but 32 groups of 512, 1024 x 6144: 282, 251).
+  if (op == MM_DW && R <= 256 * E) m.shape = 2;
+  // Too few tiles for the chip: the reduction is split into as many parts as take
+  // least time.  A step takes 0.6 us (1 us with transposed reads of both operands),
+  // all blocks' steps what their loads take at 12 TB/s; the second launch, which
+  // joins the parts in order, 4 us, and their bytes twice at 4 TB/s (R = 256,
+  // N = 1024, K = 4096: 15.2 us, 41.3 us whole; int8, R = 500, N = 4608, K = 7168:
+  // 45.4 us in parts that fill the chip, 39.6 whole).
+  const auto &shape = kMmShapes[m.shape];
   const long steps = op == MM_FORWARD ? K * item / 128 : op == MM_DX ? N / 64 : R / E / 64;
-  const long slots = 256l * kMmShapes[m.shape].occ;
-  if (tiles * 2 <= slots && steps >= 32) {
-    long splits = slots / tiles;
-    if (splits > steps / 8) splits = steps / 8;
-    if (splits > 16) splits = 16;
-    if (splits > 1) {
-      m.splits = (int)splits;
-      m.scratch = (size_t)splits * outs * pn * 4;
-    }
+  const float step = op == MM_DW ? 1.0f : 0.6f;
+  const float feed = (float)(tiles * steps * (shape.bq + shape.bp)) * (128 / 12e6f);
+  float best = steps * step > feed ? steps * step : feed;
+  for (long n = 2; n <= 16 && n * tiles <= 256l * shape.occ; n++) {
+    const float run = (float)((steps + n - 1) / n) * step;
+    const float us = (run > feed ? run : feed) + 4.0f + (float)(n * outs * pn) * 2e-6f;
+    if (us < best) best = us, m.splits = (int)n;
   }
+  if (m.splits > 1) m.scratch = (size_t)m.splits * outs * pn * 4;
   return m;
 }
 

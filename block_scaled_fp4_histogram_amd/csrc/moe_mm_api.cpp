@@ -3,6 +3,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <initializer_list>
+
 #include "moe.h"
 #include "moe_common.h"
 #include "moe_mm.h"
@@ -26,6 +28,8 @@ int launched(hipError_t e, const char *what) {
 
 // Longest row (elements) of the products: a tile's rows stay within 32-bit byte offsets.
 constexpr int kMmMaxDim = 1 << 20;
+// Most rows: row numbers a tile past the last one stay within 32 bits.
+constexpr int kMmMaxRows = 1 << 30;
 // Longest int8 reduction: (-128)^2 a term in a 32-bit sum.
 constexpr int kI8MaxK = 131056;
 
@@ -37,6 +41,7 @@ int check_shape(const char *fn, int unit, const int32_t *first, int E, int R, in
   if (E > moe::kMaxExperts) return fail(MOE_EUNSUPPORTED, "%s: E=%d above %d", fn, E, moe::kMaxExperts);
   if (N % 8 || K % unit) return fail(MOE_EUNSUPPORTED, "%s: N=%d must be a multiple of 8, K=%d of %d", fn, N, K, unit);
   if (N > kMmMaxDim || K > kMmMaxDim) return fail(MOE_EUNSUPPORTED, "%s: N=%d or K=%d above %d", fn, N, K, kMmMaxDim);
+  if (R > kMmMaxRows) return fail(MOE_EUNSUPPORTED, "%s: R=%d above %d", fn, R, kMmMaxRows);
   return MOE_OK;
 }
 
@@ -66,6 +71,28 @@ int check_scratch(const char *fn, int op, int E, int R, int N, int K, const void
   return MOE_OK;
 }
 
+// Buffers of a call: what it writes overlaps neither what it reads nor each other.
+struct Span {
+  const void *p;
+  size_t bytes;
+};
+
+int check_apart(const char *fn, std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  auto meet = [](const Span &a, const Span &b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x && y && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (const Span *w = written.begin(); w != written.end(); w++) {
+    for (const Span &r : read)
+      if (meet(*w, r)) return fail(MOE_EINVAL, "%s: an output or the scratch overlaps an input", fn);
+    for (const Span *v = written.begin(); v != w; v++)
+      if (meet(*w, *v)) return fail(MOE_EINVAL, "%s: outputs or the scratch overlap", fn);
+  }
+  return MOE_OK;
+}
+
+size_t type_size(int dtype) { return dtype == MOE_T_FP32 ? 4 : 2; }
+
 }  // namespace
 
 #define TRY(expr)              \
@@ -92,9 +119,12 @@ int moe_grouped_mm(int dtype, const void *x, long long x_rows, const int32_t *ro
   TRY(check_rows(fn, rows, x_rows, R));
   if (R == 0) return MOE_OK;
   if (!first) return fail(MOE_EINVAL, "%s: null first", fn);
-  const void *p[] = {x, w, out};
-  TRY(check_ptrs(fn, p, 3));
+  const void *p[] = {w, out, x};   // an x without rows is not read
+  TRY(check_ptrs(fn, p, x_rows ? 3 : 2));
   TRY(check_scratch(fn, MOE_MM_FORWARD, E, R, N, K, scratch, scratch_bytes));
+  TRY(check_apart(fn, {{out, (size_t)R * N * type_size(out_dtype)}, {scratch, scratch_bytes}},
+                  {{x, (size_t)x_rows * K * 2}, {w, (size_t)E * N * K * 2}, {first, (E + 1) * sizeof *first},
+                   {rows, R * sizeof *rows}}));
   moe::MmArgs a = {};
   a.part = (float *)scratch;
   a.op = moe::MM_FORWARD, a.type = dtype, a.out_type = out_dtype;
@@ -113,6 +143,8 @@ int moe_grouped_mm_dx(int dtype, const void *dy, const void *w, const int32_t *f
   const void *p[] = {dy, w, dx};
   TRY(check_ptrs(fn, p, 3));
   TRY(check_scratch(fn, MOE_MM_DX, E, R, N, K, scratch, scratch_bytes));
+  TRY(check_apart(fn, {{dx, (size_t)R * K * type_size(out_dtype)}, {scratch, scratch_bytes}},
+                  {{dy, (size_t)R * N * 2}, {w, (size_t)E * N * K * 2}, {first, (E + 1) * sizeof *first}}));
   moe::MmArgs a = {};
   a.part = (float *)scratch;
   a.op = moe::MM_DX, a.type = dtype, a.out_type = out_dtype;
@@ -131,8 +163,11 @@ int moe_grouped_mm_dw(int dtype, const void *dy, const void *x, long long x_rows
   TRY(check_rows(fn, rows, x_rows, R));
   if (!first) return fail(MOE_EINVAL, "%s: null first", fn);
   const void *p[] = {dw, dy, x};   // without rows dy and x are not read
-  TRY(check_ptrs(fn, p, R ? 3 : 1));
+  TRY(check_ptrs(fn, p, R == 0 ? 1 : x_rows ? 3 : 2));
   TRY(check_scratch(fn, MOE_MM_DW, E, R, N, K, scratch, scratch_bytes));
+  TRY(check_apart(fn, {{dw, (size_t)E * N * K * type_size(out_dtype)}, {scratch, scratch_bytes}},
+                  {{dy, (size_t)R * N * 2}, {x, (size_t)x_rows * K * 2}, {first, (E + 1) * sizeof *first},
+                   {rows, R * sizeof *rows}}));
   moe::MmArgs a = {};
   a.part = (float *)scratch;
   a.op = moe::MM_DW, a.type = dtype, a.out_type = out_dtype, a.accumulate = accumulate;
@@ -150,6 +185,7 @@ int moe_quant_int8(int dtype, const void *x, int rows, int cols, int8_t *q, floa
   const void *p[] = {x, q};
   TRY(check_ptrs(fn, p, 2));
   if (!scales || !aligned(scales, 4)) return fail(MOE_EINVAL, "%s: null or misaligned scales", fn);
+  TRY(check_apart(fn, {{q, (size_t)rows * cols}, {scales, rows * sizeof *scales}}, {{x, (size_t)rows * cols * 2}}));
   return launched(moe::launch_quant_int8(dtype, x, rows, cols, q, scales, (hipStream_t)stream), fn);
 }
 
@@ -164,11 +200,15 @@ int moe_grouped_int8_mm(const int8_t *x, const float *x_scales, long long x_rows
   if (K > kI8MaxK) return fail(MOE_EUNSUPPORTED, "%s: K=%d above %d (32-bit sums)", fn, K, kI8MaxK);
   if (!first && E != 1) return fail(MOE_EINVAL, "%s: null first", fn);
   if (R == 0) return MOE_OK;
-  const void *p[] = {x, w, out};
-  TRY(check_ptrs(fn, p, 3));
-  if (!x_scales || !w_scales || !aligned(x_scales, 4) || !aligned(w_scales, 4))
+  const void *p[] = {w, out, x};   // an x without rows is not read
+  TRY(check_ptrs(fn, p, x_rows ? 3 : 2));
+  if ((!x_scales && x_rows) || !w_scales || !aligned(x_scales, 4) || !aligned(w_scales, 4))
     return fail(MOE_EINVAL, "%s: null or misaligned scales", fn);
   TRY(check_scratch(fn, MOE_MM_INT8, E, R, N, K, scratch, scratch_bytes));
+  TRY(check_apart(fn, {{out, (size_t)R * N * type_size(out_dtype)}, {scratch, scratch_bytes}},
+                  {{x, (size_t)x_rows * K}, {x_scales, x_rows * sizeof *x_scales}, {w, (size_t)E * N * K},
+                   {w_scales, (size_t)E * N * sizeof *w_scales}, {first, (E + 1) * sizeof *first},
+                   {rows, R * sizeof *rows}}));
   moe::MmArgs a = {};
   a.part = (float *)scratch;
   a.op = moe::MM_FORWARD, a.type = moe::MM_I8, a.out_type = out_dtype;
@@ -202,6 +242,9 @@ int moe_group_routes(const int32_t *topk_ids, int T, int top_k, int E, int32_t *
   const size_t need = moe_group_routes_scratch_bytes(T, top_k, E);
   if (need && (!scratch || !aligned(scratch, 4))) return fail(MOE_EINVAL, "%s: null or misaligned scratch", fn);
   if (scratch_bytes < need) return fail(MOE_ESCRATCH, "%s: scratch holds %zu bytes, %zu needed", fn, scratch_bytes, need);
+  const size_t ids_bytes = (size_t)T * top_k * sizeof *topk_ids;
+  TRY(check_apart(fn, {{first, (E + 1) * sizeof *first}, {order, ids_bytes}, {token, ids_bytes}, {inverse, ids_bytes},
+                       {scratch, scratch_bytes}}, {{topk_ids, ids_bytes}}));
   moe::GroupArgs a = {};
   a.ids = topk_ids, a.R = T * top_k, a.topk = top_k, a.E = E;
   if (need) a.rounds = moe::group_rounds(a.R), a.blocks = moe::group_blocks(a.R);

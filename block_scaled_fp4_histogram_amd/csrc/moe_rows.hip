@@ -154,7 +154,7 @@ template <int TYPE>
 static hipError_t launch_quant(const uint16_t *x, long rows, int cols, int8_t *q, float *scales, hipStream_t s) {
   const int n = cols / 8;
   // enough rows for a wave each to fill the chip
-  if (rows >= 1024 && n <= 1024) {
+  if (rows >= 4096 && n <= 1024) {
     const dim3 g((unsigned)std::min((rows + 3) / 4, kQuantBlocks)), t(256);
     if (n <= 128) hipLaunchKernelGGL((k_quant_int8_rows<TYPE, 2>), g, t, 0, s, x, rows, cols, q, scales);
     else if (n <= 256) hipLaunchKernelGGL((k_quant_int8_rows<TYPE, 4>), g, t, 0, s, x, rows, cols, q, scales);

@@ -338,9 +338,11 @@ int moe_plan_set_activation(moe_plan_t plan, int act);
  * outside [0, x_rows) stands for a row of zeros.  NULL: row r of x itself.
  *
  * Matrices are row-major and contiguous, 16-byte aligned; N and K are
- * multiples of 8 (K of 16 for the integer products) up to 2^20, E 1 .. 1024.
- * Sums are kept in fp32 (exact int32 for integers) and rounded once, to
- * nearest even, on output.  No kernel uses atomics: results repeat bit for bit.
+ * multiples of 8 (K of 16 for the integer products) up to 2^20, E 1 .. 1024,
+ * R up to 2^30.  What a call writes may not overlap what it reads; an x of no
+ * rows may be NULL.  Sums are kept in fp32 (exact int32 for integers) and
+ * rounded once, to nearest even, on output.  Every sum has a fixed order:
+ * results repeat bit for bit.
  * All calls are stream-ordered, neither allocate nor synchronise, and may be
  * captured in a HIP graph.  They work in `scratch` (device, 16-byte aligned,
  * at least moe_mm_scratch_bytes of the call's op and sizes; NULL when that is

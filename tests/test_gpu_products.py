@@ -557,3 +557,27 @@ def test_two_products_at_once_on_two_streams():
         outs += [M.grouped_mm(x, w, first, stream=a), M.grouped_mm(x, w, first, stream=b)]
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("R,N,K", [(5, 72, 272), (200, 72, 272), (200, 136, 40)])
+def test_x_without_rows(R, N, K):
+    """Every product row then names no row: zeros, also where each kernel of the forward product runs."""
+    first, rows = offsets([R // 2, R - R // 2]).cuda(), torch.full((R,), -1, dtype=torch.int32, device="cuda")
+    x, w = torch.empty(0, K, dtype=BF16, device="cuda"), _normal(_gen(5), 2, N, K)
+    out = M.grouped_mm(x, w, first, rows=rows, out=torch.full((R, N), 7.0, dtype=BF16, device="cuda"))
+    assert not out.any()
+    dw = M.grouped_mm_dw(_normal(_gen(6), R, N), x, first, rows=rows)
+    assert not dw.any()
+    if K % 16 == 0:
+        wq, ws = M.quant_int8(w.view(2 * N, K))
+        out = M.grouped_int8_mm(x.to(torch.int8), torch.empty(0, device="cuda"), wq.view(2, N, K), ws.view(2, N), first,
+                                rows=rows, out=torch.full((R, N), 7.0, dtype=BF16, device="cuda"))
+        assert not out.any()
+
+
+def test_output_over_an_input_is_refused():
+    x, w, first = _normal(_gen(7), 64, 64), _normal(_gen(8), 2, 64, 64), offsets([30, 34]).cuda()
+    for call in (lambda: M.grouped_mm(x, w, first, out=x), lambda: M.grouped_mm_dx(x, w, first, out=x),
+                 lambda: M.grouped_mm_dw(x, x, first, out=w[:, :, :], rows=w.view(-1).view(torch.int32)[:64])):
+        with pytest.raises(M.MoeError, match="overlap"):
+            call()

@@ -116,3 +116,25 @@ def test_binding_checks():
         with pytest.raises(exc) as ei:
             call()
         assert text in str(ei.value), str(ei.value)
+
+
+def test_overlapping_buffers_are_refused():
+    """64 rows of 64 bf16 values are 8192 bytes; four experts of 64 x 64, 32768."""
+    L = _lib.load()
+    far = lambda i: P + (i << 20)  # noqa: E731
+    big = (1 << 30) + 1
+    assert _mm(L, x=far(0), w=far(1), first=far(2), out=far(0) + 8176) == M.MOE_EINVAL
+    assert b"overlaps an input" in L.moe_last_error()
+    assert _mm(L, x=far(0), w=far(1), first=far(2), out=far(1) + 32752) == M.MOE_EINVAL
+    assert _mm(L, x=far(0), w=far(1), first=far(2), out=far(2) - 8176) == M.MOE_EINVAL
+    assert _mm(L, x=far(0), w=far(1), first=far(2), rows=far(3) + 252, out=far(3)) == M.MOE_EINVAL
+    assert _mm(L, x=far(0), w=far(1), first=far(2), out=far(3), R=big, x_rows=big) == M.MOE_EUNSUPPORTED
+    assert L.moe_grouped_mm_dx(M.T_BF16, far(0), far(1), far(2), 4, 64, 64, 64, M.T_BF16, far(0), None, 0, None) == M.MOE_EINVAL
+    assert L.moe_grouped_mm_dw(M.T_BF16, far(0), far(1), 64, None, far(2), 4, 64, 64, 64, M.T_FP32, 0, far(1) - 65536 + 16,
+                               None, 0, None) == M.MOE_EINVAL
+    assert L.moe_quant_int8(M.T_BF16, far(0), 64, 64, far(0), far(1), None) == M.MOE_EINVAL
+    assert L.moe_quant_int8(M.T_BF16, far(0), 64, 64, far(1), far(1) + 4092, None) == M.MOE_EINVAL
+    assert b"outputs" in L.moe_last_error()
+    assert L.moe_int8_mm(far(0), far(1), far(2), far(3), 64, 64, 64, M.T_BF16, far(3) + 240, None, 0, None) == M.MOE_EINVAL
+    assert L.moe_group_routes(far(0), 8, 2, 4, far(1), far(0) + 60, far(2), far(3), None, 0, None) == M.MOE_EINVAL
+    assert L.moe_group_routes(far(0), 8, 2, 4, far(1), far(2), far(2), far(3), None, 0, None) == M.MOE_EINVAL
