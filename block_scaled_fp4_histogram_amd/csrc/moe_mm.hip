@@ -143,7 +143,8 @@ struct MmTile {
 // takes the i-th eighth of the tiles that exist (not of the launch's upper
 // bound, whose surplus blocks would all land on the last XCD), and inside it
 // kMmGroup row tiles share each column tile of the weights before the next one
-// is read.  Every wave does the same work: no barrier.
+// is read (16384 x 4096 x 4096 with 1, 4, 8 and 16: 485, 428, 431, 462 us; eight
+// groups' row gradient of that size: 488, 505, 497, 530).  Every wave does the same work: no barrier.
 constexpr int kMmGroup = 8;
 
 template <int BQ>
@@ -226,7 +227,6 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   constexpr int TQ = BQ / WQ, TP = BP / WP, NQ = TQ / 16, NP = TP / 16;
   constexpr int CQ = BQ / 8 / NW, CP = BP / 8 / NW;             // loads of 1 KB a wave and step
   constexpr int kStage = (BQ + BP) * 128;
-  constexpr bool HALF = OP == MM_DW || GATHER;
   static_assert(TP % 64 == 0 && TQ % 16 == 0 && CQ >= 1 && CP >= 1, "tile shape");
   static_assert(!TQ_T || (BQ % 128 == 0 && TQ % 64 == 0), "transposed Q");
   static_assert(!TP_T || BP % 128 == 0, "transposed P");
@@ -386,12 +386,14 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   // One stage of LDS: the next step's tiles are loaded once every wave has this
   // one's fragments in registers, and the other blocks of the CU (two or three,
   // by registers and LDS) multiply while they arrive and while this one stores.
-  // A second stage in its place leaves room for fewer or smaller blocks:
-  // 16382 x 4096 x 4096 in 585 us (256 x 256, eight waves, one block a CU, which
-  // spends a tenth of a tile on its start and end) against 576 us (256 x 128,
-  // two blocks); 32 experts' row gradient 315 -> 271 us.
-  // The weight gradient's transposed reads take more registers, so its first
-  // half multiplies before the second is read (256 x 128: 380 us, spilled 643 us).
+  // A second stage in its place leaves room for fewer or smaller blocks and was
+  // slower: 16382 x 4096 x 4096 by 2 % (256 x 256, eight waves, one block a CU,
+  // which spends a tenth of a tile on its start and end), 32 experts' row gradient
+  // by 16 %.
+  // Gathered rows' numbers take more registers, so the first half then multiplies
+  // before the second is read (weight gradient of 32 groups, 1024 x 6144: 269 us,
+  // 295 the other way; int8 prefill 671, 770; rows in order win by up to 5 % with
+  // both halves read at once: eight groups of 2048 rows, 4096 x 4096, 529, 558).
   if (begin < steps) {
     gather_rows(begin);
     load(begin);
@@ -415,7 +417,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
         for (int i = 0; i < NP; i++) acc[i][j] = M::mma(fp[h][i], fq[h][j], acc[i][j]);
     };
     read(0);
-    if (HALF) {
+    if (GATHER) {
       mul(0);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -426,7 +428,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       load(s + 1);
       gather_rows(s + 2);
     }
-    if (!HALF) mul(0);
+    if (!GATHER) mul(0);
     mul(1);
   }
 
@@ -704,7 +706,8 @@ static hipError_t launch_stream(const MmArgs &a, hipStream_t s) {
 //
 // Tile shapes, all of four waves, and the blocks of each that a CU holds; weight:
 // what covering an output element costs beside 256 x 128 once the chip is full
-// (16382 x 4096 x 4096: 576, 598 and 636 us for the first three).
+// (16384 x 4096 x 4096, over one and 32 groups: 435, 432, 481, 616 us and 517, 494,
+// 572, 697 us).
 enum { kShapes = 4 };
 static const struct { int bq, bp, occ; float weight; } kMmShapes[kShapes] = {
     {256, 128, 2, 1.0f}, {128, 256, 2, 1.04f}, {128, 128, 3, 1.2f}, {64, 128, 4, 1.5f}};
