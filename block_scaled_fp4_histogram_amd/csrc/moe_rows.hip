@@ -118,48 +118,69 @@ __global__ __launch_bounds__(1024) void k_quant_int8(const uint16_t *x, long row
   }
 }
 
-// One wave per row that it holds in registers, CH chunks a lane: no barrier,
-// and four rows' loads in flight a block (4097 rows of 7168: 24 us, 3.6 TB/s; 40 us
-// with a block per row).
-template <int TYPE, int CH>
-__global__ __launch_bounds__(256) void k_quant_int8_rows(const uint16_t *x, long rows, int cols, int8_t *q, float *scales) {
-  const int n = cols / 8, lane = threadIdx.x & 63;
-  for (long row = (long)blockIdx.x * 4 + (threadIdx.x >> 6); row < rows; row += (long)gridDim.x * 4) {
+// Many rows: W waves per row that they hold in registers, two chunks a lane, and
+// several rows a block where W is small.  More chunks a lane leave too few waves
+// to load, compute and store at the same time, fewer make the barrier and the
+// start of a row count: 4096 rows of 4096 in 12.6 us with two, 13.8 with four,
+// 16.2 with eight; of 7168 in 20.0 us (4.4 TB/s) with two, 26.3 with sixteen.  The
+// kernel above takes 15.2 and 29.7 us there, and is as fast at 1024 rows.
+template <int TYPE, int W>
+__global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_quant_int8_rows(const uint16_t *x, long rows, int cols,
+                                                                        int8_t *q, float *scales) {
+  constexpr int CH = 2, NR = W > 4 ? 1 : 4 / W;
+  __shared__ uint32_t red[2][NR * W];
+  const int n = cols / 8, w = threadIdx.x >> 6, at = (w % W) * 64 + (threadIdx.x & 63);
+  int turn = 0;
+  for (long base = (long)blockIdx.x * NR; base < rows; base += (long)gridDim.x * NR, turn ^= 1) {
+    const long row = base + w / W;
+    const int mine = row < rows ? n : 0;
     const v4i *src = (const v4i *)(x + row * cols);
     v2u *dst = (v2u *)(q + row * cols);
     v4i v[CH];
 #pragma unroll
-    for (int i = 0; i < CH; i++) v[i] = lane + 64 * i < n ? src[lane + 64 * i] : v4i{0, 0, 0, 0};
+    for (int i = 0; i < CH; i++) v[i] = at + 64 * W * i < mine ? src[at + 64 * W * i] : v4i{0, 0, 0, 0};
     v2us mm = {0, 0};
 #pragma unroll
     for (int i = 0; i < CH; i++) mm = quant_largest(mm, v[i]);
     uint32_t m = row16_max(max((uint32_t)mm[0], (uint32_t)mm[1]));
     m = max(m, (uint32_t)__shfl_xor((int)m, 16));
     m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+    if constexpr (W > 1) {               // two turns' slots: one barrier a turn
+      if ((threadIdx.x & 63) == 0) red[turn][w] = m;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < W; k++) m = max(m, red[turn][w / W * W + k]);
+    }
     const RowScale r = row_scale<TYPE>(m);
-    if (lane == 0) scales[row] = r.scale;
+    if (at == 0 && mine) scales[row] = r.scale;
 #pragma unroll
     for (int i = 0; i < CH; i++) {
-      if (lane + 64 * i >= n) break;
+      if (at + 64 * W * i >= mine) break;
       uint32_t o[2];
       quant_chunk<TYPE>(v[i], r.s, r.inv, r.up, o);
-      dst[lane + 64 * i] = r.zero ? v2u{0, 0} : v2u{o[0], o[1]};
+      dst[at + 64 * W * i] = r.zero ? v2u{0, 0} : v2u{o[0], o[1]};
     }
   }
 }
 
-constexpr long kQuantBlocks = 1 << 18;   // a grid holds 2^32 threads at most: longer batches take further turns
+constexpr long kQuantBlocks = 1 << 18;   // most blocks of a launch: longer batches take further turns
+
+template <int TYPE, int W>
+static void launch_quant_rows(const uint16_t *x, long rows, int cols, int8_t *q, float *scales, hipStream_t s) {
+  constexpr int NR = W > 4 ? 1 : 4 / W;
+  hipLaunchKernelGGL((k_quant_int8_rows<TYPE, W>), dim3((unsigned)std::min((rows + NR - 1) / NR, kQuantBlocks)),
+                     dim3(64 * NR * W), 0, s, x, rows, cols, q, scales);
+}
 
 template <int TYPE>
 static hipError_t launch_quant(const uint16_t *x, long rows, int cols, int8_t *q, float *scales, hipStream_t s) {
   const int n = cols / 8;
-  // enough rows for a wave each to fill the chip
-  if (rows >= 4096 && n <= 1024) {
-    const dim3 g((unsigned)std::min((rows + 3) / 4, kQuantBlocks)), t(256);
-    if (n <= 128) hipLaunchKernelGGL((k_quant_int8_rows<TYPE, 2>), g, t, 0, s, x, rows, cols, q, scales);
-    else if (n <= 256) hipLaunchKernelGGL((k_quant_int8_rows<TYPE, 4>), g, t, 0, s, x, rows, cols, q, scales);
-    else if (n <= 512) hipLaunchKernelGGL((k_quant_int8_rows<TYPE, 8>), g, t, 0, s, x, rows, cols, q, scales);
-    else hipLaunchKernelGGL((k_quant_int8_rows<TYPE, 16>), g, t, 0, s, x, rows, cols, q, scales);
+  if (rows >= 2048 && n <= 2048) {
+    if (n <= 128) launch_quant_rows<TYPE, 1>(x, rows, cols, q, scales, s);
+    else if (n <= 256) launch_quant_rows<TYPE, 2>(x, rows, cols, q, scales, s);
+    else if (n <= 512) launch_quant_rows<TYPE, 4>(x, rows, cols, q, scales, s);
+    else if (n <= 1024) launch_quant_rows<TYPE, 8>(x, rows, cols, q, scales, s);
+    else launch_quant_rows<TYPE, 16>(x, rows, cols, q, scales, s);
   } else {
     const dim3 t(cols >= 8192 ? 1024 : (n + 63) / 64 * 64);
     hipLaunchKernelGGL(k_quant_int8<TYPE>, dim3((unsigned)std::min(rows, kQuantBlocks)), t, 0, s, x, rows, cols, q, scales);
@@ -196,7 +217,7 @@ __device__ __forceinline__ void group_place(const GroupArgs &a, int r, int e, in
 
 // Few routes (R and E at most the block's threads): every thread compares its expert and its route with all ids in
 // LDS, so offsets and sorted rows come without counting or scanning (one
-// barrier instead of five: 8 tokens of top-6 over 384 experts in 4.6 us
+// barrier instead of five: 8 tokens of top-6 over 384 experts in 3.9 us
 // against 7.1 us by a counting kernel).
 __global__ __launch_bounds__(kGroupThreads) void k_group_few(GroupArgs a) {
   __shared__ __align__(16) int ids[kGroupFew];

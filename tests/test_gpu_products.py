@@ -581,3 +581,16 @@ def test_output_over_an_input_is_refused():
                  lambda: M.grouped_mm_dw(x, x, first, out=w[:, :, :], rows=w.view(-1).view(torch.int32)[:64])):
         with pytest.raises(M.MoeError, match="overlap"):
             call()
+
+
+@pytest.mark.parametrize("cols", [16, 1024, 1040, 2064, 4096, 4112, 8208, 16384, 16400])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_quantiser_on_many_rows(cols, dtype):
+    """Row counts past and no multiple of what a block takes, at each number of waves a row."""
+    rows = 2051
+    x = _normal(_gen(cols), rows, cols, dtype=dtype)
+    x[1], x[700, cols - 1], x[rows - 1, 3] = 0, float("nan"), 300.0
+    q, s = M.quant_int8(x)
+    rq, rs = ref_quant(x)
+    assert torch.equal(torch.isnan(s), torch.isnan(rs)) and torch.equal(s.nan_to_num(), rs.nan_to_num())
+    assert torch.equal(q, rq)
