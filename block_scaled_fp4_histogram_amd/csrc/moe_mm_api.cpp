@@ -64,18 +64,20 @@ int check_rows(const char *fn, const int32_t *rows, long long x_rows, int R) {
   return MOE_OK;
 }
 
-int check_scratch(const char *fn, int op, int E, int R, int N, int K, const void *scratch, size_t bytes) {
-  const size_t need = moe_mm_scratch_bytes(op, E, R, N, K);
-  if (need && (!scratch || !aligned(scratch, 16))) return fail(MOE_EINVAL, "%s: null or misaligned scratch (16 bytes)", fn);
-  if (bytes < need) return fail(MOE_ESCRATCH, "%s: scratch holds %zu bytes, %zu needed", fn, bytes, need);
-  return MOE_OK;
-}
-
 // Buffers of a call: what it writes overlaps neither what it reads nor each other.
 struct Span {
   const void *p;
   size_t bytes;
 };
+
+// `work`: the part of the scratch that the call writes.
+int check_scratch(const char *fn, int op, int E, int R, int N, int K, const void *scratch, size_t bytes, Span *work) {
+  const size_t need = moe_mm_scratch_bytes(op, E, R, N, K);
+  if (need && (!scratch || !aligned(scratch, 16))) return fail(MOE_EINVAL, "%s: null or misaligned scratch (16 bytes)", fn);
+  if (bytes < need) return fail(MOE_ESCRATCH, "%s: scratch holds %zu bytes, %zu needed", fn, bytes, need);
+  *work = {need ? scratch : nullptr, need};
+  return MOE_OK;
+}
 
 int check_apart(const char *fn, std::initializer_list<Span> written, std::initializer_list<Span> read) {
   auto meet = [](const Span &a, const Span &b) {
@@ -121,8 +123,9 @@ int moe_grouped_mm(int dtype, const void *x, long long x_rows, const int32_t *ro
   if (!first) return fail(MOE_EINVAL, "%s: null first", fn);
   const void *p[] = {w, out, x};   // an x without rows is not read
   TRY(check_ptrs(fn, p, x_rows ? 3 : 2));
-  TRY(check_scratch(fn, MOE_MM_FORWARD, E, R, N, K, scratch, scratch_bytes));
-  TRY(check_apart(fn, {{out, (size_t)R * N * type_size(out_dtype)}, {scratch, scratch_bytes}},
+  Span work;
+  TRY(check_scratch(fn, MOE_MM_FORWARD, E, R, N, K, scratch, scratch_bytes, &work));
+  TRY(check_apart(fn, {{out, (size_t)R * N * type_size(out_dtype)}, work},
                   {{x, (size_t)x_rows * K * 2}, {w, (size_t)E * N * K * 2}, {first, (E + 1) * sizeof *first},
                    {rows, R * sizeof *rows}}));
   moe::MmArgs a = {};
@@ -142,8 +145,9 @@ int moe_grouped_mm_dx(int dtype, const void *dy, const void *w, const int32_t *f
   if (!first) return fail(MOE_EINVAL, "%s: null first", fn);
   const void *p[] = {dy, w, dx};
   TRY(check_ptrs(fn, p, 3));
-  TRY(check_scratch(fn, MOE_MM_DX, E, R, N, K, scratch, scratch_bytes));
-  TRY(check_apart(fn, {{dx, (size_t)R * K * type_size(out_dtype)}, {scratch, scratch_bytes}},
+  Span work;
+  TRY(check_scratch(fn, MOE_MM_DX, E, R, N, K, scratch, scratch_bytes, &work));
+  TRY(check_apart(fn, {{dx, (size_t)R * K * type_size(out_dtype)}, work},
                   {{dy, (size_t)R * N * 2}, {w, (size_t)E * N * K * 2}, {first, (E + 1) * sizeof *first}}));
   moe::MmArgs a = {};
   a.part = (float *)scratch;
@@ -164,8 +168,9 @@ int moe_grouped_mm_dw(int dtype, const void *dy, const void *x, long long x_rows
   if (!first) return fail(MOE_EINVAL, "%s: null first", fn);
   const void *p[] = {dw, dy, x};   // without rows dy and x are not read
   TRY(check_ptrs(fn, p, R == 0 ? 1 : x_rows ? 3 : 2));
-  TRY(check_scratch(fn, MOE_MM_DW, E, R, N, K, scratch, scratch_bytes));
-  TRY(check_apart(fn, {{dw, (size_t)E * N * K * type_size(out_dtype)}, {scratch, scratch_bytes}},
+  Span work;
+  TRY(check_scratch(fn, MOE_MM_DW, E, R, N, K, scratch, scratch_bytes, &work));
+  TRY(check_apart(fn, {{dw, (size_t)E * N * K * type_size(out_dtype)}, work},
                   {{dy, (size_t)R * N * 2}, {x, (size_t)x_rows * K * 2}, {first, (E + 1) * sizeof *first},
                    {rows, R * sizeof *rows}}));
   moe::MmArgs a = {};
@@ -204,8 +209,9 @@ int moe_grouped_int8_mm(const int8_t *x, const float *x_scales, long long x_rows
   TRY(check_ptrs(fn, p, x_rows ? 3 : 2));
   if ((!x_scales && x_rows) || !w_scales || !aligned(x_scales, 4) || !aligned(w_scales, 4))
     return fail(MOE_EINVAL, "%s: null or misaligned scales", fn);
-  TRY(check_scratch(fn, MOE_MM_INT8, E, R, N, K, scratch, scratch_bytes));
-  TRY(check_apart(fn, {{out, (size_t)R * N * type_size(out_dtype)}, {scratch, scratch_bytes}},
+  Span work;
+  TRY(check_scratch(fn, MOE_MM_INT8, E, R, N, K, scratch, scratch_bytes, &work));
+  TRY(check_apart(fn, {{out, (size_t)R * N * type_size(out_dtype)}, work},
                   {{x, (size_t)x_rows * K}, {x_scales, x_rows * sizeof *x_scales}, {w, (size_t)E * N * K},
                    {w_scales, (size_t)E * N * sizeof *w_scales}, {first, (E + 1) * sizeof *first},
                    {rows, R * sizeof *rows}}));
@@ -244,7 +250,7 @@ int moe_group_routes(const int32_t *topk_ids, int T, int top_k, int E, int32_t *
   if (scratch_bytes < need) return fail(MOE_ESCRATCH, "%s: scratch holds %zu bytes, %zu needed", fn, scratch_bytes, need);
   const size_t ids_bytes = (size_t)T * top_k * sizeof *topk_ids;
   TRY(check_apart(fn, {{first, (E + 1) * sizeof *first}, {order, ids_bytes}, {token, ids_bytes}, {inverse, ids_bytes},
-                       {scratch, scratch_bytes}}, {{topk_ids, ids_bytes}}));
+                       {need ? scratch : nullptr, need}}, {{topk_ids, ids_bytes}}));
   moe::GroupArgs a = {};
   a.ids = topk_ids, a.R = T * top_k, a.topk = top_k, a.E = E;
   if (need) a.rounds = moe::group_rounds(a.R), a.blocks = moe::group_blocks(a.R);

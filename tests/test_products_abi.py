@@ -138,3 +138,16 @@ def test_overlapping_buffers_are_refused():
     assert L.moe_int8_mm(far(0), far(1), far(2), far(3), 64, 64, 64, M.T_BF16, far(3) + 240, None, 0, None) == M.MOE_EINVAL
     assert L.moe_group_routes(far(0), 8, 2, 4, far(1), far(0) + 60, far(2), far(3), None, 0, None) == M.MOE_EINVAL
     assert L.moe_group_routes(far(0), 8, 2, 4, far(1), far(2), far(2), far(3), None, 0, None) == M.MOE_EINVAL
+
+
+def test_scratch_over_buffers_is_refused():
+    """Only what a call writes counts: 64 rows need none, 300 rows of a split reduction do."""
+    L = _lib.load()
+    far = lambda i: (1 << 30) + (i << 28)  # noqa: E731
+    need = M.mm_scratch_bytes(M.MM_FORWARD, 1, 300, 64, 8192)
+    assert need > 0 and M.mm_scratch_bytes(M.MM_FORWARD, 1, 64, 64, 64) == 0
+    call = lambda scratch, nbytes: L.moe_grouped_mm(M.T_BF16, far(0), 300, None, far(1), far(2), 1, 300, 64, 8192,  # noqa: E731
+                                                    M.T_BF16, far(3), scratch, nbytes, None)
+    assert call(None, 0) == M.MOE_EINVAL and call(far(4), need - 1) == M.MOE_ESCRATCH
+    assert call(far(3) - need + 16, need) == M.MOE_EINVAL and b"overlap" in L.moe_last_error()
+    assert call(far(1), need) == M.MOE_EINVAL and b"overlaps an input" in L.moe_last_error()
