@@ -163,12 +163,23 @@ __device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile
     return true;
   }
   const int per = (a.E + 63) >> 6;
-  int cnt = 0;
-  for (int i = 0; i < per; i++) {
-    const int e = lane * per + i;
-    int lo = 0, hi = 0;
-    if (e < a.E) mm_group(a, e, lo, hi);
-    cnt += (hi - lo + BQ - 1) / BQ;
+  int cnt = 0, lo = 0, hi = 0;
+  if (per == 1) {
+    if (lane < a.E) mm_group(a, lane, lo, hi);
+    cnt = (hi - lo + BQ - 1) / BQ;
+  } else {                               // eight groups' offsets at once: one wait for them all
+    for (int i = 0; i < per; i += 8) {
+      int v[9];
+#pragma unroll
+      for (int k = 0; k < 9; k++) v[k] = a.first[min(lane * per + i + k, a.E)];
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        if (i + k >= per) break;
+        lo = min(max(v[k], 0), a.R);
+        hi = min(max(v[k + 1], lo), a.R);
+        cnt += (hi - lo + BQ - 1) / BQ;
+      }
+    }
   }
   const int sum = wave_scan(cnt);
   const int total = uniform(__shfl(sum, 63)), nt = total * ptiles;
@@ -182,13 +193,18 @@ __device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile
   const int rt = grp * kMmGroup + rem % gcur;
   const int src = __ffsll(__ballot(sum > rt)) - 1;
   const int before = __shfl(sum - cnt, src);
-  const int e = src * per + lane;
-  int lo = 0, hi = 0;
-  if (lane < per && e < a.E) mm_group(a, e, lo, hi);
-  const int c = (hi - lo + BQ - 1) / BQ, s2 = wave_scan(c);
-  const int at = __ffsll(__ballot(before + s2 > rt)) - 1;
-  const int k = rt - before - __shfl(s2 - c, at);
-  t.e = uniform(src * per + at);
+  int at = 0, k = rt - before;           // the group's number in the lane's, its tile
+  if (per == 1) {
+    at = src;
+  } else {
+    const int e = src * per + lane;
+    lo = hi = 0;
+    if (lane < per && e < a.E) mm_group(a, e, lo, hi);
+    const int c = (hi - lo + BQ - 1) / BQ, s2 = wave_scan(c);
+    at = __ffsll(__ballot(before + s2 > rt)) - 1;
+    k -= __shfl(s2 - c, at);
+  }
+  t.e = uniform(per == 1 ? src : src * per + at);
   t.row0 = uniform(__shfl(lo, at) + k * BQ);
   t.rows = min(BQ, uniform(__shfl(hi, at)) - t.row0);
   return t.rows > 0;
@@ -206,19 +222,15 @@ __device__ __forceinline__ long mm_x_row(const MmArgs &a, int r) {
 // chunks, chunk c of row r at slot c ^ swz(r); transposed ones: 64 rows of B
 // 16-bit columns, chunk c of row z at c ^ 2 swz(z).  Either way the 16 (or,
 // transposed, 32) lanes that read together touch every bank once.
-//   Q rows are read 16 consecutive ones a fragment: swz = (r >> 1) & 7.
-//   P rows are read as 4 runs of 4, 16 apart (below): bits 1, 4 and 5 of r.
-__device__ __forceinline__ int swz_q(int r) { return (r >> 1) & 7; }
+//   Contiguous rows are read 16 consecutive ones a fragment: bits 1 to 3 of r.
 //   Transposed rows are read 8 g .. 8 g + 3 by lane group g, and 4 further on
 //   next: bits 0, 1 and 3 of z.
-__device__ __forceinline__ int swz_p(int r) { return ((r >> 1) & 1) | ((r >> 3) & 6); }
+__device__ __forceinline__ int swz_r(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int swz_t(int z) { return (z & 3) | ((z >> 1) & 4); }
 
 // The MFMA's rows are the output's contiguous dimension (P: weights, or x for
 // the weight gradient), its columns the output's rows (Q), so a lane's four
-// results are contiguous.  With a reduction-contiguous P, row a of fragment j
-// of a 64-row group is row 16 (a / 4) + 4 j + a % 4: a lane then holds 16
-// consecutive outputs over the four fragments, stored 16 bytes at a time.
+// results are contiguous.
 template <int OP, int TYPE, int BQ, int BP, int WQ, int WP, bool GATHER, int MINW>
 __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   typedef MmElem<TYPE> M;
@@ -278,13 +290,13 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   // The swizzle repeats over a wave's loads, but for one bit of it that flips with
   // every load where the rows between them reach only that bit: these bytes.
   static_assert(TQ_T ? DQ % 8 == 0 : DQ % 16 == 0, "loads of Q");
-  static_assert(TP_T ? DP % 8 == 0 : DP % 32 == 0, "loads of P");
-  constexpr uint32_t FQ = TQ_T && DQ % 16 ? 128 : 0, FP = TP_T ? (DP % 16 ? 128 : 0) : (DP % 64 ? 64 : 0);
+  static_assert(TP_T ? DP % 8 == 0 : DP % 16 == 0, "loads of P");
+  constexpr uint32_t FQ = TQ_T && DQ % 16 ? 128 : 0, FP = TP_T && DP % 16 ? 128 : 0;
   const int rq0 = TQ_T ? w * (64 / LRQ) + lane / LRQ : w * 8 + (lane >> 3);
   const int rp0 = TP_T ? w * (64 / LRP) + lane / LRP : w * 8 + (lane >> 3);
   // contiguous: the chunk's byte in the step; transposed: its byte in the row
-  const uint32_t cq = TQ_T ? q0 * 2 + (((lane % LRQ) ^ (2 * swz_t(rq0))) * 16) : ((lane & 7) ^ swz_q(rq0)) * 16;
-  const uint32_t cp = TP_T ? p0 * 2 + (((lane % LRP) ^ (2 * swz_t(rp0))) * 16) : ((lane & 7) ^ swz_p(rp0)) * 16;
+  const uint32_t cq = TQ_T ? q0 * 2 + (((lane % LRQ) ^ (2 * swz_t(rq0))) * 16) : ((lane & 7) ^ swz_r(rq0)) * 16;
+  const uint32_t cp = TP_T ? p0 * 2 + (((lane % LRP) ^ (2 * swz_t(rp0))) * 16) : ((lane & 7) ^ swz_r(rp0)) * 16;
   const uint32_t ldq = OP == MM_FORWARD ? ldx : ldy;
   const uint32_t vq = (uint32_t)rq0 * ldq + cq, vp = (uint32_t)rp0 * ldx + cp;
   const Rsrc rq = OP == MM_FORWARD  ? mm_rsrc(x + (GATHER ? 0 : (size_t)t.row0 * ldx), (uint32_t)qn * ldx)
@@ -369,12 +381,12 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   auto frag_q = [&](const uint8_t *tile, int j, int h) -> v4i {
     if (TQ_T) return frag_t(tile, BQ * 2, wq * TQ + 16 * j, h);
     const int r = wq * TQ + 16 * j + l16;
-    return *(const v4i *)(tile + r * 128 + (((4 * h + g) ^ swz_q(r)) * 16));
+    return *(const v4i *)(tile + r * 128 + (((4 * h + g) ^ swz_r(r)) * 16));
   };
   auto frag_p = [&](const uint8_t *tile, int j, int h) -> v4i {
     if (TP_T) return frag_t(tile, BP * 2, wp * TP + 16 * j, h);
-    const int r = wp * TP + (j >> 2) * 64 + (l16 >> 2) * 16 + (j & 3) * 4 + (l16 & 3);
-    return *(const v4i *)(tile + r * 128 + (((4 * h + g) ^ swz_p(r)) * 16));
+    const int r = wp * TP + 16 * j + l16;
+    return *(const v4i *)(tile + r * 128 + (((4 * h + g) ^ swz_r(r)) * 16));
   };
 
   typename M::acc acc[NP][NQ];
@@ -465,11 +477,14 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     float *part = a.part + (OUT == MM_PART ? (long)blockIdx.y * outs * pn : 0);
 #pragma unroll
     for (int i0 = 0; i0 < NP; i0 += 4) {
-      const int pc = p0 + wp * TP + 16 * i0, p = pc + 16 * g, po = pc + CW * (lane % LR);
+      const int pc = p0 + wp * TP + 16 * i0, po = pc + CW * (lane % LR);
       float ws[TYPE == MM_I8 ? 16 : 1];
       if constexpr (TYPE == MM_I8) {
 #pragma unroll
-        for (int k = 0; k < 16; k++) ws[k] = p + k < pn ? a.w_scales[(size_t)t.e * a.N + p + k] : 0.f;
+        for (int k = 0; k < 16; k++) {
+          const int p = pc + 16 * (k >> 2) + 4 * g + (k & 3);
+          ws[k] = p < pn ? a.w_scales[(size_t)t.e * a.N + p] : 0.f;
+        }
       }
 #pragma unroll
       for (int j = 0; j < NQ; j++) {
@@ -483,7 +498,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
             v[k] = OUT == MM_PART ? __builtin_bit_cast(float, e) : (float)e;
             if constexpr (TYPE == MM_I8 && OUT != MM_PART) v[k] *= xs[j] * ws[4 * i + k];
           }
-          uint8_t *o = mine + l16 * RB + (TP_T ? 16 * i + 4 * g : 16 * g + 4 * i) * (WIDE ? 4 : 2);
+          uint8_t *o = mine + l16 * RB + (16 * i + 4 * g) * (WIDE ? 4 : 2);
           if constexpr (WIDE) *(v4f *)o = v4f{v[0], v[1], v[2], v[3]};
           else *(v2u *)o = v2u{mm_pack<OUT>(v[0], v[1]), mm_pack<OUT>(v[2], v[3])};
         }
@@ -621,7 +636,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_mm_stream(MmArgs a) {
 #pragma unroll
   for (int i = 0; i < 2; i++) {
     const int r = 8 * i + (lane >> 3);
-    ck[i] = (uint32_t)((lane & 7) ^ swz_q(r)) * 16;
+    ck[i] = (uint32_t)((lane & 7) ^ swz_r(r)) * 16;
     vw[i] = (uint32_t)r * ld + ck[i];
     const long xr = r < t.rows ? (GATHER ? mm_x_row(a, t.row0 + r) : (long)t.row0 + r) : -1;
     live[i] = xr >= 0;
@@ -639,7 +654,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_mm_stream(MmArgs a) {
     for (int k = 0; k < 4; k++) ws[k] = a.w_scales[(size_t)t.e * a.N + p0 + op + k];
   }
   const uint32_t base = (uint32_t)(uintptr_t)(lds_void *)&ring[w][0][0];
-  const uint32_t rd0 = base + l16 * 128 + ((g ^ swz_q(l16)) * 16), rd1 = base + l16 * 128 + (((4 + g) ^ swz_q(l16)) * 16);
+  const uint32_t rd0 = base + l16 * 128 + ((g ^ swz_r(l16)) * 16), rd1 = base + l16 * 128 + (((4 + g) ^ swz_r(l16)) * 16);
   Acc acc = {0, 0, 0, 0};
   const int n = (units - w + NW - 1) / NW;   // columns of this wave
 
