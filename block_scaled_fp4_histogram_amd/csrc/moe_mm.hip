@@ -462,7 +462,8 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   // 16 bits 150 for 122.  Weight gradients, which are read much later, are stored
   // past the caches: another 210 -> 195 us and 122 -> 87 us there; the other
   // products' rows, which the next kernel reads, gain 0 to 3 % and stay.
-  mm_barrier();                          // every wave has read its last fragments
+  wait_lgkm0();                          // every wave has read its last fragments
+  mm_barrier();
   uint8_t *mine = lds + w * kOutStage;
   auto fence = [] {                      // LDS accesses of a wave are in order: for the compiler only
     asm volatile("" ::: "memory");
