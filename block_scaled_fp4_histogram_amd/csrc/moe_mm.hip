@@ -74,6 +74,21 @@ __device__ __forceinline__ void mm_store8(const MmArgs &a, long at, const float 
   }
 }
 
+// An integer sum by the scales of its row and channel.  The scales' fractions meet in
+// [1/4, 1) and their exponents are applied last, so neither the scales' product nor a
+// scale's with the sum leaves fp32's range before the result does (1e-22 * 1e-22 * 1e9;
+// 2.4e36 * 200 * 0), and where nothing leaves it the result is sum * (x * w) bit for bit.
+struct MmScale {
+  float m;
+  int e;
+};
+__device__ __forceinline__ MmScale mm_scale(float s) {
+  return MmScale{__builtin_amdgcn_frexp_mantf(s), __builtin_amdgcn_frexp_expf(s)};
+}
+__device__ __forceinline__ float mm_scaled(int sum, MmScale x, MmScale w) {
+  return __builtin_ldexpf((float)sum * (x.m * w.m), x.e + w.e);
+}
+
 // f(integral constant of the output type): the branch on it stands outside the stores.
 template <int V>
 struct MmConst {
@@ -446,13 +461,13 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
 
   // ---- outputs
   const long orow = OP == MM_DW ? (long)t.e * a.N + q0 : (long)t.row0;   // row 0 of the tile
-  float xs[TYPE == MM_I8 ? NQ : 1];
+  MmScale xs[TYPE == MM_I8 ? NQ : 1];
   if constexpr (TYPE == MM_I8) {
 #pragma unroll
     for (int j = 0; j < NQ; j++) {
       const int q = wq * TQ + 16 * j + l16;
       const long xr = q < qn ? mm_x_row(a, t.row0 + q) : -1;
-      xs[j] = xr < 0 ? 0.f : a.x_scales[xr];
+      xs[j] = mm_scale(xr < 0 ? 0.f : a.x_scales[xr]);
     }
   }
   // Sixteen rows of 64 columns at a time go through the wave's own part of LDS, so
@@ -479,12 +494,12 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
 #pragma unroll
     for (int i0 = 0; i0 < NP; i0 += 4) {
       const int pc = p0 + wp * TP + 16 * i0, po = pc + CW * (lane % LR);
-      float ws[TYPE == MM_I8 ? 16 : 1];
+      MmScale ws[TYPE == MM_I8 ? 16 : 1];
       if constexpr (TYPE == MM_I8) {
 #pragma unroll
         for (int k = 0; k < 16; k++) {
           const int p = pc + 16 * (k >> 2) + 4 * g + (k & 3);
-          ws[k] = p < pn ? a.w_scales[(size_t)t.e * a.N + p] : 0.f;
+          ws[k] = mm_scale(p < pn ? a.w_scales[(size_t)t.e * a.N + p] : 0.f);
         }
       }
 #pragma unroll
@@ -496,8 +511,9 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
 #pragma unroll
           for (int k = 0; k < 4; k++) {
             const auto e = acc[i0 + i][j][k];
-            v[k] = OUT == MM_PART ? __builtin_bit_cast(float, e) : (float)e;
-            if constexpr (TYPE == MM_I8 && OUT != MM_PART) v[k] *= xs[j] * ws[4 * i + k];
+            if constexpr (OUT == MM_PART) v[k] = __builtin_bit_cast(float, e);
+            else if constexpr (TYPE == MM_I8) v[k] = mm_scaled(e, xs[j], ws[4 * i + k]);
+            else v[k] = e;
           }
           uint8_t *o = mine + l16 * RB + (16 * i + 4 * g) * (WIDE ? 4 : 2);
           if constexpr (WIDE) *(v4f *)o = v4f{v[0], v[1], v[2], v[3]};
@@ -542,10 +558,10 @@ __global__ __launch_bounds__(256) void k_mm_join(MmArgs a) {
     }
     if (e < 0) return;
   }
-  float xs = 0.f;
+  MmScale xs = {0.f, 0};
   if (TYPE == MM_I8) {
     const long xr = mm_x_row(a, (int)row);
-    if (xr >= 0) xs = a.x_scales[xr];
+    if (xr >= 0) xs = mm_scale(a.x_scales[xr]);
   }
   mm_by_output(a.out_type, [&](auto out) {
     constexpr int OUT = decltype(out)::value;
@@ -560,8 +576,9 @@ __global__ __launch_bounds__(256) void k_mm_join(MmArgs a) {
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-          v[k] = (float)s[k >> 2][k & 3];
-          if (TYPE == MM_I8) v[k] *= xs * a.w_scales[(size_t)e * a.N + p + k];
+          const auto sum = s[k >> 2][k & 3];
+          if constexpr (TYPE == MM_I8) v[k] = mm_scaled(sum, xs, mm_scale(a.w_scales[(size_t)e * a.N + p + k]));
+          else v[k] = sum;
         }
         mm_store8<OUT>(a, row * pn + p, v);
       }
@@ -704,7 +721,10 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_mm_stream(MmArgs a) {
     for (int v = 1; v < NW; v++) r += sum[((v * 16 + oq) * RS + op) >> 2];
     float v[4];
 #pragma unroll
-    for (int k = 0; k < 4; k++) v[k] = TYPE == MM_I8 ? (float)r[k] * (xs * ws[k]) : (float)r[k];
+    for (int k = 0; k < 4; k++) {
+      if constexpr (TYPE == MM_I8) v[k] = mm_scaled(r[k], mm_scale(xs), mm_scale(ws[k]));
+      else v[k] = r[k];
+    }
     mm_store4<OUT>(a, (long)(t.row0 + oq) * a.N + p0 + op, v);
   });
 }

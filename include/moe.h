@@ -340,9 +340,9 @@ int moe_plan_set_activation(moe_plan_t plan, int act);
  * Matrices are row-major and contiguous, 16-byte aligned; N and K are
  * multiples of 8 (K of 16 for the integer products) up to 2^20, E 1 .. 1024,
  * R up to 2^30.  What a call writes may not overlap what it reads; an x of no
- * rows may be NULL.  Sums are kept in fp32 (exact int32 for integers) and
- * rounded once, to nearest even, on output.  Every sum has a fixed order:
- * results repeat bit for bit.
+ * rows may be NULL.  Sums are kept in fp32 (exact int32 for integers) and, with
+ * their scales for integers, rounded to nearest even once on output.  Every sum
+ * has a fixed order: results repeat bit for bit.
  * All calls are stream-ordered, neither allocate nor synchronise, and may be
  * captured in a HIP graph.  They work in `scratch` (device, 16-byte aligned,
  * at least moe_mm_scratch_bytes of the call's op and sizes; NULL when that is
@@ -396,7 +396,9 @@ int moe_quant_int8(int dtype, const void *x, int rows, int cols, int8_t *q, floa
 /*
  * moe_int8_mm -- out[m, n] = x_scales[m] * w_scales[n] * sum_k x[m, k] * w[n, k]
  * over 8-bit integers x [M, K] and w [N, K], the sum exact in 32 bits (K up to
- * 131056).  out_dtype MOE_T_BF16, MOE_T_FP16 or MOE_T_FP32.
+ * 131056).  The sum's conversion to fp32, the scales' product and theirs round to
+ * 24 bits each; only the result's own range counts, not that of the scales' product.
+ * out_dtype MOE_T_BF16, MOE_T_FP16 or MOE_T_FP32.
  * moe_grouped_int8_mm -- the same over groups: w [E, N, K], w_scales [E, N],
  * x_scales [x_rows] by row of x.
  */

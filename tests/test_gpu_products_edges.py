@@ -1,0 +1,73 @@
+"""Edges of the ragged products on the GPU: scales at the ends of fp32's range, groups without rows,
+versions of given outputs, exceptions, and every tile shape next to rows, columns and values that are
+not its own. References in float64 (tests/products_util.py)."""
+import pytest
+import torch
+
+import block_scaled_fp4_histogram_amd as M
+from products_util import (BF16, FP16, FP32, assert_int8, assert_product, offsets, ref_dw, ref_dx, ref_int8, ref_mm)
+
+pytestmark = pytest.mark.gpu
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _normal(g, *shape, dtype=BF16, scale=1.0):
+    return torch.randn(*shape, device="cuda", generator=g).mul_(scale).to(dtype)
+
+
+# ---- integer products: scales at the ends of fp32's range
+
+# pairs of an x scale and a w scale whose product leaves fp32's normal range, or whose x scale times the sum
+# does, while the result is a number of fp32 (or, at the last, passes it)
+ROW_SCALES = [1e-22, 2.4e36, 1.0, 1e-37, 2.0 ** -149, 3e30, 1e-30, 0.0]
+CHANNEL_SCALES = [1e-22, 200.0, 1e-30, 2.0 ** -149, 1e-3, 3e36, 1.0, 5e-16]
+
+
+def assert_scaled(got, ref, label=""):
+    """The integer sum is exact. Its conversion to fp32, the product of the scales' fractions and their
+    product round three times (2^-24 each of the value, whatever the scales' exponents); applying the
+    exponents rounds only below 2^-126 (half of 2^-149), the output type once (half a step, or half its
+    smallest subnormal). Results past the type's range are infinite: a reference within 2^-6 of it
+    either way is not compared."""
+    fi = torch.finfo(got.dtype)
+    tol = (3.01 * 2.0 ** -24 + fi.eps / 2) * (1 + 2.0 ** -20) * ref.abs() + fi.tiny * fi.eps / 2 + 2.0 ** -150
+    past = ref.abs() > fi.max * (1 + 2.0 ** -6)
+    near = ref.abs() > fi.max * (1 - 2.0 ** -6)
+    ok = torch.where(past, got.double() == torch.sign(ref) * float("inf"), ((got.double() - ref).abs() <= tol) | near)
+    bad = (~ok).flatten().nonzero()
+    assert bad.numel() == 0, (f"{label}: {bad.numel()} of {ok.numel()} outside, first at {int(bad[0])}: got "
+                              f"{got.flatten()[bad[0]].item()}, want {ref.flatten()[bad[0]].item()}")
+
+
+@pytest.mark.parametrize("counts,K", [([5], 1040), ([3, 0, 8], 272), ([700, 0, 333], 272), ([90, 0, 140], 8192)])
+@pytest.mark.parametrize("out_dtype", [BF16, FP16, FP32])
+def test_int8_scales_at_the_ends_of_the_range(counts, K, out_dtype):
+    """Streamed rows, tiles and split reductions: a result that the output type holds comes out whatever its
+    scales' product does, and a zero sum is zero."""
+    g = _gen(K)
+    R, E, N = sum(counts), len(counts), 1032
+    i8 = lambda *s: torch.randint(-128, 128, s, device="cuda", generator=g, dtype=torch.int8)  # noqa: E731
+    x, w = i8(R, K), i8(E, N, K)
+    x[1::5] = 0
+    xs = torch.tensor(ROW_SCALES, device="cuda").repeat(R // 8 + 1)[:R].contiguous()
+    ws = torch.tensor(CHANNEL_SCALES, device="cuda").repeat_interleave(3).repeat(N // 24)[:N].repeat(E, 1).contiguous()
+    first = offsets(counts).cuda()
+    ref, _ = ref_int8(x, xs, w, ws, first, None, R)
+    assert bool((ref[1::5] == 0).all())
+    assert_scaled(M.grouped_int8_mm(x, xs, w, ws, first, out_dtype=out_dtype), ref, "grouped")
+    if E == 1:
+        assert_scaled(M.int8_mm(x, xs, w[0], ws[0], out_dtype=out_dtype), ref, "dense")
+
+
+def test_int8_products_of_a_row_near_the_largest_value():
+    """A bf16 row of 3e38 has a scale of 2.4e36; orthogonal codes still give zeros with large channel scales."""
+    x = torch.zeros(2, 32, dtype=BF16, device="cuda")
+    x[0, :16], x[1, 16:] = 3e38, 1.0
+    q, s = M.quant_int8(x)
+    w = q.repeat(4, 1).contiguous()
+    out = M.int8_mm(q, s, w, torch.full((8,), 4e3, device="cuda"), out_dtype=FP32)
+    assert out[0, 1::2].tolist() == [0.0] * 4 and out[1, 0::2].tolist() == [0.0] * 4
+    assert bool(torch.isinf(out[0, 0::2]).all())
