@@ -411,7 +411,7 @@ def grouped_mm_dw(dy, x, first, rows=None, out=None, out_dtype=None, accumulate:
     group e of the outer products dy[r] x[row(r)]; zeros for an empty group.
 
     dy [R, N], x [T, K] bf16 or fp16, rows as in grouped_mm; out [E, N, K] in dy's type or fp32.
-    accumulate adds to out (fp32, required then)."""
+    accumulate adds to out (fp32, required then), whose part of an empty group stays as it is."""
     if stream is not None:
         with _use(stream, dy):
             return grouped_mm_dw(dy, x, first, rows, out, out_dtype, accumulate, scratch)

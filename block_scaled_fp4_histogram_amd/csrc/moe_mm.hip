@@ -278,6 +278,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     mm_group(a, t.e, lo, hi);
     t.row0 = uniform(lo);
     t.rows = uniform(hi) - t.row0;
+    if (a.accumulate && t.rows == 0) return;   // nothing to add: what dw holds stays as it is
     qn = min(BQ, a.N - q0);
     zn = t.rows;
   } else {
@@ -557,6 +558,11 @@ __global__ __launch_bounds__(256) void k_mm_join(MmArgs a) {
       }
     }
     if (e < 0) return;
+  }
+  if (a.accumulate) {                    // of a weight gradient: a group without rows has no parts
+    int lo, hi;
+    mm_group(a, (int)(row / a.N), lo, hi);
+    if (lo == hi) return;
   }
   MmScale xs = {0.f, 0};
   if (TYPE == MM_I8) {

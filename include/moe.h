@@ -378,7 +378,7 @@ int moe_grouped_mm_dx(int dtype, const void *dy, const void *w, const int32_t *f
 /* moe_grouped_mm_dw -- the gradient for the weights:
  * dw[e, n, k] = sum over the rows r of group e of dy[r, n] * x[row(r), k];
  * dw [E, N, K], zeros for an empty group.  accumulate (fp32 dw only) adds to
- * what dw holds instead. */
+ * what dw holds instead, and leaves an empty group's part as it is. */
 int moe_grouped_mm_dw(int dtype, const void *dy, const void *x, long long x_rows, const int32_t *rows,
                       const int32_t *first, int E, int R, int N, int K, int out_dtype, int accumulate, void *dw,
                       void *scratch, size_t scratch_bytes, void *stream);

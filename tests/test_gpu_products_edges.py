@@ -71,3 +71,31 @@ def test_int8_products_of_a_row_near_the_largest_value():
     out = M.int8_mm(q, s, w, torch.full((8,), 4e3, device="cuda"), out_dtype=FP32)
     assert out[0, 1::2].tolist() == [0.0] * 4 and out[1, 0::2].tolist() == [0.0] * 4
     assert bool(torch.isinf(out[0, 0::2]).all())
+
+
+@pytest.mark.parametrize("counts,N,K", [([0, 70, 0, 33], 136, 72), ([5000, 0, 3001], 72, 136)])
+@pytest.mark.parametrize("gathered", [False, True])
+def test_accumulating_leaves_groups_without_rows_bit_for_bit(counts, N, K, gathered):
+    """Nothing is added there: negative zeros keep their sign, NaNs their bits (whole and split reductions)."""
+    E, R = len(counts), sum(counts)
+    g = _gen(N)
+    dy, x = _normal(g, R, N), _normal(g, R, K)
+    rows = torch.randperm(R, device="cuda", generator=g).to(torch.int32) if gathered else None
+    base = torch.randn(E, N, K, device="cuda", generator=g)
+    base[:, ::2, 1::3] = -0.0
+    base[0, 1, 2] = base[1, 3, 4] = -float("nan")
+    out = base.clone()
+    first = offsets(counts).cuda()
+    M.grouped_mm_dw(dy, x, first, rows=rows, out=out, accumulate=True)
+    ref, mag = ref_dw(dy, x, first, rows)
+    for e, c in enumerate(counts):
+        if c == 0:
+            assert torch.equal(out[e].view(torch.int32), base[e].view(torch.int32))
+            continue
+        fin = torch.isfinite(base[e])
+        assert bool((torch.isfinite(out[e]) == fin).all())
+        b = base[e].double()
+        assert_product(out[e][fin], (ref[e] + b)[fin], (mag[e] + b.abs())[fin], c + 1)
+    none = base.clone()
+    M.grouped_mm_dw(dy[:0], x[:0], torch.zeros(E + 1, dtype=torch.int32, device="cuda"), out=none, accumulate=True)
+    assert torch.equal(none.view(torch.int32), base.view(torch.int32))
