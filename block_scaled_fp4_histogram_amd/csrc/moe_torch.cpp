@@ -7,6 +7,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/torch.h>
 
@@ -204,8 +205,8 @@ PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F f) {
   } catch (const Refused &r) {
     PyErr_SetString(r.type, r.text.c_str());
   } catch (const PythonError &) {
-  } catch (const std::exception &e) {    // an allocation that fails, among others
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {                        // torch's own, with their types: an allocation that fails, among others
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

@@ -99,3 +99,12 @@ def test_accumulating_leaves_groups_without_rows_bit_for_bit(counts, N, K, gathe
     none = base.clone()
     M.grouped_mm_dw(dy[:0], x[:0], torch.zeros(E + 1, dtype=torch.int32, device="cuda"), out=none, accumulate=True)
     assert torch.equal(none.view(torch.int32), base.view(torch.int32))
+
+
+def test_out_of_memory_keeps_its_type():
+    """An output that no card holds (2 TiB): the allocator's own exception, and the next call works."""
+    dy, first = torch.zeros(1, 1 << 20, dtype=BF16, device="cuda"), offsets([1]).cuda()
+    with pytest.raises(torch.OutOfMemoryError):
+        M.grouped_mm_dw(dy, dy, first)
+    x = torch.ones(1, 8, dtype=BF16, device="cuda")
+    assert M.grouped_mm_dw(x, x, first).tolist() == [[[1.0] * 8] * 8]
