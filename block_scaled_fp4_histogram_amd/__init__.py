@@ -378,7 +378,8 @@ def mm_scratch_bytes(op: int, E: int, R: int, N: int, K: int) -> int:
 
 # The products below check types, shapes, contiguity and device of every tensor, make the outputs and the
 # scratch that are not given, and run on `stream` or on the current stream of the operands' device. autograd
-# does not record them: a training step calls the gradients itself.
+# does not record them: a training step calls the gradients itself, in an autograd.Function or under
+# torch.no_grad(). Elsewhere an operand that requires grad is refused.
 
 
 def grouped_mm(x, w, first, rows=None, out=None, out_dtype=None, scratch=None, stream=None):

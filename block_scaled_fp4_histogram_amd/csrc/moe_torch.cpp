@@ -86,7 +86,8 @@ void has_type(const Tensor &t, const char *name, Types types) {
 }
 
 // The operands of one call: types and shapes as they are added, then that all
-// are contiguous on one GPU.
+// are contiguous on one GPU and that autograd expects nothing of the call, which
+// it does not see: a result without a history would lose gradients silently.
 struct Operands {
   struct { const Tensor *t; const char *name; } list[8];
   int n = 0;
@@ -99,6 +100,11 @@ struct Operands {
     return t;
   }
   void check() const {
+    if (at::GradMode::is_enabled())
+      for (int i = 0; i < n; i++)
+        if (list[i].t->requires_grad())
+          refuse(PyExc_ValueError, std::string(list[i].name) + " requires grad, and autograd does not record this call: make it " +
+                                       "under torch.no_grad() or in an autograd.Function, and the gradients' calls yourself");
     for (int i = 0; i < n; i++) {
       const Tensor &t = *list[i].t;
       if (!t.is_contiguous()) refuse(PyExc_ValueError, std::string(list[i].name) + " must be contiguous");

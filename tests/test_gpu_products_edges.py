@@ -108,3 +108,35 @@ def test_out_of_memory_keeps_its_type():
         M.grouped_mm_dw(dy, dy, first)
     x = torch.ones(1, 8, dtype=BF16, device="cuda")
     assert M.grouped_mm_dw(x, x, first).tolist() == [[[1.0] * 8] * 8]
+
+
+class _Product(torch.autograd.Function):
+    """grouped_mm recorded by autograd, as a training program wraps it: rows in order, both gradients."""
+
+    @staticmethod
+    def forward(ctx, x, w, first):
+        ctx.save_for_backward(x, w, first)
+        return M.grouped_mm(x, w, first)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, first = ctx.saved_tensors
+        return M.grouped_mm_dx(dy, w, first), M.grouped_mm_dw(dy, x, first), None
+
+
+def test_products_in_an_autograd_function():
+    """Two products in a row through autograd: the gradients are the entry points', bit for bit, and the
+    operands themselves are refused outside the function."""
+    g = _gen(32)
+    first = offsets([9, 0, 30, 1]).cuda()
+    x, w1, w2 = (_normal(g, *s).requires_grad_() for s in ((40, 72), (4, 136, 72), (4, 24, 136)))
+    dout = _normal(g, 40, 24)
+    _Product.apply(_Product.apply(x, w1, first), w2, first).backward(dout)
+    with torch.no_grad():
+        h = M.grouped_mm(x, w1, first)
+        dh = M.grouped_mm_dx(dout, w2, first)
+        want = (M.grouped_mm_dx(dh, w1, first), M.grouped_mm_dw(dh, x, first), M.grouped_mm_dw(dout, h, first))
+    for t, r in zip((x, w1, w2), want):
+        assert torch.equal(t.grad, r)
+    with pytest.raises(ValueError, match="x requires grad"):
+        M.grouped_mm(x, w1, first)

@@ -151,3 +151,25 @@ def test_scratch_over_buffers_is_refused():
     assert call(None, 0) == M.MOE_EINVAL and call(far(4), need - 1) == M.MOE_ESCRATCH
     assert call(far(3) - need + 16, need) == M.MOE_EINVAL and b"overlap" in L.moe_last_error()
     assert call(far(1), need) == M.MOE_EINVAL and b"overlaps an input" in L.moe_last_error()
+
+
+def test_operands_that_require_grad_are_refused_while_autograd_records():
+    """The calls return results without a history: with autograd on, gradients would go missing silently."""
+    bf, i8 = torch.bfloat16, torch.int8
+    g = lambda *s, dtype=bf: torch.zeros(s, dtype=dtype, requires_grad=True)  # noqa: E731
+    x, w, dy, first = torch.zeros(6, 16, dtype=bf), torch.zeros(2, 8, 16, dtype=bf), torch.zeros(6, 8, dtype=bf), torch.zeros(3, dtype=torch.int32)
+    xq, wq, xs, ws = x.to(i8), w.to(i8), torch.zeros(6), torch.zeros(2, 8)
+    calls = [("x", lambda: M.grouped_mm(g(6, 16), w, first)), ("w", lambda: M.grouped_mm(x, g(2, 8, 16), first)),
+             ("out", lambda: M.grouped_mm(x, w, first, out=g(6, 8))),
+             ("dy", lambda: M.grouped_mm_dx(g(6, 8), w, first)), ("w", lambda: M.grouped_mm_dx(dy, g(2, 8, 16), first)),
+             ("dy", lambda: M.grouped_mm_dw(g(6, 8), x, first)), ("x", lambda: M.grouped_mm_dw(dy, g(6, 16), first)),
+             ("out", lambda: M.grouped_mm_dw(dy, x, first, out=g(2, 8, 16, dtype=torch.float32), accumulate=True)),
+             ("x", lambda: M.quant_int8(g(6, 16))), ("scales", lambda: M.quant_int8(x, scales=g(6, dtype=torch.float32))),
+             ("x_scales", lambda: M.int8_mm(xq, g(6, dtype=torch.float32), wq[0], ws[0])),
+             ("w_scales", lambda: M.grouped_int8_mm(xq, xs, wq, g(2, 8, dtype=torch.float32), first))]
+    for name, call in calls:
+        with pytest.raises(ValueError, match=f"^{name} requires grad"):
+            call()
+        for off in (torch.no_grad(), torch.inference_mode()):
+            with off, pytest.raises(ValueError, match="device tensor"):
+                call()
