@@ -194,8 +194,12 @@ void done(int rc) {
   throw PythonError();
 }
 
+// The output of a call that succeeded.  A given one has been written through its
+// pointer: its version moves on, so that autograd reports a saved tensor that was
+// overwritten (inference tensors have no version).
 PyObject *result(PyObject *given, const Tensor &made) {
   if (none(given)) return THPVariable_Wrap(made);
+  if (!made.is_inference()) made.unsafeGetTensorImpl()->bump_version();
   Py_INCREF(given);
   return given;
 }

@@ -140,3 +140,47 @@ def test_products_in_an_autograd_function():
         assert torch.equal(t.grad, r)
     with pytest.raises(ValueError, match="x requires grad"):
         M.grouped_mm(x, w1, first)
+
+
+def _written_outputs():
+    """(name, given output, call into it) of every entry point that takes one."""
+    g = _gen(31)
+    x, w, dy, first = _normal(g, 6, 16), _normal(g, 2, 8, 16), _normal(g, 6, 8), offsets([2, 4]).cuda()
+    q, s = M.quant_int8(x)
+    wq, ws = M.quant_int8(w.view(16, 16))
+    new = lambda *shape, dtype=BF16: torch.zeros(shape, dtype=dtype, device="cuda")  # noqa: E731
+    o = [new(6, 8), new(6, 16), new(2, 8, 16, dtype=FP32), new(6, 16, dtype=torch.int8), new(6, dtype=FP32), new(6, 8), new(6, 8)]
+    return [("grouped_mm", o[0], lambda t: M.grouped_mm(x, w, first, out=t)),
+            ("grouped_mm_dx", o[1], lambda t: M.grouped_mm_dx(dy, w, first, out=t)),
+            ("grouped_mm_dw", o[2], lambda t: M.grouped_mm_dw(dy, x, first, out=t, accumulate=True)),
+            ("quant_int8", o[3], lambda t: M.quant_int8(x, out=t)),
+            ("quant_int8 scales", o[4], lambda t: M.quant_int8(x, scales=t)),
+            ("int8_mm", o[5], lambda t: M.int8_mm(q, s, wq[:8], ws[:8], out=t)),
+            ("grouped_int8_mm", o[6], lambda t: M.grouped_int8_mm(q, s, wq.view(2, 8, 16), ws.view(2, 8), first, out=t))]
+
+
+def test_given_outputs_advance_their_version():
+    """As torch's own writes in place do, also where autograd is off or the output is an inference tensor."""
+    for name, out, call in _written_outputs():
+        for step in (1, 2):
+            call(out)
+            assert out._version == step, name
+        with torch.no_grad():
+            call(out)
+        assert out._version == 3, name
+        with torch.inference_mode():
+            inf = torch.zeros_like(out)
+            call(inf)
+        call(inf)
+        assert torch.equal(inf, out) or name == "grouped_mm_dw", name
+
+
+def test_overwriting_a_saved_tensor_is_reported_by_backward():
+    for name, out, call in _written_outputs():
+        if not out.is_floating_point():
+            continue
+        p = torch.ones_like(out, requires_grad=True)
+        loss = (out * p).sum()                        # saves out for p's gradient
+        call(out)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
