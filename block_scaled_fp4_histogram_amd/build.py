@@ -32,7 +32,7 @@ BINDING = os.path.join(PKG, "_products.so")
 
 
 def build_binding(verbose: bool = False) -> str:
-    """The torch binding of the products: host code only."""
+    """The torch binding of the products: host code only. The library, and the layer through it, do without."""
     import sysconfig
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
@@ -46,7 +46,10 @@ def build_binding(verbose: bool = False) -> str:
     cmd += ["-lc10", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"building the binding failed: {e}") from e
     if r.returncode != 0:
         raise RuntimeError(f"building the binding failed ({r.returncode}):\n{r.stderr}")
     os.replace(BINDING + ".tmp", BINDING)
@@ -54,6 +57,7 @@ def build_binding(verbose: bool = False) -> str:
 
 
 def build(verbose: bool = False) -> str:
+    """The library."""
     cmd = [HIPCC] + FLAGS + SOURCES + ["-o", LIB + ".tmp"]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -65,9 +69,9 @@ def build(verbose: bool = False) -> str:
     if verbose and err:
         print(err, file=sys.stderr)
     os.replace(LIB + ".tmp", LIB)
-    build_binding(verbose)
     return LIB
 
 
 if __name__ == "__main__":
     build(verbose=True)
+    build_binding(verbose=True)
