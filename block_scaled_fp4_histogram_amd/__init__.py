@@ -462,6 +462,14 @@ def group_routes(topk_ids, num_experts: int, scratch=None, stream=None):
     return (_binding or _bind()).group_routes(topk_ids, num_experts, scratch)
 
 
+def debug_mm_plan(op: int, E: int, R: int, N: int, K: int):
+    """(rows and columns of an output tile, parts of the reduction) a product of these sizes runs with
+    (moe_debug_mm_plan); op as in mm_scratch_bytes. (16, 16, 1): streamed weights."""
+    v = [C.c_int() for _ in range(3)]
+    _check(_lib.load().moe_debug_mm_plan(op, E, R, N, K, *map(C.byref, v)))
+    return tuple(x.value for x in v)
+
+
 def debug_route(plan: Plan, tiers: Sequence, topk_ids, scratch=None, stream=None):
     """Route planner alone. Returns (cnt [U], off [U+1], perm [off[U]], inv [T*k]) device tensors."""
     import torch

@@ -34,6 +34,7 @@ struct MmArgs {
 // from the sizes alone.
 struct MmPlan {
   int stream, shape, splits;
+  int rows, cols;                    // of a tile
   size_t scratch;
 };
 MmPlan mm_plan(int op, int type, long E, long R, long N, long K);

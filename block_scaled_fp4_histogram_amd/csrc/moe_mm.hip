@@ -755,7 +755,7 @@ static const struct { int bq, bp, occ; float weight; } kMmShapes[kShapes] = {
     {256, 128, 2, 1.0f}, {128, 256, 2, 1.04f}, {128, 128, 3, 1.2f}, {64, 128, 4, 1.5f}};
 
 MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
-  MmPlan m = {0, 0, 1, 0};
+  MmPlan m = {0, 0, 1, 16, 16, 0};
   const long item = type == MM_I8 ? 1 : 2, groups = E < R ? E : R;
   const long pn = op == MM_FORWARD ? N : K, qn = op == MM_DW ? N : R, outs = op == MM_DW ? E * N : R;
   // Few rows a group: the weights pass once, 16 of their rows a block.  Short rows
@@ -799,6 +799,7 @@ MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
   // N = 1024, K = 4096: 15.2 us, 41.3 us whole; int8, R = 500, N = 4608, K = 7168:
   // 45.4 us in parts that fill the chip, 39.6 whole).
   const auto &shape = kMmShapes[m.shape];
+  m.rows = shape.bq, m.cols = shape.bp;
   const long steps = op == MM_FORWARD ? K * item / 128 : op == MM_DX ? N / 64 : R / E / 64;
   const float step = op == MM_DW ? 1.0f : 0.6f;
   const float feed = (float)(tiles * steps * (shape.bq + shape.bp)) * (128 / 12e6f);

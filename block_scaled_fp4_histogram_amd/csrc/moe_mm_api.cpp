@@ -93,6 +93,16 @@ int check_apart(const char *fn, std::initializer_list<Span> written, std::initia
   return MOE_OK;
 }
 
+int check_op(const char *fn, int op, int E, int R, int N, int K) {
+  if (op < MOE_MM_FORWARD || op > MOE_MM_INT8) return fail(MOE_EINVAL, "%s: op=%d", fn, op);
+  return check_shape(fn, op == MOE_MM_INT8 ? 16 : 8, nullptr, E, R, N, K);
+}
+
+moe::MmPlan plan_of(int op, int E, int R, int N, int K) {
+  const bool i8 = op == MOE_MM_INT8;
+  return moe::mm_plan(i8 ? MOE_MM_FORWARD : op, i8 ? moe::MM_I8 : moe::MM_BF16, E, R, N, K);
+}
+
 size_t type_size(int dtype) { return dtype == MOE_T_FP32 ? 4 : 2; }
 
 }  // namespace
@@ -106,10 +116,17 @@ size_t type_size(int dtype) { return dtype == MOE_T_FP32 ? 4 : 2; }
 extern "C" {
 
 size_t moe_mm_scratch_bytes(int op, int E, int R, int N, int K) {
-  const bool i8 = op == MOE_MM_INT8;
-  if (op < MOE_MM_FORWARD || op > MOE_MM_INT8 || check_shape("moe_mm_scratch_bytes", i8 ? 16 : 8, nullptr, E, R, N, K) != MOE_OK)
-    return 0;
-  return R == 0 ? 0 : moe::mm_plan(i8 ? MOE_MM_FORWARD : op, i8 ? moe::MM_I8 : moe::MM_BF16, E, R, N, K).scratch;
+  if (check_op("moe_mm_scratch_bytes", op, E, R, N, K) != MOE_OK) return 0;
+  return R == 0 ? 0 : plan_of(op, E, R, N, K).scratch;
+}
+
+int moe_debug_mm_plan(int op, int E, int R, int N, int K, int *rows, int *cols, int *splits) {
+  const char *fn = "moe_debug_mm_plan";
+  TRY(check_op(fn, op, E, R, N, K));
+  if (R == 0 || !rows || !cols || !splits) return fail(MOE_EINVAL, "%s: R=0 or a null pointer", fn);
+  const moe::MmPlan m = plan_of(op, E, R, N, K);
+  *rows = m.rows, *cols = m.cols, *splits = m.splits;
+  return MOE_OK;
 }
 
 int moe_grouped_mm(int dtype, const void *x, long long x_rows, const int32_t *rows, const void *w,

@@ -453,6 +453,15 @@ int moe_debug_route(moe_plan_t plan, const moe_tier *tiers, int n_tiers, const i
                     void *scratch, size_t scratch_bytes, int32_t *cnt, int32_t *off, int32_t *perm,
                     int32_t *inv, void *stream);
 
+/*
+ * moe_debug_mm_plan -- how a product of these sizes runs (op as in moe_mm_op, so
+ * that the tests of the tile shapes run the shapes they name): output rows and
+ * columns of a tile (16 x 16: few rows a group, weights streamed) and the parts of
+ * its reduction.  Host only; MOE_EINVAL or MOE_EUNSUPPORTED on sizes that the call
+ * refuses and for R = 0.
+ */
+int moe_debug_mm_plan(int op, int E, int R, int N, int K, int *rows, int *cols, int *splits);
+
 /* MXFP8 quantiser alone: rows x cols (cols % 32 == 0) of bf16 or fp32 ->
  * E4M3 codes u8 [rows, cols] + E8M0 scales u8 [rows, cols/32].  The bf16 one
  * runs the block quantiser every bf16-activation path of moe_run uses (x in

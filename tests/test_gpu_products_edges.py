@@ -184,3 +184,205 @@ def test_overwriting_a_saved_tensor_is_reported_by_backward():
         call(out)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             loss.backward()
+
+
+# ---- every tile shape: sizes that select it, next to rows, columns and values that are not its own
+#
+# Reductions of more than two steps with a partial last one, columns past the last whole tile, groups of
+# odd sizes and without rows, product rows in front of the groups and behind them. Infinities and NaNs stand
+# in single operands' ends and in everything that no output may read; they have to reach the sums they are
+# a term of and no other. (E, R, N, K, rows, columns of the tile, whether the reduction is split)
+
+FORWARD = {"64x128": (5, 900, 1048, 200, 64, 128, False), "128x128": (5, 2900, 3080, 200, 128, 128, False),
+           "128x256": (40, 5000, 4104, 136, 128, 256, False), "256x128": (5, 3000, 4104, 200, 256, 128, False),
+           "split": (5, 400, 264, 4104, 64, 128, True), "stream": (5, 75, 264, 520, 16, 16, False)}
+DX = {"64x128": (5, 900, 200, 1048, 64, 128, False), "128x128": (5, 2900, 200, 3080, 128, 128, False),
+      "128x256": (40, 5000, 136, 4104, 128, 256, False), "256x128": (5, 3000, 200, 4104, 256, 128, False),
+      "split": (5, 300, 2600, 264, 64, 128, True)}
+DW = {"128x128": (8, 1200, 520, 1048, 128, 128, False), "256x128": (4, 1100, 2056, 1544, 256, 128, False),
+      "split": (3, 8040, 72, 136, 128, 128, True)}
+INT8 = {"64x128": (5, 900, 1048, 400, 64, 128, False), "128x128": (5, 2900, 3080, 400, 128, 128, False),
+        "128x256": (40, 5000, 4104, 272, 128, 256, False), "256x128": (5, 3000, 4104, 400, 256, 128, False),
+        "split": (5, 400, 264, 8208, 64, 128, True), "stream": (5, 75, 264, 1040, 16, 16, False)}
+DENSE = {"64x128": (1, 900, 1048, 400, 64, 128, False), "128x128": (1, 2900, 3080, 400, 128, 128, False),
+         "128x256": (1, 1876, 8200, 272, 128, 256, False), "256x128": (1, 3000, 4104, 400, 256, 128, False)}
+START, TAIL = 3, 5
+
+
+def _selected(op, case):
+    """Operand sizes of a case, which have to select the shape it is named after."""
+    E, R, N, K, rows, cols, split = case
+    got = M.debug_mm_plan(op, E, R, N, K)
+    assert got[:2] == (rows, cols) and (got[2] > 1) == split, got
+    return E, R, N, K
+
+
+def _ragged(E, R):
+    """Group sizes of R - START - TAIL rows: the second group empty (where there are three), the last one a
+    single row, the others uneven."""
+    n = R - START - TAIL
+    w = [1 + (5 * e) % 7 for e in range(E)]
+    w[-1] = 0
+    if E > 2:
+        w[1] = 0
+    counts = [(n - 1) * x // sum(w) for x in w]
+    counts[-1] = 1
+    counts[0] += n - sum(counts)
+    return counts
+
+
+def _numbered(g, R, T):
+    """Row numbers: any row of x but its last inside the groups (two of them no row), the last one outside."""
+    rows = torch.randint(0, T - 1, (R,), device="cuda", generator=g, dtype=torch.int32)
+    rows[START + 1], rows[START + 6] = -1, T + 3
+    rows[:START] = rows[R - TAIL:] = T - 1
+    return rows
+
+
+def _same_finite(got, ref):
+    fin = torch.isfinite(ref)
+    assert bool((torch.isfinite(got) == fin).all()) and not bool(fin.all()) and bool(fin.any())
+    return fin
+
+
+@pytest.mark.parametrize("gathered", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("shape", FORWARD)
+def test_forward_tiles(shape, dtype, gathered):
+    E, R, N, K = _selected(M.MM_FORWARD, FORWARD[shape])
+    g = _gen(41)
+    counts = _ragged(E, R)
+    first = offsets(counts, START).cuda()
+    T = R // 2 if gathered else R
+    x, w = _normal(g, T, K, dtype=dtype), _normal(g, E, N, K, dtype=dtype)
+    rows = _numbered(g, R, T) if gathered else None
+    x[T - 1] = float("nan")
+    if not gathered:
+        x[:START], x[R - TAIL:] = float("nan"), float("inf")
+    x[T // 3, K - 1], x[T // 3 + 1, 0], x[T // 2, K // 2] = float("inf"), float("nan"), float("-inf")
+    w[0, N - 1, 0], w[0, 7, K - 1], w[1], w[2, 0, 0], w[E - 1, N // 2, K // 2] = (float("nan"),) * 5
+    ref, mag, cov = ref_mm(x, w, first, rows, R)
+    assert int(cov.sum()) == R - START - TAIL
+    for out_dtype in (dtype, FP32):
+        out = M.grouped_mm(x, w, first, rows=rows, out=torch.full((R, N), 7.5, dtype=out_dtype, device="cuda"))
+        assert bool((out[~cov] == 7.5).all())
+        fin = _same_finite(out[cov], ref[cov])
+        assert_product(out[cov][fin], ref[cov][fin], mag[cov][fin], K, shape)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("shape", DX)
+def test_row_gradient_tiles(shape, dtype):
+    E, R, N, K = _selected(M.MM_DX, DX[shape])
+    g = _gen(42)
+    first = offsets(_ragged(E, R), START).cuda()
+    dy, w = _normal(g, R, N, dtype=dtype), _normal(g, E, N, K, dtype=dtype)
+    dy[:START], dy[R - TAIL:] = float("nan"), float("inf")
+    dy[R // 3, N - 1], dy[R // 3 + 1, 0], dy[R // 2, N // 2] = float("inf"), float("nan"), float("-inf")
+    w[0, 0, K - 1], w[0, N - 1, 9], w[1], w[2, 0, 0], w[E - 1, N // 2, K // 2] = (float("nan"),) * 5
+    ref, mag, cov = ref_dx(dy, w, first)
+    for out_dtype in (dtype, FP32):
+        out = M.grouped_mm_dx(dy, w, first, out=torch.full((R, K), 7.5, dtype=out_dtype, device="cuda"))
+        assert bool((out[~cov] == 7.5).all())
+        fin = _same_finite(out[cov], ref[cov])
+        assert_product(out[cov][fin], ref[cov][fin], mag[cov][fin], N, shape)
+
+
+@pytest.mark.parametrize("gathered", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("shape", DW)
+def test_weight_gradient_tiles(shape, dtype, gathered):
+    """Each group held to its own number of terms; accumulated, to one more."""
+    E, R, N, K = _selected(M.MM_DW, DW[shape])
+    g = _gen(43)
+    counts = _ragged(E, R)
+    first = offsets(counts, START).cuda()
+    T = R // 2 if gathered else R
+    dy, x = _normal(g, R, N, dtype=dtype), _normal(g, T, K, dtype=dtype)
+    rows = _numbered(g, R, T) if gathered else None
+    dy[:START], dy[R - TAIL:], x[T - 1] = float("nan"), float("inf"), float("nan")
+    if not gathered:
+        x[:START], x[R - TAIL:] = float("inf"), float("nan")
+    last = START + counts[0] - 1                        # last row of the first group; the next begins behind it
+    dy[last, N - 1], dy[last + 1, 3], dy[R - TAIL - 1, N // 2] = float("inf"), float("nan"), float("-inf")
+    x[T // 3, K - 1], x[T // 3 + 1, 0] = float("nan"), float("inf")
+    ref, mag = ref_dw(dy, x, first, rows)
+    for out_dtype in (dtype, FP32):
+        dw = M.grouped_mm_dw(dy, x, first, rows=rows, out_dtype=out_dtype)
+        fin = _same_finite(dw, ref)
+        for e, c in enumerate(counts):
+            assert_product(dw[e][fin[e]], ref[e][fin[e]], mag[e][fin[e]], c, f"{shape}, group {e}")
+    base = torch.randn(E, N, K, device="cuda", generator=g)
+    dw = M.grouped_mm_dw(dy, x, first, rows=rows, out=base.clone(), accumulate=True)
+    _same_finite(dw, ref)
+    for e, c in enumerate(counts):
+        b = base[e].double()
+        assert_product(dw[e][fin[e]], (ref[e] + b)[fin[e]], (mag[e] + b.abs())[fin[e]], c + 1, f"{shape}, group {e}")
+
+
+def _int8_operands(g, E, R, N, K, T):
+    i8 = lambda *s: torch.randint(-128, 128, s, device="cuda", generator=g, dtype=torch.int8)  # noqa: E731
+    x, w = i8(T, K), i8(E, N, K)
+    xs, ws = torch.rand(T, device="cuda", generator=g) + 0.1, (torch.rand(E, N, device="cuda", generator=g) + 0.1) / K / 100
+    xs[T // 3], xs[T // 2] = float("nan"), float("inf")
+    ws[0, N - 1], ws[E - 1, 0] = float("nan"), float("inf")
+    return x, xs, w, ws
+
+
+@pytest.mark.parametrize("gathered", [False, True])
+@pytest.mark.parametrize("shape", INT8)
+def test_int8_tiles(shape, gathered):
+    E, R, N, K = _selected(M.MM_INT8, INT8[shape])
+    g = _gen(44)
+    first = offsets(_ragged(E, R), START).cuda()
+    T = R // 2 if gathered else R
+    x, xs, w, ws = _int8_operands(g, E, R, N, K, T)
+    rows = _numbered(g, R, T) if gathered else None
+    xs[T - 1], ws[1] = float("nan"), float("nan")
+    if not gathered:
+        xs[:START] = xs[R - TAIL:] = float("nan")
+    ref, cov = ref_int8(x, xs, w, ws, first, rows, R)
+    for out_dtype in (BF16, FP16, FP32):
+        out = M.grouped_int8_mm(x, xs, w, ws, first, rows=rows, out=torch.full((R, N), 7.5, dtype=out_dtype, device="cuda"))
+        assert bool((out[~cov] == 7.5).all())
+        fin = _same_finite(out[cov], ref[cov])
+        assert_int8(out[cov][fin], ref[cov][fin], shape)
+
+
+@pytest.mark.parametrize("shape", DENSE)
+def test_dense_int8_tiles(shape):
+    E, R, N, K = _selected(M.MM_INT8, DENSE[shape])
+    x, xs, w, ws = _int8_operands(_gen(45), E, R, N, K, R)
+    ref, _ = ref_int8(x, xs, w, ws, offsets([R]).cuda(), None, R)
+    for out_dtype in (BF16, FP32):
+        out = M.int8_mm(x, xs, w[0], ws[0], out_dtype=out_dtype)
+        fin = _same_finite(out, ref)
+        assert_int8(out[fin], ref[fin], shape)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("shape", ["64x128", "128x128", "256x128"])
+def test_one_group_tiles(shape, dtype):
+    """A single group of all rows, forward and row gradient: the sizes of the tile shapes above."""
+    R, N, K = FORWARD[shape][1:4]
+    assert M.debug_mm_plan(M.MM_FORWARD, 1, R, N, K) == FORWARD[shape][4:6] + (1,)
+    assert M.debug_mm_plan(M.MM_DX, 1, R, K, N) == FORWARD[shape][4:6] + (1,)
+    g = _gen(46)
+    first = offsets([R]).cuda()
+    x, w = _normal(g, R, K, dtype=dtype), _normal(g, 1, N, K, dtype=dtype)
+    ref, mag, _ = ref_mm(x, w, first, None, R)
+    assert_product(M.grouped_mm(x, w, first), ref, mag, K, shape)
+    wt = w.transpose(1, 2).contiguous()                 # the same product as a row gradient
+    assert_product(M.grouped_mm_dx(x, wt, first), ref, mag, K, shape)
+
+
+def test_exact_sums_in_each_shape():
+    """Integers whose sums fp32 holds exactly: every shape gives the definition's values, twice."""
+    g = _gen(47)
+    for E, R, N, K, _, _, _ in FORWARD.values():
+        ints = lambda *s: torch.randint(-3, 4, s, device="cuda", generator=g).to(BF16)  # noqa: E731
+        x, w, first = ints(R, K), ints(E, N, K), offsets(_ragged(E, R), START).cuda()
+        out = M.grouped_mm(x, w, first, out_dtype=FP32)
+        ref, _, cov = ref_mm(x, w, first, None, R)
+        assert torch.equal(out[cov].double(), ref[cov])
+        assert torch.equal(M.grouped_mm(x, w, first, out_dtype=FP32)[cov], out[cov])

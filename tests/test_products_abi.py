@@ -173,3 +173,19 @@ def test_operands_that_require_grad_are_refused_while_autograd_records():
         for off in (torch.no_grad(), torch.inference_mode()):
             with off, pytest.raises(ValueError, match="device tensor"):
                 call()
+
+
+def test_plan_query():
+    """The shape a product runs with; refused sizes as the products refuse them."""
+    L = _lib.load()
+    assert M.debug_mm_plan(M.MM_FORWARD, 384, 48, 1152, 7168) == (16, 16, 1)
+    rows, cols, splits = M.debug_mm_plan(M.MM_DW, 3, 8001, 72, 136)
+    assert (rows, cols) == (128, 128) and splits > 1
+    assert M.mm_scratch_bytes(M.MM_DW, 3, 8001, 72, 136) == splits * 3 * 72 * 136 * 4
+    for args, code in [((0, 4, 64, 64, 64), M.MOE_EINVAL), ((9, 4, 64, 64, 64), M.MOE_EINVAL), ((1, 4, 0, 64, 64), M.MOE_EINVAL),
+                       ((1, 4, 64, 60, 64), M.MOE_EUNSUPPORTED), ((4, 4, 64, 64, 24), M.MOE_EUNSUPPORTED)]:
+        with pytest.raises(M.MoeError, match="moe_debug_mm_plan") as e:
+            M.debug_mm_plan(*args)
+        assert e.value.code == code
+    one = C.c_int()
+    assert L.moe_debug_mm_plan(M.MM_DX, 4, 64, 64, 64, C.byref(one), None, C.byref(one)) == M.MOE_EINVAL
