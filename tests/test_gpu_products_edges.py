@@ -386,3 +386,87 @@ def test_exact_sums_in_each_shape():
         ref, _, cov = ref_mm(x, w, first, None, R)
         assert torch.equal(out[cov].double(), ref[cov])
         assert torch.equal(M.grouped_mm(x, w, first, out_dtype=FP32)[cov], out[cov])
+
+
+# ---- rows past 4 GiB
+
+def test_gathered_rows_past_4_gib():
+    """Row numbers whose bytes begin past 2^32, in products of a few rows (streamed, and weight gradients) and
+    of many (tiles). Values are integers up to 3 in magnitude and sums stay below 2^24, so results are exact in
+    fp32 and compared with equality; the row that each number would name with its byte offset cut to 32 bits
+    holds other values, whose result is not the same."""
+    g = _gen(51)
+    K, N = 4096, 72
+    T = 530001                                        # x of 4.34e9 bytes
+    x = torch.randint(-3, 4, (T, K), device="cuda", generator=g, dtype=torch.int8).to(BF16)
+    wrapped = 2 ** 32 // (2 * K)                      # rows in 4 GiB
+    for R in (7, 700):
+        rows = torch.randint(wrapped + 1, T, (R,), device="cuda", generator=g, dtype=torch.int32)
+        rows[0], rows[-1] = T - 1, wrapped
+        first = offsets([R - 3, 3]).cuda()
+        ints = lambda *s: torch.randint(-3, 4, s, device="cuda", generator=g).to(BF16)  # noqa: E731
+        w, dy = ints(2, N, K), ints(R, N)
+        far, near = x[rows.long()], x[rows.long() - wrapped]
+        ref, other = (ref_mm(t, w, first, None, R)[0] for t in (far, near))
+        assert bool((ref != other).any(1).all())      # a cut offset changes every row
+        assert torch.equal(M.grouped_mm(x, w, first, rows=rows, out_dtype=FP32).double(), ref)
+        ref, other = (ref_dw(dy, t, first, None)[0] for t in (far, near))
+        assert bool((ref != other).flatten(1).any(1).all())
+        assert torch.equal(M.grouped_mm_dw(dy, x, first, rows=rows, out_dtype=FP32).double(), ref)
+
+
+def test_rows_in_order_past_4_gib():
+    """The same without row numbers: groups at the end of an x, a dy and an output past 4 GiB."""
+    g = _gen(52)
+    K, N, R = 4096, 72, 530001
+    big = torch.randint(-3, 4, (R, K), device="cuda", generator=g, dtype=torch.int8).to(BF16)
+    ints = lambda *s: torch.randint(-3, 4, s, device="cuda", generator=g).to(BF16)  # noqa: E731
+    small, w = ints(R, N), ints(3, N, K)
+    first = offsets([R - 307, 300, 7]).cuda()
+    end, cut = slice(R - 307, R), offsets([0, 300, 7]).cuda()
+    out = M.grouped_mm(big, w, first, out_dtype=FP32)
+    assert torch.equal(out[end].double(), ref_mm(big[end], w, cut, None, 307)[0])
+    dx = M.grouped_mm_dx(small, w, first)             # sums up to 648: bf16 rounds them, half a step each
+    ref, mag, _ = ref_dx(small[end], w, cut)
+    assert_product(dx[end], ref, mag, N)
+    dw = M.grouped_mm_dw(small, big, first, out_dtype=FP32)
+    assert torch.equal(dw[1:].double(), ref_dw(small[end], big[end], cut, None)[0][1:])
+    wt = w.transpose(1, 2).contiguous()               # the forward product as a row gradient: a dy past 4 GiB
+    dx = M.grouped_mm_dx(big, wt, first, out_dtype=FP32)
+    assert torch.equal(dx[end].double(), ref_mm(big[end], w, cut, None, 307)[0])
+
+
+def test_gathered_int8_rows_past_4_gib():
+    g = _gen(53)
+    K, N, T = 4096, 72, 1060001
+    i8 = lambda *s: torch.randint(-128, 128, s, device="cuda", generator=g, dtype=torch.int8)  # noqa: E731
+    x, wrapped = i8(T, K), 2 ** 32 // K
+    xs = torch.rand(T, device="cuda", generator=g) + 0.1
+    for R in (7, 700):
+        w, ws = i8(2, N, K), (torch.rand(2, N, device="cuda", generator=g) + 0.1) / K
+        rows = torch.randint(wrapped + 1, T, (R,), device="cuda", generator=g, dtype=torch.int32)
+        rows[0], rows[-1] = T - 1, wrapped
+        first = offsets([R - 3, 3]).cuda()
+        at = rows.long()
+        ref = ref_int8(x[at], xs[at], w, ws, first, None, R)[0]
+        assert_int8(M.grouped_int8_mm(x, xs, w, ws, first, rows=rows, out_dtype=FP32), ref)
+        with pytest.raises(AssertionError):           # the bound tells the row 4 GiB before apart
+            assert_int8(ref_int8(x[at - wrapped], xs[at], w, ws, first, None, R)[0].float(), ref)
+
+
+@pytest.mark.parametrize("gathered", [False, True])
+def test_weight_gradient_is_held_to_each_groups_own_rows(gathered):
+    """Rows outside the groups hold infinities and NaNs; a group's bound counts its own rows."""
+    counts, start, tail, N, K = [5, 0, 70, 140, 1], 3, 9, 72, 40
+    g = _gen(54)
+    R = start + sum(counts) + tail
+    first = offsets(counts, start).cuda()
+    x, dy = _normal(g, R + 1, K), _normal(g, R, N)
+    x[:start], x[R - tail:], dy[:start], dy[R - tail:] = float("nan"), float("inf"), float("inf"), float("nan")
+    rows = torch.randint(start, R - tail, (R,), device="cuda", generator=g, dtype=torch.int32) if gathered else None
+    if gathered:
+        rows[:start] = rows[R - tail:] = R
+    dw = M.grouped_mm_dw(dy, x if gathered else x[:R], first, rows=rows)
+    ref, mag = ref_dw(dy, x if gathered else x[:R], first, rows)
+    for e, c in enumerate(counts):
+        assert_product(dw[e], ref[e], mag[e], c)
