@@ -32,7 +32,7 @@ struct MmElem<MM_I8> {
   }
 };
 
-// Eight or four consecutive results (16- or 8-byte aligned in the output's type).
+// Two results in one register, each rounded to nearest even.
 template <int OUT>
 __device__ __forceinline__ uint32_t mm_pack(float lo, float hi) {
   if (OUT == MM_BF16) return pack_bf16x2(lo, hi);
@@ -55,6 +55,7 @@ __device__ __forceinline__ void mm_store_f32(const MmArgs &a, long at, v4f r) {
   mm_store<NT>(o, r);
 }
 
+// Four or eight consecutive results (8- or 16-byte aligned in the output's type).
 template <int OUT>
 __device__ __forceinline__ void mm_store4(const MmArgs &a, long at, const float *v) {
   if (OUT == MM_FP32) mm_store_f32(a, at, v4f{v[0], v[1], v[2], v[3]});
@@ -793,11 +794,12 @@ MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
   // 2048 x 2048: 45, 50; but 32 groups of 512, 1024 x 6144: 282, 251).
   if (op == MM_DW && R <= 256 * E) m.shape = 2;
   // Too few tiles for the chip: the reduction is split into as many parts as take
-  // least time.  A step takes 0.6 us (1 us with transposed reads of both operands),
-  // all blocks' steps what their loads take at 12 TB/s; the second launch, which
-  // joins the parts in order, 4 us, and their bytes twice at 4 TB/s (R = 256,
-  // N = 1024, K = 4096: 15.2 us, 41.3 us whole; int8, R = 500, N = 4608, K = 7168:
-  // 45.4 us in parts that fill the chip, 39.6 whole).
+  // least time.  The estimate is fitted to whole and split times: a step takes 0.6 us
+  // (1 us with transposed reads of both operands), all blocks' steps no less than
+  // their loads at 12 TB/s (not a bound: full rounds of blocks fill LDS at 14 to 16);
+  // the second launch, which joins the parts in order, 4 us, and their bytes twice at
+  // 4 TB/s (R = 256, N = 1024, K = 4096: 15.2 us, 41.3 us whole; int8, R = 500,
+  // N = 4608, K = 7168: 45.4 us in parts that fill the chip, 39.6 whole).
   const auto &shape = kMmShapes[m.shape];
   m.rows = shape.bq, m.cols = shape.bp;
   const long steps = op == MM_FORWARD ? K * item / 128 : op == MM_DX ? N / 64 : R / E / 64;

@@ -339,8 +339,8 @@ int moe_plan_set_activation(moe_plan_t plan, int act);
  *
  * Matrices are row-major and contiguous, 16-byte aligned; N and K are
  * multiples of 8 (K of 16 for the integer products) up to 2^20, E 1 .. 1024,
- * R up to 2^30.  What a call writes may not overlap what it reads; an x of no
- * rows may be NULL.  Sums are kept in fp32 (exact int32 for integers) and, with
+ * R up to 2^30 (a launch of more than 2^23 - 1 tiles is refused with MOE_EHIP).  What
+ * a call writes may not overlap what it reads; an x of no rows may be NULL.  Sums are kept in fp32 (exact int32 for integers) and, with
  * their scales for integers, rounded to nearest even once on output.  Every sum
  * has a fixed order: results repeat bit for bit.
  * All calls are stream-ordered, neither allocate nor synchronise, and may be
