@@ -195,15 +195,20 @@ def test_overwriting_a_saved_tensor_is_reported_by_backward():
 
 FORWARD = {"64x128": (5, 900, 1048, 200, 64, 128, False), "128x128": (5, 2900, 3080, 200, 128, 128, False),
            "128x256": (40, 5000, 4104, 136, 128, 256, False), "256x128": (5, 3000, 4104, 200, 256, 128, False),
-           "split": (5, 400, 264, 4104, 64, 128, True), "stream": (5, 75, 264, 520, 16, 16, False)}
+           "split": (5, 400, 264, 4104, 64, 128, True), "stream": (5, 75, 264, 520, 16, 16, False),
+           "130 groups": (130, 9000, 136, 200, 64, 128, False), "1000 groups": (1000, 9000, 264, 136, 64, 128, False),
+           "split of 100 groups": (100, 6500, 72, 4104, 64, 128, True)}
 DX = {"64x128": (5, 900, 200, 1048, 64, 128, False), "128x128": (5, 2900, 200, 3080, 128, 128, False),
       "128x256": (40, 5000, 136, 4104, 128, 256, False), "256x128": (5, 3000, 200, 4104, 256, 128, False),
-      "split": (5, 300, 2600, 264, 64, 128, True)}
+      "split": (5, 300, 2600, 264, 64, 128, True), "130 groups": (130, 9000, 200, 136, 64, 128, False),
+      "1000 groups": (1000, 9000, 136, 264, 64, 128, False), "split of 100 groups": (100, 6500, 4104, 72, 64, 128, True)}
 DW = {"128x128": (8, 1200, 520, 1048, 128, 128, False), "256x128": (4, 1100, 2056, 1544, 256, 128, False),
-      "split": (3, 8040, 72, 136, 128, 128, True)}
+      "split": (3, 8040, 72, 136, 128, 128, True), "1000 groups": (1000, 3000, 72, 40, 128, 128, False)}
 INT8 = {"64x128": (5, 900, 1048, 400, 64, 128, False), "128x128": (5, 2900, 3080, 400, 128, 128, False),
         "128x256": (40, 5000, 4104, 272, 128, 256, False), "256x128": (5, 3000, 4104, 400, 256, 128, False),
-        "split": (5, 400, 264, 8208, 64, 128, True), "stream": (5, 75, 264, 1040, 16, 16, False)}
+        "split": (5, 400, 264, 8208, 64, 128, True), "stream": (5, 75, 264, 1040, 16, 16, False),
+        "130 groups": (130, 9000, 136, 400, 64, 128, False), "1000 groups": (1000, 9000, 264, 272, 64, 128, False),
+        "split of 100 groups": (100, 6500, 72, 8208, 64, 128, True)}
 DENSE = {"64x128": (1, 900, 1048, 400, 64, 128, False), "128x128": (1, 2900, 3080, 400, 128, 128, False),
          "128x256": (1, 1876, 8200, 272, 128, 256, False), "256x128": (1, 3000, 4104, 400, 256, 128, False)}
 START, TAIL = 3, 5
@@ -470,3 +475,23 @@ def test_weight_gradient_is_held_to_each_groups_own_rows(gathered):
     ref, mag = ref_dw(dy, x if gathered else x[:R], first, rows)
     for e, c in enumerate(counts):
         assert_product(dw[e], ref[e], mag[e], c)
+
+
+# ---- grouping
+
+@pytest.mark.parametrize("T,k,E", [(262144, 1, 1024), (262145, 1, 7), (70001, 8, 384), (9001, 64, 1)])
+def test_group_routes_of_several_rounds_a_block(T, k, E):
+    """At most 262144 routes fit one round of 1024 a block: below, at and past it."""
+    g = _gen(T)
+    ids = torch.randint(-2, E + 2, (T, k), device="cuda", generator=g, dtype=torch.int32)
+    ids[T // 2] = 2 ** 31 - 1
+    flat = ids.flatten().long().cpu()
+    key = torch.where((flat >= 0) & (flat < E), flat, E)
+    keys, order = torch.sort(key, stable=True)
+    n = int((key < E).sum())
+    first, got, token, inverse = (t.cpu() for t in M.group_routes(ids, E))
+    assert torch.equal(first.long(), torch.searchsorted(keys, torch.arange(E + 1)))
+    assert torch.equal(got[:n].long(), order[:n]) and torch.equal(token[:n].long(), order[:n] // k)
+    assert bool((got[n:] == -1).all()) and bool((token[n:] == -1).all())
+    want = torch.full((T * k,), -1).scatter(0, order[:n], torch.arange(n))
+    assert torch.equal(inverse.flatten().long(), want)
