@@ -16,6 +16,15 @@ products over rows sorted by expert:
     dw = grouped_mm_dw(dy, x, first, rows=token, out_dtype=torch.float32)
     xq, xs = quant_int8(x)
     y = grouped_int8_mm(xq, xs, wq, ws, first, rows=token)
+
+The gated block in front of the down product is one call each way, and runs on 8-bit
+floating-point experts too:
+
+    h, pre = grouped_glu(x, w13, first, rows=token, keep_pre=True)     # [T * top_k, I]
+    d_pre, h = grouped_glu_dx(dy, w2, pre, first, keep_h=True)         # dy of w13's product
+    xq, xs = quant_fp8(x)
+    h = grouped_fp8_glu(xq, xs, w13q, s13, first, rows=token)
+    y = grouped_fp8_mm(*quant_fp8(h), w2q, s2, first)
 """
 from __future__ import annotations
 
@@ -40,7 +49,7 @@ NSLOTS = len(RACE_SLOTS)
 
 
 T_BF16, T_FP16, T_FP32 = 1, 2, 3
-MM_FORWARD, MM_DX, MM_DW, MM_INT8 = 1, 2, 3, 4
+MM_FORWARD, MM_DX, MM_DW, MM_INT8, MM_GLU, MM_GLU_DX, MM_FP8, MM_FP8_GLU = 1, 2, 3, 4, 5, 6, 7, 8
 
 
 class MoeError(RuntimeError):
@@ -357,7 +366,7 @@ def _bind():
             raise ImportError("block_scaled_fp4_histogram_amd/_products.so is missing or was built for another torch: "
                               "build it with block_scaled_fp4_histogram_amd/build.py (or __graft_entry__.build())") from e
         names = [n for n in _lib.SIGNATURES if n.startswith(("moe_grouped", "moe_mm", "moe_quant", "moe_int8", "moe_group_",
-                                                             "moe_last_error"))]
+                                                             "moe_glu", "moe_last_error"))]
         b.bind({n: C.cast(getattr(L, n), C.c_void_p).value for n in names}, MoeError, torch._C._cuda_getCurrentRawStream)
         _binding = b
     return _binding
@@ -372,7 +381,8 @@ def _use(stream, t):
 
 
 def mm_scratch_bytes(op: int, E: int, R: int, N: int, K: int) -> int:
-    """Scratch bytes of a product (moe_mm_scratch_bytes): op MM_FORWARD, MM_DX, MM_DW or MM_INT8."""
+    """Scratch bytes of a product (moe_mm_scratch_bytes): op MM_FORWARD, MM_DX, MM_DW, MM_INT8, MM_GLU (N: the
+    block's I), MM_GLU_DX (K: the block's I), MM_FP8 or MM_FP8_GLU (N: the block's I)."""
     return _lib.load().moe_mm_scratch_bytes(op, E, R, N, K)
 
 
@@ -449,6 +459,125 @@ def grouped_int8_mm(x, x_scales, w, w_scales, first, rows=None, out=None, out_dt
     return (_binding or _bind()).grouped_int8_mm(x, x_scales, w, w_scales, first, rows, out, out_dtype, scratch)
 
 
+# A gated block's form, in the calls below: h = act(gate, up) of its two projections. activation ACT_SWIGLU is
+# g sigmoid(alpha g) (u + beta) with g = min(gate, limit), u = clamp(up, -limit, limit) (limit None: no clamp);
+# ACT_SITU is silu(4 tanh(gate / 4)) 25 tanh(up / 25), without a limit, alpha or beta. layout says which branch
+# comes first in the rows of w and in the columns of the projections: W13_UP_GATE or W13_GATE_UP.
+
+
+def glu(x, w, activation: int = ACT_SWIGLU, limit: Optional[float] = None, alpha: float = 1.0, beta: float = 0.0,
+        layout: int = W13_UP_GATE, keep_pre: bool = False, out=None, out_dtype=None, pre=None, scratch=None, stream=None):
+    """A gated block's projections and activation in one product (moe_grouped_glu): h = act(x @ w.T).
+
+    x [T, K] and w [2 I, K] bf16 or fp16; h [T, I] in x's type or fp32. keep_pre, or a given pre, returns
+    (h, pre): the projections x @ w.T [T, 2 I] in x's type, for glu_dx or glu_grad."""
+    if stream is not None:
+        with _use(stream, x):
+            return glu(x, w, activation, limit, alpha, beta, layout, keep_pre, out, out_dtype, pre, scratch)
+    return (_binding or _bind()).glu(x, w, activation, limit, alpha, beta, layout, keep_pre, out, out_dtype, pre, scratch)
+
+
+def grouped_glu(x, w, first, rows=None, activation: int = ACT_SWIGLU, limit: Optional[float] = None, alpha: float = 1.0,
+                beta: float = 0.0, layout: int = W13_UP_GATE, keep_pre: bool = False, out=None, out_dtype=None, pre=None,
+                scratch=None, stream=None):
+    """glu over ragged groups (moe_grouped_glu): w [E, 2 I, K], first and rows as in grouped_mm; h [R, I],
+    pre [R, 2 I]. Rows in no group keep what out and pre held (unset in new tensors)."""
+    if stream is not None:
+        with _use(stream, x):
+            return grouped_glu(x, w, first, rows, activation, limit, alpha, beta, layout, keep_pre, out, out_dtype, pre, scratch)
+    return (_binding or _bind()).grouped_glu(x, w, first, rows, activation, limit, alpha, beta, layout, keep_pre, out,
+                                             out_dtype, pre, scratch)
+
+
+def glu_dx(dy, w, pre, activation: int = ACT_SWIGLU, limit: Optional[float] = None, alpha: float = 1.0, beta: float = 0.0,
+           layout: int = W13_UP_GATE, keep_h: bool = False, out=None, h=None, scratch=None, stream=None):
+    """A gated block's backward pass from its down product to its projections (moe_grouped_glu_dx):
+    d_pre = (dy @ w) times the activation's gradient at pre.
+
+    dy [T, N], w [N, I] (the down weights) and pre [T, 2 I] (glu's) bf16 or fp16; d_pre [T, 2 I] in that
+    type. keep_h, or a given h, returns (d_pre, h): the activation [T, I] once more. The gradients of glu's
+    x and w are those of a product with dy = d_pre (grouped_mm_dx, grouped_mm_dw)."""
+    if stream is not None:
+        with _use(stream, dy):
+            return glu_dx(dy, w, pre, activation, limit, alpha, beta, layout, keep_h, out, h, scratch)
+    return (_binding or _bind()).glu_dx(dy, w, pre, activation, limit, alpha, beta, layout, keep_h, out, h, scratch)
+
+
+def grouped_glu_dx(dy, w, pre, first, activation: int = ACT_SWIGLU, limit: Optional[float] = None, alpha: float = 1.0,
+                   beta: float = 0.0, layout: int = W13_UP_GATE, keep_h: bool = False, out=None, h=None, scratch=None,
+                   stream=None):
+    """glu_dx over ragged groups (moe_grouped_glu_dx): w [E, N, I], first as in grouped_mm. Rows in no group
+    keep what out and h held (unset in new tensors)."""
+    if stream is not None:
+        with _use(stream, dy):
+            return grouped_glu_dx(dy, w, pre, first, activation, limit, alpha, beta, layout, keep_h, out, h, scratch)
+    return (_binding or _bind()).grouped_glu_dx(dy, w, pre, first, activation, limit, alpha, beta, layout, keep_h, out, h,
+                                                scratch)
+
+
+def glu_grad(dh, pre, activation: int = ACT_SWIGLU, limit: Optional[float] = None, alpha: float = 1.0, beta: float = 0.0,
+             layout: int = W13_UP_GATE, keep_h: bool = False, out=None, h=None, stream=None):
+    """The same from a gradient dh [T, I] of the activation itself (moe_glu_grad), for every row."""
+    if stream is not None:
+        with _use(stream, dh):
+            return glu_grad(dh, pre, activation, limit, alpha, beta, layout, keep_h, out, h)
+    return (_binding or _bind()).glu_grad(dh, pre, activation, limit, alpha, beta, layout, keep_h, out, h)
+
+
+def quant_fp8(x, out=None, scales=None, stream=None):
+    """Rows of a bf16 or fp16 [rows, cols] tensor to 8-bit floating point with one fp32 scale for each 128
+    columns (moe_quant_fp8): (codes float8_e4m3fn [rows, cols], scales [rows, ceil(cols / 128)])."""
+    if stream is not None:
+        with _use(stream, x):
+            return quant_fp8(x, out, scales)
+    return (_binding or _bind()).quant_fp8(x, out, scales)
+
+
+def fp8_mm(x, x_scales, w, w_scales, out=None, out_dtype=None, scratch=None, stream=None):
+    """8-bit floating-point product with a scale for each block of 128 (moe_grouped_fp8_mm): x and w times
+    their scales, x @ w.T, the sums in 32 bits.
+
+    x float8_e4m3fn [M, K], x_scales fp32 [M, ceil(K / 128)], w float8_e4m3fn [N, K], w_scales fp32
+    [ceil(N / 128), ceil(K / 128)]; out [M, N] bf16 (default), fp16 or fp32."""
+    if stream is not None:
+        with _use(stream, x):
+            return fp8_mm(x, x_scales, w, w_scales, out, out_dtype, scratch)
+    return (_binding or _bind()).fp8_mm(x, x_scales, w, w_scales, out, out_dtype, scratch)
+
+
+def grouped_fp8_mm(x, x_scales, w, w_scales, first, rows=None, out=None, out_dtype=None, scratch=None, stream=None):
+    """fp8_mm over ragged groups (moe_grouped_fp8_mm): w [E, N, K], w_scales [E, ceil(N / 128), ceil(K / 128)],
+    first and rows as in grouped_mm; x_scales belongs to the rows of x."""
+    if stream is not None:
+        with _use(stream, x):
+            return grouped_fp8_mm(x, x_scales, w, w_scales, first, rows, out, out_dtype, scratch)
+    return (_binding or _bind()).grouped_fp8_mm(x, x_scales, w, w_scales, first, rows, out, out_dtype, scratch)
+
+
+def fp8_glu(x, x_scales, w, w_scales, activation: int = ACT_SWIGLU, limit: Optional[float] = None, alpha: float = 1.0,
+            beta: float = 0.0, layout: int = W13_UP_GATE, out=None, out_dtype=None, scratch=None, stream=None):
+    """glu on 8-bit floating-point operands (moe_grouped_fp8_glu): x and x_scales as in fp8_mm, w float8_e4m3fn
+    [2 I, K], w_scales fp32 [2, ceil(I / 128), ceil(K / 128)] by branch; h [M, I] bf16 (default), fp16 or fp32."""
+    if stream is not None:
+        with _use(stream, x):
+            return fp8_glu(x, x_scales, w, w_scales, activation, limit, alpha, beta, layout, out, out_dtype, scratch)
+    return (_binding or _bind()).fp8_glu(x, x_scales, w, w_scales, activation, limit, alpha, beta, layout, out, out_dtype,
+                                         scratch)
+
+
+def grouped_fp8_glu(x, x_scales, w, w_scales, first, rows=None, activation: int = ACT_SWIGLU,
+                    limit: Optional[float] = None, alpha: float = 1.0, beta: float = 0.0, layout: int = W13_UP_GATE,
+                    out=None, out_dtype=None, scratch=None, stream=None):
+    """fp8_glu over ragged groups (moe_grouped_fp8_glu): w [E, 2 I, K], w_scales [E, 2, ceil(I / 128),
+    ceil(K / 128)], first and rows as in grouped_mm."""
+    if stream is not None:
+        with _use(stream, x):
+            return grouped_fp8_glu(x, x_scales, w, w_scales, first, rows, activation, limit, alpha, beta, layout, out,
+                                   out_dtype, scratch)
+    return (_binding or _bind()).grouped_fp8_glu(x, x_scales, w, w_scales, first, rows, activation, limit, alpha, beta,
+                                                 layout, out, out_dtype, scratch)
+
+
 def group_routes(topk_ids, num_experts: int, scratch=None, stream=None):
     """The routes of a batch sorted by expert (moe_group_routes), for grouped_mm and its kin.
 
@@ -464,7 +593,7 @@ def group_routes(topk_ids, num_experts: int, scratch=None, stream=None):
 
 def debug_mm_plan(op: int, E: int, R: int, N: int, K: int):
     """(rows and columns of an output tile, parts of the reduction) a product of these sizes runs with
-    (moe_debug_mm_plan); op as in mm_scratch_bytes. (16, 16, 1): streamed weights."""
+    (moe_debug_mm_plan); op as in mm_scratch_bytes. (16, 16, 1), for a gated block (16, 8, 1): streamed weights."""
     v = [C.c_int() for _ in range(3)]
     _check(_lib.load().moe_debug_mm_plan(op, E, R, N, K, *map(C.byref, v)))
     return tuple(x.value for x in v)

@@ -49,11 +49,22 @@ SIGNATURES = {
     "moe_quant_int8": (_i, [_i, _vp, _i, _i, _vp, _vp, _vp]),
     "moe_int8_mm": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "moe_grouped_int8_mm": (_i, [_vp, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "moe_grouped_glu": (_i, [_i, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
+    "moe_grouped_glu_dx": (_i, [_i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_glu_grad": (_i, [_i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp]),
+    "moe_quant_fp8": (_i, [_i, _vp, _i, _i, _vp, _vp, _vp]),
+    "moe_grouped_fp8_mm": (_i, [_vp, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "moe_grouped_fp8_glu": (_i, [_vp, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _vp, _vp, _sz, _vp]),
     "moe_debug_route": (_i, [_vp, _vp, _i, _vp, _i, _vp, _sz, _vp, _vp, _vp, _vp, _vp]),
     "moe_debug_mm_plan": (_i, [_i, _i, _i, _i, _i, C.POINTER(_i), C.POINTER(_i), C.POINTER(_i)]),
     "moe_debug_quant_mxfp8_bf16": (_i, [_vp, _i, _i, _vp, _vp, _vp]),
     "moe_debug_quant_mxfp8_f32": (_i, [_vp, _i, _i, _vp, _vp, _vp]),
 }
+
+
+class GluForm(C.Structure):
+    _fields_ = [("activation", C.c_int), ("layout", C.c_int), ("limit", C.c_float), ("alpha", C.c_float),
+                ("beta", C.c_float)]
 
 
 class MoeTier(C.Structure):

@@ -11,6 +11,7 @@ LIB = os.path.join(PKG, "libmoe_gfx950.so")
 SOURCES = [os.path.join(CSRC, "moe_kernels.hip"), os.path.join(CSRC, "moe_decode.hip"),
            os.path.join(CSRC, "moe_prefill.hip"), os.path.join(CSRC, "moe_static.hip"),
            os.path.join(CSRC, "moe_mm.hip"), os.path.join(CSRC, "moe_rows.hip"),
+           os.path.join(CSRC, "moe_glu.hip"), os.path.join(CSRC, "moe_fp8.hip"),
            os.path.join(CSRC, "moe_api.cpp"), os.path.join(CSRC, "moe_mm_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,72 @@
+// Products over 8-bit floating point (E4M3) with a scale for each block of 128 for
+// gfx950, alone and as a gated block, and the quantiser of their rows.
+#include <algorithm>
+
+#include "moe_mm_tile.h"
+
+namespace moe {
+
+// fp32 results are summed in fp32 throughout, in tiles whose operands fit the registers twice.
+template <int OP>
+static hipError_t launch_fp8_tiles(const MmArgs &a, int shape, hipStream_t s) {
+  if (a.out_type == MM_FP32)
+    return shape == 3 ? launch_tile<OP, MM_F8X, 64, 128, 2, 2, 3>(a, s) : launch_tile<OP, MM_F8X, 128, 128, 2, 2, 2>(a, s);
+  switch (shape) {
+    case 0: return launch_tile<OP, MM_F8, 256, 128, OP == MM_GLU ? 4 : 2, OP == MM_GLU ? 1 : 2, 2>(a, s);
+    case 1: return launch_tile<OP, MM_F8, 128, 256, 2, 2, 2>(a, s);
+    case 2: return launch_tile<OP, MM_F8, 128, 128, 2, 2, 3>(a, s);
+    default: return launch_tile<OP, MM_F8, 64, 128, 2, 2, 4>(a, s);
+  }
+}
+
+hipError_t launch_fp8(const MmArgs &a, const MmPlan &m, hipStream_t s) {
+  if (a.op == MM_GLU) return m.stream ? launch_stream<MM_GLU, MM_F8X>(a, s) : launch_fp8_tiles<MM_GLU>(a, m.shape, s);
+  return m.stream ? launch_stream<MM_FORWARD, MM_F8X>(a, s) : launch_fp8_tiles<MM_FORWARD>(a, m.shape, s);
+}
+
+// ------------------------------------------------------------ quantiser
+
+// Sixteen lanes a block of 128 columns, eight values a lane: the block's largest
+// magnitude by its bits (which order as the values do, infinities and NaN above
+// all), then the codes of x * fp32(448 / amax).  Blocks too small for that factor
+// to stay in range are worked 2^64 larger, which is exact.  A block that holds an
+// infinity or NaN gets scale NaN and codes 0, so its products are NaN.
+template <int TYPE>
+__global__ __launch_bounds__(256) void k_quant_fp8(const uint16_t *x, long units, int kbs, int cols, uint8_t *q, float *scales) {
+  typedef uint16_t v2us __attribute__((ext_vector_type(2)));
+  const int l = threadIdx.x & 15;
+  for (long u = (long)blockIdx.x * 16 + (threadIdx.x >> 4); u < units; u += (long)gridDim.x * 16) {
+    const long row = u / kbs;
+    const int c = (int)(u - row * kbs) * 128 + l * 8;
+    v4i v = {0, 0, 0, 0};
+    if (c < cols) v = *(const v4i *)(x + row * cols + c);
+    v2us mm = {0, 0};
+#pragma unroll
+    for (int d = 0; d < 4; d++) mm = __builtin_elementwise_max(mm, __builtin_bit_cast(v2us, (uint32_t)v[d] & 0x7FFF7FFFu));
+    const uint32_t m = row16_max(max((uint32_t)mm[0], (uint32_t)mm[1]));
+    const bool bad = m >= (TYPE == MM_BF16 ? 0x7F80u : 0x7C00u);
+    const float amax = glu_elem<TYPE>(m, 0), up = amax < 0x1p-100f ? 0x1p64f : 1.0f;
+    const float r = m == 0 || bad ? 0.0f : 448.0f / (amax * up);
+    if (l == 0) scales[u] = bad ? __uint_as_float(0x7FC00000u) : amax / 448.0f;
+    uint32_t o[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      float f[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++) f[k] = glu_elem<TYPE>(v[2 * h + (k >> 1)], k & 1) * up * r;
+      o[h] = e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16;
+    }
+    if (c < cols) *(v2u *)(q + row * cols + c) = bad ? v2u{0, 0} : v2u{o[0], o[1]};
+  }
+}
+
+hipError_t launch_quant_fp8(int type, const void *x, long rows, int cols, uint8_t *q, float *scales, hipStream_t s) {
+  const int kbs = (cols + kF8Block - 1) / kF8Block;
+  const long units = rows * kbs;
+  const dim3 grid((unsigned)std::min((units + 15) / 16, 1l << 20)), threads(256);
+  if (type == MM_BF16) hipLaunchKernelGGL(k_quant_fp8<MM_BF16>, grid, threads, 0, s, (const uint16_t *)x, units, kbs, cols, q, scales);
+  else hipLaunchKernelGGL(k_quant_fp8<MM_FP16>, grid, threads, 0, s, (const uint16_t *)x, units, kbs, cols, q, scales);
+  return hipGetLastError();
+}
+
+}  // namespace moe

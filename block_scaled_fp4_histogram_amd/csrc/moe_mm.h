@@ -1,5 +1,6 @@
-// Internal declarations of the ragged expert products, the 8-bit integer
-// products, the row quantiser and the route grouping (moe_mm.hip, moe_rows.hip).
+// Internal declarations of the ragged expert products, the 8-bit integer and
+// floating-point products, the gated block, the row quantisers and the route
+// grouping (moe_mm.hip, moe_glu.hip, moe_fp8.hip, moe_rows.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -8,8 +9,19 @@
 
 namespace moe {
 
-enum MmType { MM_BF16 = 1, MM_FP16 = 2, MM_FP32 = 3, MM_I8 = 4 };
-enum MmOp { MM_FORWARD = 1, MM_DX = 2, MM_DW = 3 };
+enum MmType { MM_BF16 = 1, MM_FP16 = 2, MM_FP32 = 3, MM_I8 = 4, MM_F8 = 5, MM_F8X = 6 };
+// (MM_F8X: the same operands as MM_F8, summed without its matrix instruction's cut.)
+// MM_GLU: a forward product with the gate's and the up branch's rows of w, N of each,
+// then the activation; MM_GLU_DX: MM_DX, then the activation's gradient.
+enum MmOp { MM_FORWARD = 1, MM_DX = 2, MM_DW = 3, MM_GLU = 4, MM_GLU_DX = 5 };
+
+// The activation of a gated block of I columns, and where its branches lie in rows
+// (of w) or columns (of the projections) of 2 I: gate0 and up0 are 0 and I or I and 0.
+struct GluForm {
+  int act, has_limit;
+  float limit, alpha, beta;
+  int gate0, up0;
+};
 
 // One product over E groups of rows; group e holds rows first[e] .. first[e+1]
 // (first == NULL: one group of R rows).  Every kernel clamps the offsets to
@@ -23,10 +35,14 @@ struct MmArgs {
   long x_rows;                       // rows of x (checked against `rows` on the device)
   const int32_t *first;
   int E, R, N, K;
-  const float *x_scales, *w_scales;  // MM_I8: per row of x, per channel [E, N]
-  void *out;                         // [R, N], [R, K] or [E, N, K]
+  const float *x_scales, *w_scales;  // MM_I8: per row of x, per channel [E, N]; MM_F8 and MM_F8X: per block of 128
+  void *out;                         // [R, N], [R, K] or [E, N, K]; MM_GLU_DX: the projections' gradient [R, 2 K]
   float *part;                       // scratch of a split reduction: [splits] of out in 32 bits
   int splits;                        // set by launch_mm
+  GluForm glu;                       // MM_GLU, MM_GLU_DX
+  const void *pre;                   // MM_GLU_DX: the projections [R, 2 K]
+  void *pre_out;                     // MM_GLU: the projections [R, 2 N], or NULL
+  void *h;                           // MM_GLU_DX: the activation [R, K], or NULL
 };
 
 // How a product of these sizes runs: by streaming or in tiles of a shape, with
@@ -40,6 +56,16 @@ struct MmPlan {
 MmPlan mm_plan(int op, int type, long E, long R, long N, long K);
 
 hipError_t launch_mm(const MmArgs &a, hipStream_t s);
+// The same for MM_GLU and MM_GLU_DX of 16-bit operands, and for MM_F8, under plan m.
+hipError_t launch_glu(const MmArgs &a, const MmPlan &m, hipStream_t s);
+hipError_t launch_fp8(const MmArgs &a, const MmPlan &m, hipStream_t s);
+
+// The activation's gradient from dh [R, I] alone.
+hipError_t launch_glu_grad(int type, const void *dh, const void *pre, long R, int I, const GluForm &f, void *d_pre,
+                           void *h, hipStream_t s);
+
+// Quantiser to E4M3: blocks of 128 columns of a row, scale = fp32(amax / 448).
+hipError_t launch_quant_fp8(int type, const void *x, long rows, int cols, uint8_t *q, float *scales, hipStream_t s);
 
 // Row quantiser: scale = fp32(amax / 127), codes = x / scale to nearest even.
 hipError_t launch_quant_int8(int type, const void *x, long rows, int cols, int8_t *q, float *scales, hipStream_t s);

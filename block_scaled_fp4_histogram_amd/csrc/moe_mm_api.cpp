@@ -1,5 +1,7 @@
-// C ABI of the ragged expert products, the 8-bit integer products and the
-// route grouping (declared in include/moe.h): argument validation and launches.
+// C ABI of the ragged expert products, the 8-bit integer and floating-point products,
+// the gated block and the route grouping (declared in include/moe.h): argument
+// validation and launches.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -93,15 +95,42 @@ int check_apart(const char *fn, std::initializer_list<Span> written, std::initia
   return MOE_OK;
 }
 
+bool one_byte(int op) { return op == MOE_MM_INT8 || op == MOE_MM_FP8 || op == MOE_MM_FP8_GLU; }
+
 int check_op(const char *fn, int op, int E, int R, int N, int K) {
-  if (op < MOE_MM_FORWARD || op > MOE_MM_INT8) return fail(MOE_EINVAL, "%s: op=%d", fn, op);
-  return check_shape(fn, op == MOE_MM_INT8 ? 16 : 8, nullptr, E, R, N, K);
+  if (op < MOE_MM_FORWARD || op > MOE_MM_FP8_GLU) return fail(MOE_EINVAL, "%s: op=%d", fn, op);
+  // (the gated block's two branches together are as long as a row or column may be)
+  const int two = op == MOE_MM_GLU || op == MOE_MM_FP8_GLU ? N : op == MOE_MM_GLU_DX ? K : 0;
+  if (two > kMmMaxDim / 2) return fail(MOE_EUNSUPPORTED, "%s: I=%d above %d", fn, two, kMmMaxDim / 2);
+  return check_shape(fn, one_byte(op) ? 16 : 8, nullptr, E, R, N, K);
 }
 
 moe::MmPlan plan_of(int op, int E, int R, int N, int K) {
-  const bool i8 = op == MOE_MM_INT8;
-  return moe::mm_plan(i8 ? MOE_MM_FORWARD : op, i8 ? moe::MM_I8 : moe::MM_BF16, E, R, N, K);
+  static const struct { int op, type; } kinds[] = {
+      {moe::MM_FORWARD, moe::MM_BF16}, {moe::MM_DX, moe::MM_BF16},     {moe::MM_DW, moe::MM_BF16},
+      {moe::MM_FORWARD, moe::MM_I8},   {moe::MM_GLU, moe::MM_BF16},    {moe::MM_GLU_DX, moe::MM_BF16},
+      {moe::MM_FORWARD, moe::MM_F8},   {moe::MM_GLU, moe::MM_F8}};
+  return moe::mm_plan(kinds[op - 1].op, kinds[op - 1].type, E, R, N, K);
 }
+
+// The activation that a call names, for a block of I columns.
+int check_form(const char *fn, const moe_glu_form *form, int I, moe::GluForm *out) {
+  static const moe_glu_form plain = {MOE_ACT_SWIGLU, MOE_W13_UP_GATE, 0.f, 1.f, 0.f};
+  const moe_glu_form &f = form ? *form : plain;
+  if (f.activation != MOE_ACT_SWIGLU && f.activation != MOE_ACT_SITU)
+    return fail(MOE_EUNSUPPORTED, "%s: activation %d is not a gated one", fn, f.activation);
+  if (f.layout != MOE_W13_UP_GATE && f.layout != MOE_W13_GATE_UP) return fail(MOE_EINVAL, "%s: layout=%d", fn, f.layout);
+  if (!isfinite(f.alpha) || !isfinite(f.beta)) return fail(MOE_EINVAL, "%s: alpha and beta must be finite", fn);
+  const bool limit = f.limit > 0.f;
+  if (f.activation == MOE_ACT_SITU && (limit || f.alpha != 1.f || f.beta != 0.f))
+    return fail(MOE_EUNSUPPORTED, "%s: the limit, alpha and beta belong to the SwiGLU", fn);
+  const bool gate_first = f.layout == MOE_W13_GATE_UP;
+  *out = {f.activation, limit, limit ? f.limit : 0.f, f.alpha, f.beta, gate_first ? 0 : I, gate_first ? I : 0};
+  return MOE_OK;
+}
+
+// Blocks of one scale along n values.
+size_t blocks(int n) { return ((size_t)n + 127) / 128; }
 
 size_t type_size(int dtype) { return dtype == MOE_T_FP32 ? 4 : 2; }
 
@@ -244,6 +273,140 @@ int moe_int8_mm(const int8_t *x, const float *x_scales, const int8_t *w, const f
                 int out_dtype, void *out, void *scratch, size_t scratch_bytes, void *stream) {
   return moe_grouped_int8_mm(x, x_scales, M, nullptr, w, w_scales, nullptr, 1, M, N, K, out_dtype, out, scratch,
                              scratch_bytes, stream);
+}
+
+int moe_grouped_glu(int dtype, const void *x, long long x_rows, const int32_t *rows, const void *w,
+                    const int32_t *first, int E, int R, int I, int K, const moe_glu_form *form, int out_dtype, void *h,
+                    void *pre, void *scratch, size_t scratch_bytes, void *stream) {
+  const char *fn = first ? "moe_grouped_glu" : "moe_glu";
+  moe::MmArgs a = {};
+  TRY(check_16bit(fn, dtype, out_dtype));
+  TRY(check_op(fn, MOE_MM_GLU, E, R, I, K));
+  TRY(check_form(fn, form, I, &a.glu));
+  TRY(check_rows(fn, rows, x_rows, R));
+  if (!aligned(first, 4)) return fail(MOE_EINVAL, "%s: first needs 4-byte alignment", fn);
+  if (!first && E != 1) return fail(MOE_EINVAL, "%s: null first", fn);
+  if (R == 0) return MOE_OK;
+  const void *p[] = {w, h, x};   // an x without rows is not read
+  TRY(check_ptrs(fn, p, x_rows ? 3 : 2));
+  if (!aligned(pre, 16)) return fail(MOE_EINVAL, "%s: misaligned pre (16 bytes)", fn);
+  Span work;
+  TRY(check_scratch(fn, MOE_MM_GLU, E, R, I, K, scratch, scratch_bytes, &work));
+  TRY(check_apart(fn, {{h, (size_t)R * I * type_size(out_dtype)}, {pre, (size_t)R * I * 4}, work},
+                  {{x, (size_t)x_rows * K * 2}, {w, (size_t)E * I * K * 4}, {first, (E + 1) * sizeof *first},
+                   {rows, R * sizeof *rows}}));
+  a.part = (float *)scratch;
+  a.op = moe::MM_GLU, a.type = dtype, a.out_type = out_dtype;
+  a.x = x, a.x_rows = (long)x_rows, a.rows = rows, a.w = w, a.first = first;
+  a.E = E, a.R = R, a.N = I, a.K = K, a.out = h, a.pre_out = pre;
+  return launched(moe::launch_mm(a, (hipStream_t)stream), fn);
+}
+
+int moe_grouped_glu_dx(int dtype, const void *dy, const void *w, const void *pre, const int32_t *first, int E, int R,
+                       int N, int I, const moe_glu_form *form, void *d_pre, void *h, void *scratch,
+                       size_t scratch_bytes, void *stream) {
+  const char *fn = first ? "moe_grouped_glu_dx" : "moe_glu_dx";
+  moe::MmArgs a = {};
+  TRY(check_16bit(fn, dtype, dtype));
+  TRY(check_op(fn, MOE_MM_GLU_DX, E, R, N, I));
+  TRY(check_form(fn, form, I, &a.glu));
+  if (!aligned(first, 4)) return fail(MOE_EINVAL, "%s: first needs 4-byte alignment", fn);
+  if (!first && E != 1) return fail(MOE_EINVAL, "%s: null first", fn);
+  if (R == 0) return MOE_OK;
+  const void *p[] = {dy, w, pre, d_pre};
+  TRY(check_ptrs(fn, p, 4));
+  if (!aligned(h, 16)) return fail(MOE_EINVAL, "%s: misaligned h (16 bytes)", fn);
+  Span work;
+  TRY(check_scratch(fn, MOE_MM_GLU_DX, E, R, N, I, scratch, scratch_bytes, &work));
+  TRY(check_apart(fn, {{d_pre, (size_t)R * I * 4}, {h, (size_t)R * I * 2}, work},
+                  {{dy, (size_t)R * N * 2}, {w, (size_t)E * N * I * 2}, {pre, (size_t)R * I * 4},
+                   {first, (E + 1) * sizeof *first}}));
+  a.part = (float *)scratch;
+  a.op = moe::MM_GLU_DX, a.type = dtype, a.out_type = dtype;
+  a.dy = dy, a.w = w, a.pre = pre, a.first = first;
+  a.E = E, a.R = R, a.N = N, a.K = I, a.out = d_pre, a.h = h;
+  return launched(moe::launch_mm(a, (hipStream_t)stream), fn);
+}
+
+int moe_glu_grad(int dtype, const void *dh, const void *pre, int R, int I, const moe_glu_form *form, void *d_pre,
+                 void *h, void *stream) {
+  const char *fn = "moe_glu_grad";
+  moe::GluForm f;
+  TRY(check_16bit(fn, dtype, dtype));
+  TRY(check_op(fn, MOE_MM_GLU, 1, R, I, 8));
+  TRY(check_form(fn, form, I, &f));
+  if (R == 0) return MOE_OK;
+  const void *p[] = {dh, pre, d_pre};
+  TRY(check_ptrs(fn, p, 3));
+  if (!aligned(h, 16)) return fail(MOE_EINVAL, "%s: misaligned h (16 bytes)", fn);
+  TRY(check_apart(fn, {{d_pre, (size_t)R * I * 4}, {h, (size_t)R * I * 2}},
+                  {{dh, (size_t)R * I * 2}, {pre, (size_t)R * I * 4}}));
+  return launched(moe::launch_glu_grad(dtype, dh, pre, R, I, f, d_pre, h, (hipStream_t)stream), fn);
+}
+
+int moe_quant_fp8(int dtype, const void *x, int rows, int cols, uint8_t *q, float *scales, void *stream) {
+  const char *fn = "moe_quant_fp8";
+  if (dtype != MOE_T_BF16 && dtype != MOE_T_FP16) return fail(MOE_EUNSUPPORTED, "%s: dtype %d is not bf16 or fp16", fn, dtype);
+  if (rows < 0 || cols < 1) return fail(MOE_EINVAL, "%s: rows=%d, cols=%d", fn, rows, cols);
+  if (cols % 16 || cols > kMmMaxDim) return fail(MOE_EUNSUPPORTED, "%s: cols=%d must be a multiple of 16 up to %d", fn, cols, kMmMaxDim);
+  if (rows == 0) return MOE_OK;
+  const void *p[] = {x, q};
+  TRY(check_ptrs(fn, p, 2));
+  if (!scales || !aligned(scales, 4)) return fail(MOE_EINVAL, "%s: null or misaligned scales", fn);
+  TRY(check_apart(fn, {{q, (size_t)rows * cols}, {scales, rows * blocks(cols) * sizeof *scales}},
+                  {{x, (size_t)rows * cols * 2}}));
+  return launched(moe::launch_quant_fp8(dtype, x, rows, cols, q, scales, (hipStream_t)stream), fn);
+}
+
+namespace {
+
+// The two products of 8-bit floating-point operands: N outputs, of as many or 2 N rows of w.
+int fp8_product(const char *fn, int op, const uint8_t *x, const float *x_scales, long long x_rows, const int32_t *rows,
+                const uint8_t *w, const float *w_scales, const int32_t *first, int E, int R, int N, int K,
+                const moe_glu_form *form, int out_dtype, void *out, void *scratch, size_t scratch_bytes, void *stream) {
+  const bool glu = op == MOE_MM_FP8_GLU;
+  moe::MmArgs a = {};
+  if (out_dtype != MOE_T_BF16 && out_dtype != MOE_T_FP16 && out_dtype != MOE_T_FP32)
+    return fail(MOE_EUNSUPPORTED, "%s: out_dtype %d", fn, out_dtype);
+  TRY(check_op(fn, op, E, R, N, K));
+  if (glu) TRY(check_form(fn, form, N, &a.glu));
+  TRY(check_rows(fn, rows, x_rows, R));
+  if (!aligned(first, 4)) return fail(MOE_EINVAL, "%s: first needs 4-byte alignment", fn);
+  if (!first && E != 1) return fail(MOE_EINVAL, "%s: null first", fn);
+  if (R == 0) return MOE_OK;
+  const void *p[] = {w, out, x};   // an x without rows is not read
+  TRY(check_ptrs(fn, p, x_rows ? 3 : 2));
+  if ((!x_scales && x_rows) || !w_scales || !aligned(x_scales, 4) || !aligned(w_scales, 4))
+    return fail(MOE_EINVAL, "%s: null or misaligned scales", fn);
+  Span work;
+  TRY(check_scratch(fn, op, E, R, N, K, scratch, scratch_bytes, &work));
+  const size_t wide = glu ? 2 : 1;
+  TRY(check_apart(fn, {{out, (size_t)R * N * type_size(out_dtype)}, work},
+                  {{x, (size_t)x_rows * K}, {x_scales, x_rows * blocks(K) * sizeof *x_scales}, {w, wide * E * N * K},
+                   {w_scales, wide * E * blocks(N) * blocks(K) * sizeof *w_scales}, {first, (E + 1) * sizeof *first},
+                   {rows, R * sizeof *rows}}));
+  a.part = (float *)scratch;
+  a.op = glu ? moe::MM_GLU : moe::MM_FORWARD, a.type = moe::MM_F8, a.out_type = out_dtype;
+  a.x = x, a.x_rows = (long)x_rows, a.rows = rows, a.x_scales = x_scales, a.w = w, a.w_scales = w_scales;
+  a.first = first, a.E = E, a.R = R, a.N = N, a.K = K, a.out = out;
+  return launched(moe::launch_mm(a, (hipStream_t)stream), fn);
+}
+
+}  // namespace
+
+int moe_grouped_fp8_mm(const uint8_t *x, const float *x_scales, long long x_rows, const int32_t *rows, const uint8_t *w,
+                       const float *w_scales, const int32_t *first, int E, int R, int N, int K, int out_dtype,
+                       void *out, void *scratch, size_t scratch_bytes, void *stream) {
+  return fp8_product(first ? "moe_grouped_fp8_mm" : "moe_fp8_mm", MOE_MM_FP8, x, x_scales, x_rows, rows, w, w_scales,
+                     first, E, R, N, K, nullptr, out_dtype, out, scratch, scratch_bytes, stream);
+}
+
+int moe_grouped_fp8_glu(const uint8_t *x, const float *x_scales, long long x_rows, const int32_t *rows,
+                        const uint8_t *w, const float *w_scales, const int32_t *first, int E, int R, int I, int K,
+                        const moe_glu_form *form, int out_dtype, void *h, void *scratch, size_t scratch_bytes,
+                        void *stream) {
+  return fp8_product(first ? "moe_grouped_fp8_glu" : "moe_fp8_glu", MOE_MM_FP8_GLU, x, x_scales, x_rows, rows, w,
+                     w_scales, first, E, R, I, K, form, out_dtype, h, scratch, scratch_bytes, stream);
 }
 
 size_t moe_group_routes_scratch_bytes(int T, int top_k, int E) {

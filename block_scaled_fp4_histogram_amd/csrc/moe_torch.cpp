@@ -1,4 +1,4 @@
-// Python binding of the products, the quantiser and the route grouping
+// Python binding of the products, the gated block, the quantisers and the route grouping
 // (include/moe.h) for torch tensors: checks of the operands, outputs and scratch
 // from torch's allocator, the current stream, and the call.  A few rows' product
 // runs in a few microseconds, which the same steps in Python took longer than
@@ -26,6 +26,12 @@ decltype(&moe_mm_scratch_bytes) f_mm_scratch;
 decltype(&moe_quant_int8) f_quant;
 decltype(&moe_int8_mm) f_int8;
 decltype(&moe_grouped_int8_mm) f_grouped_int8;
+decltype(&moe_grouped_glu) f_glu;
+decltype(&moe_grouped_glu_dx) f_glu_dx;
+decltype(&moe_glu_grad) f_glu_grad;
+decltype(&moe_quant_fp8) f_quant_fp8;
+decltype(&moe_grouped_fp8_mm) f_fp8;
+decltype(&moe_grouped_fp8_glu) f_fp8_glu;
 decltype(&moe_group_routes) f_group;
 decltype(&moe_group_routes_scratch_bytes) f_group_scratch;
 decltype(&moe_last_error) f_last_error;
@@ -55,6 +61,7 @@ std::string type_text(ScalarType t) {
     case at::kChar: return "torch.int8";
     case at::kInt: return "torch.int32";
     case at::kByte: return "torch.uint8";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return std::string("torch.") + c10::toString(t);
   }
 }
@@ -381,6 +388,195 @@ PyObject *grouped_int8_mm(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// An argument that a gated block's form takes, and the form of five in a row:
+// activation, limit (None: no clamp), alpha, beta, layout.
+double number(PyObject *o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw PythonError();
+  return v;
+}
+int whole(PyObject *o) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) throw PythonError();
+  return v < INT32_MIN || v > INT32_MAX ? -1 : (int)v;
+}
+moe_glu_form form(PyObject *const *a) {
+  return {whole(a[0]), whole(a[4]), none(a[1]) ? 0.f : (float)number(a[1]), (float)number(a[2]), (float)number(a[3])};
+}
+bool truth(PyObject *o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw PythonError();
+  return v;
+}
+// An output that is made, given, or neither made nor given (want false).
+Tensor optional_out(Operands &ops, PyObject *given, const char *name, at::IntArrayRef shape, ScalarType type) {
+  if (none(given)) return Tensor();
+  return ops.add(tensor(given, name), name, {type}, shape);
+}
+PyObject *pair(PyObject *given0, const Tensor &t0, PyObject *given1, const Tensor &t1) {
+  PyObject *p0 = result(given0, t0), *p1 = result(given1, t1), *r = p0 && p1 ? PyTuple_Pack(2, p0, p1) : nullptr;
+  Py_XDECREF(p0);
+  Py_XDECREF(p1);
+  return r;
+}
+int64_t half(int64_t n, const char *name) {
+  if (n % 2) refuse(PyExc_ValueError, std::string(name) + ": expected two branches, got " + std::to_string(n) + " rows");
+  return n / 2;
+}
+
+// The groups of a product's rows, or one of all of them; the arguments are first and rows.
+template <bool GROUPED>
+struct Groups {
+  const Tensor *first = nullptr, *rows = nullptr;
+  int64_t R;
+  Groups(Operands &ops, PyObject *const *a, int64_t E, int64_t T) : R(T) {
+    if (!GROUPED) return;
+    first = &tensor(a[0], "first");
+    ops.add(*first, "first", {at::kInt}, {E + 1});
+    if (none(a[1])) return;
+    rows = &tensor_of(a[1], "rows", 1);
+    R = rows->size(0);
+    ops.add(*rows, "rows", {at::kInt}, {R});
+  }
+};
+
+// (x, w[, first, rows], the form's five, keep_pre, out, out_dtype, pre, scratch) -> h or (h, pre)
+template <bool GROUPED>
+PyObject *glu(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, GROUPED ? 14 : 12, [&]() -> PyObject * {
+    Operands ops;
+    const Tensor &x = tensor_of(a[0], "x", 2), &w = tensor_of(a[1], "w", GROUPED ? 3 : 2);
+    const int64_t T = x.size(0), K = x.size(1), E = GROUPED ? w.size(0) : 1, I = half(w.size(w.dim() - 2), "w");
+    const ScalarType type = x.scalar_type();
+    ops.add(x, "x", {at::kBFloat16, at::kHalf}, x.sizes());
+    if (GROUPED) ops.add(w, "w", {type}, {E, 2 * I, K});
+    else ops.add(w, "w", {type}, {2 * I, K});
+    const Groups<GROUPED> g(ops, a + 2, E, T);
+    PyObject *const *o = a + (GROUPED ? 4 : 2);
+    const moe_glu_form f = form(o);
+    const bool keep = truth(o[5]) || !none(o[8]);
+    const ScalarType ot = out_type(ops, o[6], o[7], type, {type, at::kFloat}, {g.R, I});
+    Tensor pre = optional_out(ops, o[8], "pre", {g.R, 2 * I}, type);
+    ops.check();
+    const int e = size32(E, "E"), r = size32(g.R, "R"), i = size32(I, "I"), k = size32(K, "K");
+    c10::DeviceGuard guard(x.device());
+    const Tensor out = none(o[6]) ? make({g.R, I}, ot, x) : tensor(o[6], "out");
+    if (keep && !pre.defined()) pre = make({g.R, 2 * I}, type, x);
+    const Scratch s(o[9], f_mm_scratch(MOE_MM_GLU, e, r, i, k), x);
+    done(f_glu(code(type), ptr(&x), T, (const int32_t *)ptr(g.rows), ptr(&w), (const int32_t *)ptr(g.first), e, r, i, k,
+               &f, code(ot), out.data_ptr(), keep ? pre.data_ptr() : nullptr, s.p, s.bytes, stream_of(x)));
+    return keep ? pair(o[6], out, o[8], pre) : result(o[6], out);
+  });
+}
+
+// (dy, w, pre[, first], the form's five, keep_h, out, h, scratch) -> d_pre or (d_pre, h)
+template <bool GROUPED>
+PyObject *glu_dx(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, GROUPED ? 13 : 12, [&]() -> PyObject * {
+    Operands ops;
+    const Tensor &dy = tensor_of(a[0], "dy", 2), &w = tensor_of(a[1], "w", GROUPED ? 3 : 2), &pre = tensor_of(a[2], "pre", 2);
+    const int64_t R = dy.size(0), N = dy.size(1), E = GROUPED ? w.size(0) : 1, I = w.size(w.dim() - 1);
+    const ScalarType type = dy.scalar_type();
+    ops.add(dy, "dy", {at::kBFloat16, at::kHalf}, dy.sizes());
+    if (GROUPED) ops.add(w, "w", {type}, {E, N, I});
+    else ops.add(w, "w", {type}, {N, I});
+    ops.add(pre, "pre", {type}, {R, 2 * I});
+    const Tensor *first = nullptr;
+    if (GROUPED) first = &ops.add(tensor(a[3], "first"), "first", {at::kInt}, {E + 1});
+    PyObject *const *o = a + (GROUPED ? 4 : 3);
+    const moe_glu_form f = form(o);
+    const bool keep = truth(o[5]) || !none(o[7]);
+    Tensor out = optional_out(ops, o[6], "out", {R, 2 * I}, type), h = optional_out(ops, o[7], "h", {R, I}, type);
+    ops.check();
+    const int e = size32(E, "E"), r = size32(R, "R"), nn = size32(N, "N"), i = size32(I, "I");
+    c10::DeviceGuard guard(dy.device());
+    if (!out.defined()) out = make({R, 2 * I}, type, dy);
+    if (keep && !h.defined()) h = make({R, I}, type, dy);
+    const Scratch s(o[8], f_mm_scratch(MOE_MM_GLU_DX, e, r, nn, i), dy);
+    done(f_glu_dx(code(type), ptr(&dy), ptr(&w), ptr(&pre), (const int32_t *)ptr(first), e, r, nn, i, &f, out.data_ptr(),
+                  keep ? h.data_ptr() : nullptr, s.p, s.bytes, stream_of(dy)));
+    return keep ? pair(o[6], out, o[7], h) : result(o[6], out);
+  });
+}
+
+// (dh, pre, the form's five, keep_h, out, h) -> d_pre or (d_pre, h)
+PyObject *glu_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject * {
+    Operands ops;
+    const Tensor &dh = tensor_of(a[0], "dh", 2), &pre = tensor_of(a[1], "pre", 2);
+    const int64_t R = dh.size(0), I = dh.size(1);
+    const ScalarType type = dh.scalar_type();
+    ops.add(dh, "dh", {at::kBFloat16, at::kHalf}, dh.sizes());
+    ops.add(pre, "pre", {type}, {R, 2 * I});
+    const moe_glu_form f = form(a + 2);
+    const bool keep = truth(a[7]) || !none(a[9]);
+    Tensor out = optional_out(ops, a[8], "out", {R, 2 * I}, type), h = optional_out(ops, a[9], "h", {R, I}, type);
+    ops.check();
+    const int r = size32(R, "R"), i = size32(I, "I");
+    c10::DeviceGuard guard(dh.device());
+    if (!out.defined()) out = make({R, 2 * I}, type, dh);
+    if (keep && !h.defined()) h = make({R, I}, type, dh);
+    done(f_glu_grad(code(type), ptr(&dh), ptr(&pre), r, i, &f, out.data_ptr(), keep ? h.data_ptr() : nullptr, stream_of(dh)));
+    return keep ? pair(a[8], out, a[9], h) : result(a[8], out);
+  });
+}
+
+int64_t blocks(int64_t n) { return (n + 127) / 128; }
+
+// (x, out, scales) -> (codes, scales)
+PyObject *quant_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 3, [&]() -> PyObject * {
+    Operands ops;
+    const Tensor &x = tensor_of(a[0], "x", 2);
+    const int64_t R = x.size(0), b = blocks(x.size(1));
+    ops.add(x, "x", {at::kBFloat16, at::kHalf}, x.sizes());
+    Tensor q = optional_out(ops, a[1], "out", x.sizes(), at::kFloat8_e4m3fn);
+    Tensor s = optional_out(ops, a[2], "scales", {R, b}, at::kFloat);
+    ops.check();
+    const int rows = size32(R, "rows"), cols = size32(x.size(1), "cols");
+    c10::DeviceGuard guard(x.device());
+    if (!q.defined()) q = make(x.sizes(), at::kFloat8_e4m3fn, x);
+    if (!s.defined()) s = make({R, b}, at::kFloat, x);
+    done(f_quant_fp8(code(x.scalar_type()), ptr(&x), rows, cols, (uint8_t *)q.data_ptr(), (float *)s.data_ptr(), stream_of(x)));
+    return pair(a[1], q, a[2], s);
+  });
+}
+
+// (x, x_scales, w, w_scales[, first, rows][, the form's five], out, out_dtype, scratch)
+template <bool GROUPED, bool GLU>
+PyObject *fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 7 + (GROUPED ? 2 : 0) + (GLU ? 5 : 0), [&] {
+    Operands ops;
+    const Tensor &x = tensor_of(a[0], "x", 2), &w = tensor_of(a[2], "w", GROUPED ? 3 : 2);
+    const int64_t T = x.size(0), K = x.size(1), E = GROUPED ? w.size(0) : 1, W = w.size(w.dim() - 2);
+    const int64_t N = GLU ? half(W, "w") : W;
+    ops.add(x, "x", {at::kFloat8_e4m3fn}, x.sizes());
+    const Tensor &xs = ops.add(tensor(a[1], "x_scales"), "x_scales", {at::kFloat}, {T, blocks(K)});
+    if (GROUPED) ops.add(w, "w", {at::kFloat8_e4m3fn}, {E, W, K});
+    else ops.add(w, "w", {at::kFloat8_e4m3fn}, {W, K});
+    const Tensor &ws = tensor(a[3], "w_scales");
+    const int64_t shape[4] = {E, 2, blocks(N), blocks(K)}, plain[3] = {E, blocks(N), blocks(K)};
+    const at::IntArrayRef want = GLU ? at::IntArrayRef(shape, 4) : at::IntArrayRef(plain, 3);
+    ops.add(ws, "w_scales", {at::kFloat}, GROUPED ? want : want.slice(1));
+    const Groups<GROUPED> g(ops, a + 4, E, T);
+    PyObject *const *o = a + (GROUPED ? 6 : 4);
+    moe_glu_form f = {};
+    if (GLU) f = form(o), o += 5;
+    const ScalarType ot = out_type(ops, o[0], o[1], at::kBFloat16, {at::kBFloat16, at::kHalf, at::kFloat}, {g.R, N});
+    ops.check();
+    const int e = size32(E, "E"), r = size32(g.R, "R"), nn = size32(N, "N"), k = size32(K, "K");
+    c10::DeviceGuard guard(x.device());
+    const Tensor out = none(o[0]) ? make({g.R, N}, ot, x) : tensor(o[0], "out");
+    const Scratch s(o[2], f_mm_scratch(GLU ? MOE_MM_FP8_GLU : MOE_MM_FP8, e, r, nn, k), x);
+    const uint8_t *px = (const uint8_t *)ptr(&x), *pw = (const uint8_t *)ptr(&w);
+    const float *pxs = (const float *)ptr(&xs), *pws = (const float *)ptr(&ws);
+    const int32_t *first = (const int32_t *)ptr(g.first), *rows = (const int32_t *)ptr(g.rows);
+    if (GLU) done(f_fp8_glu(px, pxs, T, rows, pw, pws, first, e, r, nn, k, &f, code(ot), out.data_ptr(), s.p, s.bytes, stream_of(x)));
+    else done(f_fp8(px, pxs, T, rows, pw, pws, first, e, r, nn, k, code(ot), out.data_ptr(), s.p, s.bytes, stream_of(x)));
+    return result(o[0], out);
+  });
+}
+
 // (topk_ids, num_experts, scratch) -> (first, order, token, inverse)
 PyObject *group_routes(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(n, 3, [&]() -> PyObject * {
@@ -431,6 +627,12 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     f_quant = (decltype(f_quant))get("moe_quant_int8");
     f_int8 = (decltype(f_int8))get("moe_int8_mm");
     f_grouped_int8 = (decltype(f_grouped_int8))get("moe_grouped_int8_mm");
+    f_glu = (decltype(f_glu))get("moe_grouped_glu");
+    f_glu_dx = (decltype(f_glu_dx))get("moe_grouped_glu_dx");
+    f_glu_grad = (decltype(f_glu_grad))get("moe_glu_grad");
+    f_quant_fp8 = (decltype(f_quant_fp8))get("moe_quant_fp8");
+    f_fp8 = (decltype(f_fp8))get("moe_grouped_fp8_mm");
+    f_fp8_glu = (decltype(f_fp8_glu))get("moe_grouped_fp8_glu");
     f_group = (decltype(f_group))get("moe_group_routes");
     f_group_scratch = (decltype(f_group_scratch))get("moe_group_routes_scratch_bytes");
     f_last_error = (decltype(f_last_error))get("moe_last_error");
@@ -442,9 +644,15 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-#define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
+#define NAMED(name, ...) {name, (PyCFunction)(void (*)(void))__VA_ARGS__, METH_FASTCALL, nullptr}
+#define FAST(name) NAMED(#name, name)
 PyMethodDef g_methods[] = {FAST(bind),       FAST(grouped_mm), FAST(grouped_mm_dx),   FAST(grouped_mm_dw), FAST(quant_int8),
-                           FAST(int8_mm),    FAST(grouped_int8_mm), FAST(group_routes), {nullptr, nullptr, 0, nullptr}};
+                           FAST(int8_mm),    FAST(grouped_int8_mm), FAST(group_routes), FAST(glu_grad), FAST(quant_fp8),
+                           NAMED("glu", glu<false>),       NAMED("grouped_glu", glu<true>),
+                           NAMED("glu_dx", glu_dx<false>), NAMED("grouped_glu_dx", glu_dx<true>),
+                           NAMED("fp8_mm", fp8<false, false>), NAMED("grouped_fp8_mm", fp8<true, false>),
+                           NAMED("fp8_glu", fp8<false, true>), NAMED("grouped_fp8_glu", fp8<true, true>),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_products", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

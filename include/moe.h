@@ -350,11 +350,22 @@ int moe_plan_set_activation(moe_plan_t plan, int act);
  * nothing, except moe_grouped_mm_dw, whose sums are then zeros.
  */
 typedef enum { MOE_T_BF16 = 1, MOE_T_FP16 = 2, MOE_T_FP32 = 3 } moe_dtype;
-typedef enum { MOE_MM_FORWARD = 1, MOE_MM_DX = 2, MOE_MM_DW = 3, MOE_MM_INT8 = 4 } moe_mm_op;
+typedef enum {
+  MOE_MM_FORWARD = 1,
+  MOE_MM_DX = 2,
+  MOE_MM_DW = 3,
+  MOE_MM_INT8 = 4,
+  MOE_MM_GLU = 5,           /* N is the gated block's I */
+  MOE_MM_GLU_DX = 6,        /* K is the gated block's I */
+  MOE_MM_FP8 = 7,
+  MOE_MM_FP8_GLU = 8        /* N is the gated block's I */
+} moe_mm_op;
 
 /* Scratch bytes of one product: op as in moe_mm_op (MOE_MM_FORWARD is
  * moe_grouped_mm, MOE_MM_INT8 moe_int8_mm with E = 1 and R = M, and
- * moe_grouped_int8_mm).  Host only; 0 on sizes that the call refuses. */
+ * moe_grouped_int8_mm; MOE_MM_GLU to MOE_MM_FP8_GLU are moe_grouped_glu,
+ * moe_grouped_glu_dx, moe_grouped_fp8_mm and moe_grouped_fp8_glu).  Host only; 0
+ * on sizes that the call refuses. */
 size_t moe_mm_scratch_bytes(int op, int E, int R, int N, int K);
 
 /*
@@ -408,6 +419,94 @@ int moe_grouped_int8_mm(const int8_t *x, const float *x_scales, long long x_rows
                         const float *w_scales, const int32_t *first, int E, int R, int N, int K, int out_dtype,
                         void *out, void *scratch, size_t scratch_bytes, void *stream);
 
+/* ---- the gated block ---------------------------------------------------
+ *
+ * Activation of a gated block of I columns: h = act(gate, up) of two projections,
+ *   MOE_ACT_SWIGLU  g sigmoid(alpha g) (u + beta), g = min(gate, limit),
+ *                   u = clamp(up, -limit, limit); limit NaN or <= 0: no clamp
+ *   MOE_ACT_SITU    silu(4 tanh(gate / 4)) 25 tanh(up / 25); no limit, alpha 1, beta 0
+ * layout (moe_w13_layout) says which branch comes first, in the rows of w and in the
+ * columns of the projections.  A NULL form is SwiGLU, [up; gate], no limit, alpha 1,
+ * beta 0.  alpha and beta must be finite.  A NaN projection is not clamped away: h and
+ * the gradients that its value enters are NaN.
+ */
+typedef struct {
+  int activation, layout;
+  float limit, alpha, beta;
+} moe_glu_form;
+
+/*
+ * moe_grouped_glu -- both projections and the activation in one product:
+ * pre[r, c] = sum_k x[row(r), k] * w[e, c, k] for the rows r of group e and the 2 I
+ * rows c of w[e], h[r, i] = act of the two branches' columns i, of the 32-bit sums.
+ *   dtype      MOE_T_BF16 or MOE_T_FP16: type of x and w
+ *   x          [x_rows, K];  w [E, 2 I, K]
+ *   out_dtype  dtype or MOE_T_FP32;  h [R, I]
+ *   pre        [R, 2 I] in dtype, or NULL: the projections, which the backward pass
+ *              takes, rounded to dtype
+ *   first      NULL with E = 1: one group of all R rows
+ */
+int moe_grouped_glu(int dtype, const void *x, long long x_rows, const int32_t *rows, const void *w,
+                    const int32_t *first, int E, int R, int I, int K, const moe_glu_form *form, int out_dtype, void *h,
+                    void *pre, void *scratch, size_t scratch_bytes, void *stream);
+
+/*
+ * moe_grouped_glu_dx -- the backward pass from the down product to the projections:
+ * dh[r, i] = sum_n dy[r, n] * w[e, n, i] (32 bits, not stored), d_pre[r] = dh times the
+ * activation's gradient at pre[r].  A branch beyond the limit has gradient 0, at the
+ * limit it has the clamp's from inside.
+ *   dy [R, N], w [E, N, I], pre [R, 2 I], d_pre [R, 2 I], all dtype
+ *   h  [R, I] in dtype, or NULL: the activation once more, for the gradient of w
+ * d_pre is then the dy of moe_grouped_mm_dx and moe_grouped_mm_dw with moe_grouped_glu's w and x.
+ */
+int moe_grouped_glu_dx(int dtype, const void *dy, const void *w, const void *pre, const int32_t *first, int E, int R,
+                       int N, int I, const moe_glu_form *form, void *d_pre, void *h, void *scratch,
+                       size_t scratch_bytes, void *stream);
+
+/* moe_glu_grad -- the same from a dh [R, I] in memory: every row, no groups. */
+int moe_glu_grad(int dtype, const void *dh, const void *pre, int R, int I, const moe_glu_form *form, void *d_pre,
+                 void *h, void *stream);
+
+/* ---- 8-bit floating point with a scale for each block of 128 -----------
+ *
+ * Codes are OCP E4M3 (a byte; largest value 448).  A row of x has one fp32 scale for
+ * each 128 values of the reduction, x_scales [x_rows, ceil(K / 128)]; w has one for each
+ * block of 128 x 128, w_scales [E, ceil(N / 128), ceil(K / 128)], the last blocks cut
+ * short where N or K ends.  K is a multiple of 16.
+ */
+
+/*
+ * moe_quant_fp8 -- rows of bf16 or fp16 to such codes and scales:
+ * scales[r, b] = fp32(amax / 448) of the block's largest magnitude, q = x * fp32(448 / amax)
+ * rounded to fp32, then to the nearest code, ties to even.  A block of zeros has scale 0
+ * and codes 0; one that holds an infinity or NaN has scale NaN and codes 0, so that
+ * products with it are NaN.  (Below amax = 2^-100 both factors of the code's product
+ * are taken 2^64 away, so that they stay in range.)  cols % 16 == 0.
+ */
+int moe_quant_fp8(int dtype, const void *x, int rows, int cols, uint8_t *q, float *scales, void *stream);
+
+/*
+ * moe_grouped_fp8_mm -- out[r, n] = sum over the blocks b of K of
+ * x_scales[row(r), b] * w_scales[e, n / 128, b] * sum_{k in b} x[row(r), k] * w[e, n, k].
+ * A block's sum is kept in fp32; it is scaled by the two scales' powers of two and by
+ * their fractions' product, so only the result's range counts, not that of the scales'
+ * product.  out_dtype MOE_T_BF16, MOE_T_FP16 or MOE_T_FP32; out [R, N].  first NULL with
+ * E = 1: one group of all R rows.
+ */
+int moe_grouped_fp8_mm(const uint8_t *x, const float *x_scales, long long x_rows, const int32_t *rows, const uint8_t *w,
+                       const float *w_scales, const int32_t *first, int E, int R, int N, int K, int out_dtype,
+                       void *out, void *scratch, size_t scratch_bytes, void *stream);
+
+/*
+ * moe_grouped_fp8_glu -- the gated block on such operands: w [E, 2 I, K], w_scales
+ * [E, 2, ceil(I / 128), ceil(K / 128)] (each branch's blocks start at its first row),
+ * h [R, I] in out_dtype.
+ */
+int moe_grouped_fp8_glu(const uint8_t *x, const float *x_scales, long long x_rows, const int32_t *rows,
+                        const uint8_t *w, const float *w_scales, const int32_t *first, int E, int R, int I, int K,
+                        const moe_glu_form *form, int out_dtype, void *h, void *scratch, size_t scratch_bytes,
+                        void *stream);
+
 /*
  * moe_group_routes -- the routes of a batch sorted by expert, for the products
  * above: route r = t * top_k + j of token t, slot j, in ascending order inside
@@ -456,7 +555,7 @@ int moe_debug_route(moe_plan_t plan, const moe_tier *tiers, int n_tiers, const i
 /*
  * moe_debug_mm_plan -- how a product of these sizes runs (op as in moe_mm_op, so
  * that the tests of the tile shapes run the shapes they name): output rows and
- * columns of a tile (16 x 16: few rows a group, weights streamed) and the parts of
+ * columns of a tile (16 x 16, for a gated block 16 x 8: few rows a group, weights streamed) and the parts of
  * its reduction.  Host only; MOE_EINVAL or MOE_EUNSUPPORTED on sizes that the call
  * refuses and for R = 0.
  */
