@@ -12,7 +12,7 @@ static hipError_t launch_fp8_tiles(const MmArgs &a, int shape, hipStream_t s) {
   if (a.out_type == MM_FP32)
     return shape == 3 ? launch_tile<OP, MM_F8X, 64, 128, 2, 2, 3>(a, s) : launch_tile<OP, MM_F8X, 128, 128, 2, 2, 2>(a, s);
   switch (shape) {
-    case 0: return launch_tile<OP, MM_F8, 256, 128, OP == MM_GLU ? 4 : 2, OP == MM_GLU ? 1 : 2, 2>(a, s);
+    case 0: return launch_tile<OP, MM_F8, 256, 128, 4, 1, 2>(a, s);
     case 1: return launch_tile<OP, MM_F8, 128, 256, 2, 2, 2>(a, s);
     case 2: return launch_tile<OP, MM_F8, 128, 128, 2, 2, 3>(a, s);
     default: return launch_tile<OP, MM_F8, 64, 128, 2, 2, 4>(a, s);

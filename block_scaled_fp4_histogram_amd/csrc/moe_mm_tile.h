@@ -63,18 +63,18 @@ __device__ __forceinline__ v8h codes_f16(int lo, int hi) {
   return v8h{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// A block's scale as the E8M0 code of a power of two and a factor of magnitude in
-// [1, 2) (less for subnormal scales; 0, infinite or NaN where the scale is).  The sum
-// meets the powers of two and the factors' product apart, so the product of two scales
-// never leaves fp32's range before the result does.
+// A block's scale as the E8M0 code of a power of two, which is its exponent's bits, and
+// a factor of magnitude in [1, 2): less for subnormal scales, and 0 with the least power
+// of two for 0, so that no sum is infinite before it meets the 0.  (Infinite and NaN
+// scales have E8M0's NaN.)  The sum meets the powers of two and the factors' product
+// apart, so the product of two scales never leaves fp32's range before the result does.
 struct MmScale8 {
   float m;
   int code;
 };
 __device__ __forceinline__ MmScale8 mm_scale8(float s) {
-  // (a scale of 0 takes the least power of two, so that no sum is infinite before it meets the 0)
-  const int e = s == 0.0f ? -127 : max(__builtin_amdgcn_frexp_expf(s) - 1, -127);
-  return MmScale8{__builtin_ldexpf(s, -e), e + 127};
+  const int code = (int)((__float_as_uint(s) >> 23) & 0xFFu);
+  return MmScale8{__builtin_ldexpf(s, 127 - code), code};
 }
 constexpr int kF8Block = 128;            // values of a scale, along either side
 
@@ -94,6 +94,7 @@ __device__ __forceinline__ v4f f8_block(v4f acc, v8i p, v8i q, int row, MmScale8
     for (int k = 0; k < 4; k++) d = mfma_f16(codes_f16(p[2 * k], p[2 * k + 1]), codes_f16(q[2 * k], q[2 * k + 1]), d);
 #pragma unroll
     for (int k = 0; k < 4; k++) acc[k] += __builtin_ldexpf(d[k] * m, sum.code + x.code - 254);
+    // (an infinite or NaN scale's factor is one too: NaN or, where MM_F8 gives NaN, infinite)
   }
   return acc;
 }
@@ -338,6 +339,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   constexpr int kOutStage = 16 * (64 * 4 + 16);                 // of one wave, for its outputs
   static_assert(NW * kOutStage <= kStage, "outputs through LDS");
   __shared__ __align__(1024) uint8_t lds[kStage];
+  __shared__ __align__(16) float xsl[F8 ? BQ * 4 : 4];          // scales of x's rows: four blocks of K
 
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   constexpr int BC = mm_tile_cols(OP, BP);
@@ -493,20 +495,23 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   };
 
   // ---- scales of 8-bit floating point: a row of x has one a step, so has the tile's
-  // part of w (two in a gated block: its branches'); read a step ahead
+  // part of w (two in a gated block: its branches').  w's are read a step ahead into
+  // scalar registers; x's, with the tiles, four steps' at once straight to LDS, as
+  // [row][4], or [4][row] from rows of fewer than four.  (A load a row and step into
+  // registers, 16 lines a quarter wave, took half the kernel's time.)
   const int kbs = (a.K + kF8Block - 1) / kF8Block;
   static_assert(!F8 || kF8Block % TP == 0, "a wave's columns of one block");
-  constexpr int NW8 = F8 && GLU ? 2 : 1;
-  const float *sxp[F8 ? NQ : 1];
-  float sx[F8 ? NQ : 1];
+  constexpr int NW8 = F8 && GLU ? 2 : 1, XW = F8 ? (BQ / 64 + NW - 1) / NW : 1;
+  const float *sxp[XW];
   const MmConstF *swp[NW8];
   float sw[NW8];
+  int sx0 = 0;                                                  // first block of K in LDS
   if constexpr (F8) {
 #pragma unroll
-    for (int j = 0; j < NQ; j++) {
-      const int q = wq * TQ + 16 * j + l16;
+    for (int i = 0; i < XW; i++) {
+      const int q = (i * NW + w) * 64 + lane;
       const long xr = q < qn ? mm_x_row(a, t.row0 + q) : -1;
-      sxp[j] = xr < 0 ? nullptr : a.x_scales + xr * kbs;
+      sxp[i] = xr < 0 ? nullptr : a.x_scales + xr * kbs;
     }
     const int nbs = (a.N + kF8Block - 1) / kF8Block;
 #pragma unroll
@@ -520,9 +525,23 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   auto load_scales = [&](int s) {
     if constexpr (F8) {
 #pragma unroll
-      for (int j = 0; j < NQ; j++) sx[j] = sxp[j] ? sxp[j][s] : 0.f;
-#pragma unroll
       for (int i = 0; i < NW8; i++) sw[i] = swp[i][s];
+      if (s > begin && s < sx0 + 4) return;
+      sx0 = kbs < 4 ? 0 : min(s, kbs - 4);
+#pragma unroll
+      for (int i = 0; i < XW; i++) {
+        const int r0 = (i * NW + w) * 64;
+        if (r0 >= BQ) break;
+        if (kbs >= 4) {
+          const float *p = sxp[i] ? sxp[i] + sx0 : (const float *)g_mm_zeros;
+          __builtin_amdgcn_global_load_lds(p, (lds_void *)(xsl + r0 * 4), 16, 0, 0);
+        } else {
+          for (int k = 0; k < kbs; k++) {
+            const float *p = sxp[i] ? sxp[i] + k : (const float *)g_mm_zeros;
+            __builtin_amdgcn_global_load_lds(p, (lds_void *)(xsl + k * BQ + r0), 4, 0, 0);
+          }
+        }
+      }
     }
   };
 
@@ -568,19 +587,46 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
           for (int i = 0; i < NP; i++) acc[i][j] = M::mma(fp[h][i], fq[h][j], acc[i][j]);
       }
     };
+    // 8-bit floating point: the operands of half the columns (gated: of a branch) at a time
     MmScale8 zx[F8 ? NQ : 1], zw[NW8];
+    constexpr int HF = NP / 2;
+    auto read8 = [&](int b) {
+#pragma unroll
+      for (int i = 0; i < HF; i++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) fp[h][b * HF + i] = frag_p(lp, b * HF + i, h);
+    };
+    auto mul8 = [&](int b) {
+      if constexpr (F8) {
+#pragma unroll
+        for (int i = b * HF; i < b * HF + HF; i++)
+#pragma unroll
+          for (int j = 0; j < NQ; j++)
+            acc[i][j] = f8_block<TYPE>(acc[i][j], join8(fp[0][i], fp[1][i]), join8(fq[0][j], fq[1][j]), zw[GLU ? b : 0].code, zw[GLU ? b : 0], zx[j]);
+      }
+    };
     if constexpr (F8) {
 #pragma unroll
-      for (int j = 0; j < NQ; j++) zx[j] = mm_scale8(sx[j]);
+      for (int j = 0; j < NQ; j++) {
+        const int q = wq * TQ + 16 * j + l16;
+        zx[j] = mm_scale8(xsl[kbs >= 4 ? q * 4 + s - sx0 : s * BQ + q]);
+#pragma unroll
+        for (int h = 0; h < 2; h++) fq[h][j] = frag_q(lq, j, h);
+      }
 #pragma unroll
       for (int i = 0; i < NW8; i++) zw[i] = mm_scale8(sw[i]);
-    }
-    read(0);
-    if (GATHER && !F8) {
-      mul(0);
+      read8(0);
+      mul8(0);
       __builtin_amdgcn_sched_barrier(0);
+      read8(1);
+    } else {
+      read(0);
+      if (GATHER) {
+        mul(0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      read(1);
     }
-    read(1);
     if (s + 1 < steps) {
       wait_lgkm0();                      // the stage is free once every wave has read it
       mm_barrier();
@@ -589,13 +635,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       gather_rows(s + 2);
     }
     if constexpr (F8) {
-#pragma unroll
-      for (int j = 0; j < NQ; j++)
-#pragma unroll
-        for (int i = 0; i < NP; i++) {
-          const MmScale8 &z = zw[GLU ? i / (NP / 2) : 0];
-          acc[i][j] = f8_block<TYPE>(acc[i][j], join8(fp[0][i], fp[1][i]), join8(fq[0][j], fq[1][j]), z.code, z, zx[j]);
-        }
+      mul8(1);
     } else {
       if (!GATHER) mul(0);
       mul(1);
