@@ -597,7 +597,30 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
         for (int h = 0; h < 2; h++) fp[h][b * HF + i] = frag_p(lp, b * HF + i, h);
     };
     auto mul8 = [&](int b) {
-      if constexpr (F8) {
+      if constexpr (TYPE == MM_F8) {
+        // a block's sums meet the accumulators two instructions later, in the shadow of the
+        // ones between; the order is pinned, or more sums are in flight than registers hold
+        constexpr int L = 2, CNT = HF * NQ;
+        v4f d[L + 1];
+        float m[NQ];
+#pragma unroll
+        for (int j = 0; j < NQ; j++) m[j] = zw[GLU ? b : 0].m * zx[j].m;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int c = 0; c < CNT + L; c++) {
+          if (c < CNT) {
+            const int i = b * HF + c / NQ, j = c % NQ;
+            d[c % (L + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                join8(fp[0][i], fp[1][i]), join8(fq[0][j], fq[1][j]), v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, zw[GLU ? b : 0].code, 0, zx[j].code);
+          }
+          if (c >= L) {
+            const int o = c - L, i = b * HF + o / NQ, j = o % NQ;
+#pragma unroll
+            for (int k = 0; k < 4; k++) acc[i][j][k] = fmaf(d[o % (L + 1)][k], m[j], acc[i][j][k]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else if constexpr (F8) {
 #pragma unroll
         for (int i = b * HF; i < b * HF + HF; i++)
 #pragma unroll
@@ -617,6 +640,12 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       for (int i = 0; i < NW8; i++) zw[i] = mm_scale8(sw[i]);
       read8(0);
       mul8(0);
+      // (kept in front of the second half's reads and the branch below: sunk past them, both
+      // halves' operands would be live and the accumulators spill)
+#pragma unroll
+      for (int i = 0; i < HF; i++)
+#pragma unroll
+        for (int j = 0; j < NQ; j++) asm volatile("" : "+v"(acc[i][j]));
       __builtin_amdgcn_sched_barrier(0);
       read8(1);
     } else {
