@@ -593,7 +593,8 @@ def group_routes(topk_ids, num_experts: int, scratch=None, stream=None):
 
 def debug_mm_plan(op: int, E: int, R: int, N: int, K: int):
     """(rows and columns of an output tile, parts of the reduction) a product of these sizes runs with
-    (moe_debug_mm_plan); op as in mm_scratch_bytes. (16, 16, 1), for a gated block (16, 8, 1): streamed weights."""
+    (moe_debug_mm_plan); op as in mm_scratch_bytes. (16, 16, 1), for a gated block (16, 8, 1): streamed weights;
+    0 parts: the last round's tiles alone may be split."""
     v = [C.c_int() for _ in range(3)]
     _check(_lib.load().moe_debug_mm_plan(op, E, R, N, K, *map(C.byref, v)))
     return tuple(x.value for x in v)

@@ -39,6 +39,7 @@ struct MmArgs {
   void *out;                         // [R, N], [R, K] or [E, N, K]; MM_GLU_DX: the projections' gradient [R, 2 K]
   float *part;                       // scratch of a split reduction: [splits] of out in 32 bits
   int splits;                        // set by launch_mm
+  int tail;                          // set by launch_mm: the last round's tiles are split (mm_tail)
   GluForm glu;                       // MM_GLU, MM_GLU_DX
   const void *pre;                   // MM_GLU_DX: the projections [R, 2 K]
   void *pre_out;                     // MM_GLU: the projections [R, 2 N], or NULL
@@ -51,6 +52,7 @@ struct MmArgs {
 struct MmPlan {
   int stream, shape, splits;
   int rows, cols;                    // of a tile
+  int tail;                          // the tiles of the last round in parts
   size_t scratch;
 };
 MmPlan mm_plan(int op, int type, long E, long R, long N, long K);

@@ -14,17 +14,22 @@ namespace moe {
 enum { kShapes = 4 };
 static const struct { int bq, bp, occ; float weight; } kMmShapes[kShapes] = {
     {256, 128, 2, 1.0f}, {128, 256, 2, 1.04f}, {128, 128, 3, 1.2f}, {64, 128, 4, 1.5f}};
+// 8-bit floating point, whose scales of x's rows weigh less on wide tiles (one group of
+// that size: 309, 272, 304, 339 us; 64-row tiles read the weights of more groups twice:
+// 384 groups of 64 rows on average, 1152 x 7168: 870, 622, 680, 733 us).
+static const float kF8Weights[kShapes] = {1.0f, 0.9f, 1.05f, 1.45f};
 
-MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
-  MmPlan m = {0, 0, 1, 16, 16, 0};
+// Steps that a tile's start and end cost, fitted to 50 drawn sizes: in the gated block
+// little more than a product's, whose rounds are compared by their steps alone; with the
+// activation's gradient, which moves 10 bytes an output, what smaller tiles have less of
+// (6546 rows, 240 x 2040: 48.3 us in 128 x 256, 29.8 in 64 x 128).
+static const float kGluStart[kShapes] = {9.f, 8.f, 7.f, 6.f}, kGradStart[kShapes] = {40.f, 38.f, 25.f, 17.f};
+
+// built: a product that mm_tail and the starts above are for (op as the product's).
+enum { kPlain = 0, kBuilt = 1, kBuiltGrad = 2 };
+static MmPlan shape_plan(int op, int type, long E, long R, long N, long K, int built) {
+  MmPlan m = {0, 0, 1, 16, 16, 0, 0};
   const long item = type == MM_I8 || type == MM_F8 ? 1 : 2, groups = E < R ? E : R;
-  // a gated block is chosen for as the product with both its branches' channels
-  if (op == MM_GLU) {
-    m = mm_plan(MM_FORWARD, type, E, R, 2 * N, K);
-    m.cols /= 2;
-    return m;
-  }
-  if (op == MM_GLU_DX) op = MM_DX;
   const long pn = op == MM_FORWARD ? N : K, qn = op == MM_DW ? N : R, outs = op == MM_DW ? E * N : R;
   // Few rows a group: the weights pass once, 16 of their rows a block.  Short rows
   // make for blocks that mostly start and end (64 groups of 5 rows, N = 1024:
@@ -46,6 +51,8 @@ MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
   // estimated for groups of even size, half a tile a group lost.
   long tiles = 0;
   float least = 0.f;
+  const long steps = op == MM_FORWARD ? K * item / 128 : op == MM_DX ? N / 64 : R / E / 64;
+  auto start = [&](int i) { return built ? (built == kBuiltGrad ? kGradStart : kGluStart)[i] : 0.f; };
   for (int i = 0; i < kShapes; i++) {
     const auto &s = kMmShapes[i];
     if (op == MM_DW && i != 0 && i != 2) continue;
@@ -53,7 +60,9 @@ MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
     if (op == MM_DW) rows *= E;
     else if (E > 1) rows = (R + groups * (s.bq / 2)) / s.bq > groups ? (R + groups * (s.bq / 2)) / s.bq : groups;
     const long n = rows * ((pn + s.bp - 1) / s.bp), slots = 256l * s.occ;
-    const float cost = (float)((n + slots - 1) / slots * s.occ) * (float)(s.bq * s.bp) * s.weight;
+    const float weight = type == MM_F8 ? kF8Weights[i] : s.weight;
+    float cost = (float)((n + slots - 1) / slots * s.occ) * (float)(s.bq * s.bp) * weight;
+    if (built) cost *= (float)steps + start(i);
     if (!tiles || cost < least) m.shape = i, least = cost, tiles = n;
   }
   // Short weight gradients write more than they read, and more blocks store better
@@ -69,7 +78,6 @@ MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
   // N = 4608, K = 7168: 45.4 us in parts that fill the chip, 39.6 whole).
   const auto &shape = kMmShapes[m.shape];
   m.rows = shape.bq, m.cols = shape.bp;
-  const long steps = op == MM_FORWARD ? K * item / 128 : op == MM_DX ? N / 64 : R / E / 64;
   const float step = op == MM_DW ? 1.0f : 0.6f;
   const float feed = (float)(tiles * steps * (shape.bq + shape.bp)) * (128 / 12e6f);
   float best = steps * step > feed ? steps * step : feed;
@@ -79,6 +87,37 @@ MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
     if (us < best) best = us, m.splits = (int)n;
   }
   if (m.splits > 1) m.scratch = (size_t)m.splits * outs * pn * 4;
+  if (!built || m.splits > 1) return m;
+  // The last round in parts (mm_tail), in the shapes of two blocks a CU, where its share
+  // of a round and the second launch (about 12 us for a round's parts, in rounds of 1.5 us
+  // a step) cost less than what the best whole rounds do: 32 groups of 512 rows on average
+  // with loads of rank^-0.5, row gradient 1024 x 6144 to the projections 323 -> 267 us; 4097
+  // rows, 2 x 2304 x 7168 242 -> 233 us.  Launches of less than a round gain where the
+  // reduction is long (64 groups of 2 rows on average, 576 x 7168, row gradient: 110 -> 77
+  // us) and lose where it is short (190 rows, 2 x 2024 x 1280: 11.1, 23.0 us; 1302 rows,
+  // 8 bits, 2 x 2152 x 2544: 44.7, 57.4).
+  for (int i = 0; i < 2; i++) {
+    const auto &s = kMmShapes[i];
+    const long rows = E > 1 ? ((R + groups * (s.bq / 2)) / s.bq > groups ? (R + groups * (s.bq / 2)) / s.bq : groups)
+                            : (R + s.bq - 1) / s.bq;
+    const long slots = 256l * s.occ, n = rows * ((pn + s.bp - 1) / s.bp);
+    if (n > 1l << 23) continue;
+    const MmTail t = mm_tail((int)n, (int)slots, (int)steps);
+    if (t.parts < 2 || (t.full == 0 && steps < 64)) continue;
+    const float cost = ((float)(t.full / slots) * ((float)steps + start(i)) + (1.0f / t.parts + 0.05f) * (float)steps + 8.0f) *
+                       s.occ * (float)(s.bq * s.bp) * (type == MM_F8 ? kF8Weights[i] : s.weight);
+    if (cost < least) least = cost, m.shape = i, m.tail = 1, m.rows = s.bq, m.cols = s.bp;
+  }
+  if (m.tail) m.scratch = 256l * kMmShapes[m.shape].occ * kMmShapes[m.shape].bq * kMmShapes[m.shape].bp * 4;
+  return m;
+}
+
+// A gated block is chosen for as the product with both its branches' channels.
+MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
+  if (op == MM_GLU_DX) return shape_plan(MM_DX, type, E, R, N, K, kBuiltGrad);
+  if (op != MM_GLU) return shape_plan(op, type, E, R, N, K, type == MM_F8 ? kBuilt : kPlain);
+  MmPlan m = shape_plan(MM_FORWARD, type, E, R, 2 * N, K, kBuilt);
+  m.cols /= 2;
   return m;
 }
 
@@ -107,7 +146,7 @@ static hipError_t launch_16bit(const MmArgs &a, const MmPlan &m, hipStream_t s) 
 hipError_t launch_mm(const MmArgs &args, hipStream_t s) {
   const MmPlan m = mm_plan(args.op, args.type, args.E, args.R, args.N, args.K);
   MmArgs a = args;
-  a.splits = m.splits;
+  a.splits = m.splits, a.tail = m.tail;
   if (a.type == MM_F8) return launch_fp8(a, m, s);
   if (a.op == MM_GLU || a.op == MM_GLU_DX) return launch_glu(a, m, s);
   return a.type == MM_I8     ? launch_forward<MM_I8>(a, m, s)

@@ -154,7 +154,7 @@ int moe_debug_mm_plan(int op, int E, int R, int N, int K, int *rows, int *cols, 
   TRY(check_op(fn, op, E, R, N, K));
   if (R == 0 || !rows || !cols || !splits) return fail(MOE_EINVAL, "%s: R=0 or a null pointer", fn);
   const moe::MmPlan m = plan_of(op, E, R, N, K);
-  *rows = m.rows, *cols = m.cols, *splits = m.splits;
+  *rows = m.rows, *cols = m.cols, *splits = m.tail ? 0 : m.splits;
   return MOE_OK;
 }
 

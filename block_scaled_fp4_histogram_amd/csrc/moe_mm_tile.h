@@ -240,13 +240,13 @@ constexpr int mm_tile_cols(int op, int bp) { return op == MM_GLU ? bp / 2 : bp; 
 // groups' row gradient of that size: 488, 505, 497, 530).  Every wave does the same work: no barrier.
 constexpr int kMmGroup = 8;
 
-template <int BQ>
-__device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile &t) {
+// pick(number of tiles): this block's tile, or -1.
+template <int BQ, typename Pick>
+__device__ __forceinline__ bool mm_tile_by(const MmArgs &a, int ptiles, MmTile &t, Pick pick) {
   const int lane = threadIdx.x & 63;
   if (!a.first) {                        // one group: the same order without the scans
-    const int total = (a.R + BQ - 1) / BQ, nt = total * ptiles, chunk = (nt + 7) >> 3;
-    const int id = ((int)blockIdx.x & 7) * chunk + ((int)blockIdx.x >> 3);
-    if (((int)blockIdx.x >> 3) >= chunk || id >= nt) return false;
+    const int total = (a.R + BQ - 1) / BQ, id = pick(total * ptiles);
+    if (id < 0) return false;
     const int grp = id / (kMmGroup * ptiles), rem = id - grp * kMmGroup * ptiles;
     const int gcur = min(kMmGroup, total - grp * kMmGroup);
     t.e = 0;
@@ -275,11 +275,10 @@ __device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile
     }
   }
   const int sum = wave_scan(cnt);
-  const int total = uniform(__shfl(sum, 63)), nt = total * ptiles;
-  const int chunk = (nt + 7) >> 3, b = (int)blockIdx.x;
-  const int id = (b & 7) * chunk + (b >> 3);
+  const int total = uniform(__shfl(sum, 63));
   // (a total below zero: offsets that fall, whose groups overlap past 2^31 tiles)
-  if (total <= 0 || (b >> 3) >= chunk || id >= nt) return false;
+  const int id = total <= 0 ? -1 : pick(total * ptiles);
+  if (id < 0) return false;
   const int grp = id / (kMmGroup * ptiles), rem = id - grp * kMmGroup * ptiles;
   const int gcur = min(kMmGroup, total - grp * kMmGroup);
   t.pt = rem / gcur;
@@ -301,6 +300,35 @@ __device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile
   t.row0 = uniform(__shfl(lo, at) + k * BQ);
   t.rows = min(BQ, uniform(__shfl(hi, at)) - t.row0);
   return t.rows > 0;
+}
+
+// Tile of block b of n that each XCD takes an eighth of, or -1.
+__device__ __forceinline__ int mm_eighths(int b, int n) {
+  const int chunk = (n + 7) >> 3, id = (b & 7) * chunk + (b >> 3);
+  return (b >> 3) >= chunk || id >= n ? -1 : id;
+}
+template <int BQ>
+__device__ __forceinline__ bool mm_find_tile(const MmArgs &a, int ptiles, MmTile &t) {
+  return mm_tile_by<BQ>(a, ptiles, t, [](int nt) { return mm_eighths((int)blockIdx.x, nt); });
+}
+
+// The last round of a launch of more than one.  Where its tiles would fill half of the
+// chip's slots or less, each is taken by several blocks, which split its reduction and
+// leave their sums in scratch for k_tail_join to add in order.  (Groups of unequal size
+// make any number of tiles: 32 experts' 16384 rows are 512 tiles of 256 x 128 if all
+// have the same number, one round in 228 us, and 640 with loads of rank^-0.5, 381 us.)
+// full: tiles before them, taken whole; rem: tiles of the last round; parts of each (1: whole).
+constexpr int kTailParts = 8, kTailSteps = 8;      // most parts of a tile, fewest steps of a part
+struct MmTail {
+  int full, rem, parts;
+};
+__host__ __device__ __forceinline__ MmTail mm_tail(int nt, int slots, int steps) {
+  const int full = nt / slots * slots, rem = nt - full;
+  int parts = rem ? slots / rem : 1;
+  parts = parts < kTailParts ? parts : kTailParts;
+  parts = parts < steps / kTailSteps ? parts : steps / kTailSteps;
+  if (parts < 2) return MmTail{nt, 0, 1};
+  return MmTail{full, rem, parts};
 }
 
 // Row of x behind product row r, or -1.
@@ -347,6 +375,9 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   const int ptiles = (pn + BC - 1) / BC;
   MmTile t;
   int q0 = 0, qn, zn;                                           // output rows of the tile, reduction
+  // of the products built on these: a tile of the last round in parts (mm_tail)
+  constexpr bool TAIL = GLU || OP == MM_GLU_DX || F8;
+  int part = 0, parts = 1, tail_at = 0;                         // this block's part, and its tile's number among them
   if (OP == MM_DW) {
     // each group's tiles spread over the XCDs, so that a large group does not load one of them
     const int tiles = ((a.N + BQ - 1) / BQ) * ptiles, per8 = (tiles + 7) >> 3;
@@ -363,15 +394,34 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     qn = min(BQ, a.N - q0);
     zn = t.rows;
   } else {
-    if (!mm_find_tile<BQ>(a, ptiles, t)) return;
+    if (TAIL && a.tail) {
+      const int reduction = FWD ? a.K : a.N, all = (reduction + 128 / ES - 1) / (128 / ES);
+      const bool any = mm_tile_by<BQ>(a, ptiles, t, [&](int nt) {
+        const MmTail m = mm_tail(nt, 256 * MINW, all);
+        const int b = (int)blockIdx.x;
+        if (m.rem == 0 || b < m.full) return mm_eighths(b, m.full);
+        const int u = mm_eighths(b - m.full, m.rem * m.parts);
+        if (u < 0) return -1;
+        part = u / m.rem, parts = m.parts, tail_at = u % m.rem;
+        return m.full + tail_at;
+      });
+      if (!any) return;
+      part = uniform(part), parts = uniform(parts), tail_at = uniform(tail_at);
+    } else if (!mm_find_tile<BQ>(a, ptiles, t)) {
+      return;
+    }
+    if constexpr (F8) {                  // (in scalar registers from here on, or the loads loop over their lanes' resources)
+      t.row0 = uniform(t.row0), t.rows = uniform(t.rows);
+      t.e = uniform(t.e), t.pt = uniform(t.pt);
+    }
     qn = t.rows;
     zn = FWD ? a.K : a.N;
   }
   const int p0 = t.pt * BC;
   constexpr int ZS = (TQ_T || TP_T) ? 64 : 128 / ES;            // reduction elements a step
   // with a split reduction, this block's share of the steps
-  const int all = (zn + ZS - 1) / ZS, share = a.splits > 1 ? (all + a.splits - 1) / a.splits : all;
-  const int begin = (int)blockIdx.y * share, steps = min(all, begin + share);
+  const int all = (zn + ZS - 1) / ZS, cut = TAIL && parts > 1 ? parts : a.splits, share = cut > 1 ? (all + cut - 1) / cut : all;
+  const int begin = (TAIL && parts > 1 ? part : (int)blockIdx.y) * share, steps = min(all, begin + share);
 
   // ---- loads of one step
   const uint8_t *x = (const uint8_t *)a.x, *dy = (const uint8_t *)a.dy;
@@ -404,6 +454,11 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   constexpr int HP = TP / 2;
   static_assert(!GLU || (DP <= HP && HP % DP == 0), "branches of P");
   const Rsrc rp = FWD ? mm_rsrc(wt + (size_t)(p0 + (GLU ? a.glu.gate0 : 0)) * ldx, (uint32_t)min(BC, pn - p0) * ldx) : mm_rsrc(wt, 0);
+  // Gathered rows within 2 GiB are loaded through one resource over x, as rows in order are.
+  constexpr bool NEAR = GATHER && TAIL;
+  bool near = false;
+  if constexpr (NEAR) near = a.x_rows * (long)ldx < 0x7FFFFFFFl;
+  const Rsrc rx = mm_rsrc(x, (uint32_t)(near ? a.x_rows * (long)ldx : 0));
   const Rsrc rup = GLU ? mm_rsrc(wt + (size_t)(p0 + a.glu.up0) * ldx, (uint32_t)min(BC, pn - p0) * ldx) : rp;
   // forward gather: each load's row of x
   constexpr bool GF = GATHER && FWD, GW = GATHER && OP == MM_DW;
@@ -413,6 +468,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     for (int i = 0; i < CQ; i++) {
       const int r = rq0 + i * DQ;
       grow[i] = r < qn ? (int)mm_x_row(a, t.row0 + r) : -1;
+      if constexpr (NEAR) if (near) grow[i] = grow[i] < 0 ? (int)kOutside : (int)((uint32_t)grow[i] * ldx + cq);
     }
   }
   // weight gradient gather: rows of x behind this lane's rows of step s, read one
@@ -439,6 +495,14 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
 #pragma unroll
     for (int i = 0; i < CQ; i++) {
       lds_void *dst = (lds_void *)(lq + i * NW * 1024);
+      if constexpr (NEAR) {
+        if (near) {
+          const Rsrc sx = TQ_T ? sq : rx;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(sx, dst, 16, (int)(NEAR && (int)cq < left ? (uint32_t)grow[GF ? i : 0] : kOutside),
+                                                   TQ_T ? 0 : s * 128, 0, 0);
+          continue;
+        }
+      }
       if constexpr (GF) {
         const bool ok = grow[i] >= 0 && (int)cq < left;
         const uint8_t *g = ok ? x + ((size_t)(uint32_t)grow[i] * ldx + (cq + s * 128)) : (const uint8_t *)g_mm_zeros;
@@ -650,7 +714,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       read8(1);
     } else {
       read(0);
-      if (GATHER) {
+      if (GATHER && !NEAR) {
         mul(0);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -666,7 +730,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     if constexpr (F8) {
       mul8(1);
     } else {
-      if (!GATHER) mul(0);
+      if (!GATHER || NEAR) mul(0);
       mul(1);
     }
   }
@@ -717,15 +781,18 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
         if (row < 16 && q < qn && c < pn) o((long)t.row0 + q, c, d);
       }
     };
-    if (a.splits > 1) {
-      float *part = a.part + (long)blockIdx.y * a.R * 2 * pn;
+    if (a.splits > 1 || parts > 1) {
+      // [gate, up][row][column] of a tile's part, or the rows' columns as w has them
+      const bool tile = parts > 1;
+      float *sum = a.part + (tile ? ((long)tail_at * parts + part) * BQ * BP : (long)blockIdx.y * a.R * 2 * pn);
 #pragma unroll
       for (int j = 0; j < NQ; j++)
 #pragma unroll
         for (int b = 0; b < 2; b++) {
           const int c0 = b ? a.glu.up0 : a.glu.gate0;
-          rows_out(MmConst<4>{}, j, [&](int i, int k) { return acc[b * NG + i][j][k]; },
-                   [&](long r, int c, v4i d) { *(v4i *)(part + r * 2 * pn + c0 + c) = d; });
+          rows_out(MmConst<4>{}, j, [&](int i, int k) { return acc[b * NG + i][j][k]; }, [&](long r, int c, v4i d) {
+            *(v4i *)(sum + (tile ? (long)((b * BQ + (int)(r - t.row0)) * BC + c - p0) : r * 2 * pn + c0 + c)) = d;
+          });
         }
       return;
     }
@@ -764,7 +831,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     });
     return;
   }
-  if constexpr (OP == MM_GLU_DX) if (a.splits <= 1) {
+  if constexpr (OP == MM_GLU_DX) if (a.splits <= 1 && parts <= 1) {
     // 16 rows of 64 columns of dh, eight columns a lane, with the projections there
     constexpr int RB = 64 * 4 + 16;
 #pragma unroll
@@ -785,13 +852,13 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       }
     return;
   }
-  mm_by_output(a.splits > 1 ? MM_PART : a.out_type, [&](auto out) {
+  mm_by_output(a.splits > 1 || parts > 1 ? MM_PART : a.out_type, [&](auto out) {
     constexpr int OUT = decltype(out)::value;
     constexpr bool WIDE = OUT == MM_FP32 || OUT == MM_PART, NT = OP == MM_DW && OUT != MM_PART;
     constexpr int RB = WIDE ? 64 * 4 + 16 : 64 * 2 + 16;   // a row, and 16 bytes that spread the rows over the banks
     constexpr int LR = WIDE ? 16 : 8, CW = 64 / LR;        // lanes a row, columns a lane
     const long outs = OP == MM_DW ? (long)a.E * a.N : (long)a.R;
-    float *part = a.part + (OUT == MM_PART ? (long)blockIdx.y * outs * pn : 0);
+    float *sums = a.part + (OUT == MM_PART && parts <= 1 ? (long)blockIdx.y * outs * pn : 0);
 #pragma unroll
     for (int i0 = 0; i0 < NP; i0 += 4) {
       const int pc = p0 + wp * TP + 16 * i0, po = pc + CW * (lane % LR);
@@ -827,7 +894,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
           const v4i d = *(const v4i *)(mine + row * RB + (lane % LR) * 16);
           if (q >= qn || po >= pn) continue;
           const long at = (orow + q) * pn + po;
-          if constexpr (OUT == MM_PART) *(v4i *)(part + at) = d;
+          if constexpr (OUT == MM_PART) *(v4i *)(sums + (parts > 1 ? ((long)tail_at * parts + part) * BQ * BP + q * BP + po - p0 : at)) = d;
           else if constexpr (OUT == MM_FP32) mm_store_f32<NT>(a, at, __builtin_bit_cast(v4f, d));
           else mm_store<NT>((v4i *)((uint16_t *)a.out + at), d);
         }
@@ -892,6 +959,40 @@ __global__ __launch_bounds__(256) void k_mm_join(MmArgs a) {
   });
 }
 
+// Eight columns from p of row `row` out of their joined sums, sum(b, s) for branch b (gate,
+// up) or of the only one: as they are, through the activation, or dh through its gradient.
+template <int OP, int TYPE, typename Sum>
+__device__ __forceinline__ void glu_finish(const MmArgs &a, int pn, long row, int p, Sum sum) {
+  v4f s[2][2];
+  sum(0, s[0]);
+  if constexpr (OP == MM_GLU_DX) {
+    glu_back8<TYPE>(a.glu, pn, a.pre, a.out, a.h, row, p, s[0][0], s[0][1]);
+  } else {
+    float v[8];
+    if constexpr (OP == MM_GLU) {
+      sum(1, s[1]);
+      if constexpr (TYPE == MM_BF16 || TYPE == MM_FP16) {
+        if (a.pre_out) {
+#pragma unroll
+          for (int b = 0; b < 2; b++)
+            *(v4i *)((uint16_t *)a.pre_out + row * 2 * pn + (b ? a.glu.up0 : a.glu.gate0) + p) =
+                v4i{(int)mm_pack<TYPE>(s[b][0][0], s[b][0][1]), (int)mm_pack<TYPE>(s[b][0][2], s[b][0][3]),
+                    (int)mm_pack<TYPE>(s[b][1][0], s[b][1][1]), (int)mm_pack<TYPE>(s[b][1][2], s[b][1][3])};
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      if constexpr (OP == MM_GLU) v[k] = glu_act(s[0][k >> 2][k & 3], s[1][k >> 2][k & 3], a.glu);
+      else v[k] = s[0][k >> 2][k & 3];
+    }
+    mm_by_output(a.out_type, [&](auto out) {
+      constexpr int OUT = decltype(out)::value;
+      if constexpr (OUT != MM_PART) mm_store8<OUT>(a, row * pn + p, v);
+    });
+  }
+}
+
 // The same for the gated block: the parts of both projections, then the activation,
 // or the parts of dh, then its gradient.
 template <int OP, int TYPE>
@@ -908,57 +1009,67 @@ __global__ __launch_bounds__(256) void k_glu_join(MmArgs a) {
     }
     if (!in) return;
   }
-  for (int p = threadIdx.x * 8; p < pn; p += 256 * 8) {
-    auto sum = [&](int c, v4f *s) {
+  for (int p = threadIdx.x * 8; p < pn; p += 256 * 8)
+    glu_finish<OP, TYPE>(a, pn, row, p, [&](int b, v4f *s) {
+      const int c = OP != MM_GLU ? p : p + (b ? a.glu.up0 : a.glu.gate0);
       s[0] = s[1] = v4f{0.f, 0.f, 0.f, 0.f};
       for (int i = 0; i < a.splits; i++) {
         const v4f *part = (const v4f *)(a.part + ((long)i * a.R + row) * wide + c);
         s[0] += part[0];
         s[1] += part[1];
       }
-    };
-    if constexpr (OP == MM_GLU_DX) {
-      v4f d[2];
-      sum(p, d);
-      glu_back8<TYPE>(a.glu, pn, a.pre, a.out, a.h, row, p, d[0], d[1]);
-    } else {
-      v4f gate[2], up[2];
-      sum(a.glu.gate0 + p, gate);
-      sum(a.glu.up0 + p, up);
-      if constexpr (TYPE == MM_BF16 || TYPE == MM_FP16) {
-        if (a.pre_out) {
-#pragma unroll
-          for (int b = 0; b < 2; b++) {
-            const v4f *s = b ? up : gate;
-            *(v4i *)((uint16_t *)a.pre_out + row * 2 * pn + (b ? a.glu.up0 : a.glu.gate0) + p) =
-                v4i{(int)mm_pack<TYPE>(s[0][0], s[0][1]), (int)mm_pack<TYPE>(s[0][2], s[0][3]),
-                    (int)mm_pack<TYPE>(s[1][0], s[1][1]), (int)mm_pack<TYPE>(s[1][2], s[1][3])};
-          }
-        }
-      }
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; k++) v[k] = glu_act(gate[k >> 2][k & 3], up[k >> 2][k & 3], a.glu);
-      mm_by_output(a.out_type, [&](auto out) {
-        constexpr int OUT = decltype(out)::value;
-        if constexpr (OUT != MM_PART) mm_store8<OUT>(a, row * pn + p, v);
-      });
+    });
+}
+
+// Joins the parts of the last round's tiles: a block per tile and what rows of it 256
+// threads have at eight columns each.
+template <int OP, int TYPE, int BQ, int BP, int MINW>
+__global__ __launch_bounds__(256) void k_tail_join(MmArgs a) {
+  constexpr int BC = mm_tile_cols(OP, BP), TR = BC / 8, ES = sizeof(typename MmElem<TYPE>::t);
+  const int pn = mm_outs(OP, a.N, a.K), ptiles = (pn + BC - 1) / BC;
+  const int reduction = mm_forward(OP) ? a.K : a.N, all = (reduction + 128 / ES - 1) / (128 / ES);
+  MmTile t;
+  int parts = 1;
+  const int at = (int)blockIdx.x;
+  if (!mm_tile_by<BQ>(a, ptiles, t, [&](int nt) {
+        const MmTail m = mm_tail(nt, 256 * MINW, all);
+        parts = m.parts;
+        return at < m.rem ? m.full + at : -1;
+      }))
+    return;
+  const float *tile = a.part + (long)at * parts * BQ * BP;
+  const int c = (int)threadIdx.x % TR * 8, p = t.pt * BC + c;
+  if (p >= pn) return;
+  const int q = (int)blockIdx.y * (256 / TR) + (int)threadIdx.x / TR;
+  if (q >= t.rows) return;
+  glu_finish<OP, TYPE>(a, pn, (long)t.row0 + q, p, [&](int b, v4f *s) {
+    const float *v = tile + (b * BQ + q) * BC + c;
+    s[0] = s[1] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < parts; i++) {
+      s[0] += *(const v4f *)(v + (long)i * BQ * BP);
+      s[1] += *(const v4f *)(v + (long)i * BQ * BP + 4);
     }
-  }
+  });
 }
 
 template <int OP, int TYPE, int BQ, int BP, int WQ, int WP, int MINW>
 static hipError_t launch_tile(const MmArgs &a, hipStream_t s) {
+  constexpr bool TAIL = OP == MM_GLU || OP == MM_GLU_DX || TYPE == MM_F8 || TYPE == MM_F8X;
   constexpr int BC = mm_tile_cols(OP, BP);
   const long pn = mm_outs(OP, a.N, a.K), ptiles = (pn + BC - 1) / BC;
   long blocks;
   if (OP == MM_DW) blocks = 8l * a.E * (((a.N + BQ - 1) / BQ * ptiles + 7) / 8);
   else blocks = (((a.R + BQ - 1) / BQ + (a.first ? (a.E < a.R ? a.E : a.R) : 0)) * ptiles + 7) / 8 * 8;
+  const long slots = 256 * MINW;
+  if (TAIL && a.tail) blocks += slots;   // the last round's parts
   if (blocks > INT32_MAX / (64 * WQ * WP)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks, (unsigned)a.splits), threads(64 * WQ * WP);
   // (row gradients have no gathered rows)
   if (!mm_dx(OP) && a.rows) hipLaunchKernelGGL((k_mm_tile<OP, TYPE, BQ, BP, WQ, WP, !mm_dx(OP), MINW>), grid, threads, 0, s, a);
   else hipLaunchKernelGGL((k_mm_tile<OP, TYPE, BQ, BP, WQ, WP, false, MINW>), grid, threads, 0, s, a);
+  if constexpr (TAIL) {
+    if (a.tail) hipLaunchKernelGGL((k_tail_join<OP, TYPE, BQ, BP, MINW>), dim3((unsigned)(slots / 2), BQ * BC / 2048), dim3(256), 0, s, a);
+  }
   if (a.splits > 1) {
     const long outs = OP == MM_DW ? (long)a.E * a.N : (long)a.R;
     if constexpr (OP == MM_GLU || OP == MM_GLU_DX) hipLaunchKernelGGL((k_glu_join<OP, TYPE>), dim3((unsigned)outs), dim3(256), 0, s, a);

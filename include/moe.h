@@ -556,7 +556,8 @@ int moe_debug_route(moe_plan_t plan, const moe_tier *tiers, int n_tiers, const i
  * moe_debug_mm_plan -- how a product of these sizes runs (op as in moe_mm_op, so
  * that the tests of the tile shapes run the shapes they name): output rows and
  * columns of a tile (16 x 16, for a gated block 16 x 8: few rows a group, weights streamed) and the parts of
- * its reduction.  Host only; MOE_EINVAL or MOE_EUNSUPPORTED on sizes that the call
+ * its reduction (0, of the gated and 8-bit floating-point products: where the tiles
+ * of the last round fill half of it or less, these alone are split).  Host only; MOE_EINVAL or MOE_EUNSUPPORTED on sizes that the call
  * refuses and for R = 0.
  */
 int moe_debug_mm_plan(int op, int E, int R, int N, int K, int *rows, int *cols, int *splits);

@@ -169,12 +169,15 @@ def test_dense_gated_block(M_, I, K, form):
 TILES = [(16, 16), (64, 128), (128, 128), (128, 256), (256, 128)]
 
 
-def sizes_for(op, shape, K):
+def sizes_for(op, shape, parts, reductions=(144, 272, 528, 1040, 2064, 4112)):
+    """The least sizes of a list, (counts, N, K), for which the plan names this shape and these parts of the
+    reduction (0: of the last round's tiles)."""
     found = None
-    for c, e, n in itertools.product([11, 70, 130, 260, 600, 1000, 2561], [3, 9, 12, 24, 40], [72, 136, 264, 520, 600, 1032, 2056]):
+    for c, e, n, k in itertools.product([11, 70, 130, 260, 600, 1000, 2561], [3, 9, 12, 24, 40],
+                                        [72, 136, 264, 520, 600, 1032, 2056], reductions):
         counts = [c + 3, 0, c - 2] + [c] * (e - 3)
-        if M.debug_mm_plan(op, e, sum(counts), n, K) == (*shape, 1) and (found is None or sum(counts) * n < found[0]):
-            found = (sum(counts) * n, counts, n)
+        if (found is None or sum(counts) * n * k < found[0]) and M.debug_mm_plan(op, e, sum(counts), n, k) == (*shape, parts):
+            found = (sum(counts) * n * k, counts, n, k)
     assert found, f"no sizes with tiles of {shape}"
     return found[1:]
 
@@ -185,8 +188,7 @@ def sizes_for(op, shape, K):
 def test_tiles(shape, gathered, glu):
     """Every tile shape over two blocks of K and a short one, with NaN codes and scales next to rows and columns
     that are not theirs, and rows outside the groups."""
-    K = 4112 if shape == (16, 16) else 272
-    counts, N = sizes_for(M.MM_FP8_GLU, (shape[0], shape[1] // 2), K) if glu else sizes_for(M.MM_FP8, shape, K)
+    counts, N, K = sizes_for(M.MM_FP8_GLU, (shape[0], shape[1] // 2), 1) if glu else sizes_for(M.MM_FP8, shape, 1)
     R = sum(counts)
     x, xs, w, ws, first, rows = _case(counts, N, K, False, glu=glu, seed=N)
     if gathered:
@@ -219,6 +221,33 @@ def test_tiles(shape, gathered, glu):
     assert not bool(torch.isfinite(got[bad - 1]).all())
 
 
+@pytest.mark.parametrize("out_dtype", [BF16, FP32])
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("shape", [(128, 256), (256, 128)])
+def test_last_rounds_in_parts(shape, glu, out_dtype):
+    """The tiles of a last round, split and joined, with scratch full of NaN; fp32 results take other tiles."""
+    op = M.MM_FP8_GLU if glu else M.MM_FP8
+    try:
+        counts, N, K = sizes_for(op, (shape[0], shape[1] // 2) if glu else shape, 0)
+    except AssertionError:
+        assert shape == (256, 128)            # (128 x 256 is the better of the two almost everywhere)
+        return
+    R, E = sum(counts), len(counts)
+    x, xs, w, ws, first, rows = _case(counts, N, K, True, glu=glu, seed=N)
+    first[-1] -= 2
+    scratch = torch.full((M.mm_scratch_bytes(op, E, R, N, K),), 255, dtype=torch.uint8, device="cuda")
+    out = torch.full((R, N), 7.5, dtype=out_dtype, device="cuda")
+    call = M.grouped_fp8_glu if glu else M.grouped_fp8_mm
+    call(x, xs, w, ws, first, rows=rows, out=out, scratch=scratch)
+    case = (x, xs, w, ws, first, rows)
+    if glu:
+        _check_glu(out, case, {}, keep=slice(0, -2))
+    else:
+        _check(out, case, keep=slice(0, -2))
+    assert bool((out[-2:] == 7.5).all())
+    assert torch.equal(call(x, xs, w, ws, first, rows=rows, out_dtype=out_dtype)[:-2], out[:-2])
+
+
 @pytest.mark.parametrize("counts,N,K", [([300], 64, 8192), ([90, 0, 140], 72, 8192), ([200], 72, 8208)])
 @pytest.mark.parametrize("glu", [False, True])
 @pytest.mark.parametrize("gathered", [False, True])
@@ -235,6 +264,19 @@ def test_split_reductions(counts, N, K, glu, gathered):
         else:
             _check(out, (x, xs, w, ws, first, rows), keep=slice(0, -1))
         assert bool((out[-1] == 7.5).all())
+
+
+@pytest.mark.parametrize("glu", [False, True])
+def test_last_rounds_of_a_dense_product(glu):
+    """More tiles than a round has, the rest in parts."""
+    T, N, K = 4097, 2304 if glu else 4608, 4112
+    assert M.debug_mm_plan(M.MM_FP8_GLU if glu else M.MM_FP8, 1, T, N, K)[2] == 0
+    x, xs, w, ws, first, _ = _case([T], N, K, False, glu=glu, seed=K)
+    case = (x, xs, w, ws, first, None)
+    if glu:
+        _check_glu(M.fp8_glu(x, xs, w[0], ws[0]), case, {})
+    else:
+        _check(M.fp8_mm(x, xs, w[0], ws[0]), case)
 
 
 # pairs of scales whose product leaves fp32's range, or whose x scale times the sum does, while the result

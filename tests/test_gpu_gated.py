@@ -206,14 +206,20 @@ TILES = [(16, 8), (64, 64), (128, 64), (128, 128), (256, 64)]
 TILES_DX = [(64, 128), (128, 128), (128, 256), (256, 128)]
 
 
-def sizes_for(op, shape, reduction):
-    """The least counts and I of a list for which the plan names this shape, unsplit."""
+def plan_of(op, counts, I, reduction):
+    n, k = (reduction, I) if op == M.MM_GLU_DX else (I, reduction)
+    return M.debug_mm_plan(op, len(counts), sum(counts), n, k)
+
+
+def sizes_for(op, shape, parts, reductions=(72, 136, 264, 520, 1032, 2056, 4104)):
+    """The least sizes of a list, (counts, I, reduction), for which the plan names this shape and these parts of
+    the reduction (0: of the last round's tiles)."""
     found = None
-    for c, e, I in itertools.product([11, 70, 130, 260, 600, 1000, 2561], [3, 9, 12, 24, 40], [72, 136, 264, 520, 600, 1032, 2056]):
+    for c, e, I, k in itertools.product([11, 70, 130, 260, 600, 1000, 2561], [3, 9, 12, 24, 40],
+                                        [72, 136, 264, 520, 600, 1032, 2056], reductions):
         counts = [c + 3, 0, c - 2] + [c] * (e - 3)
-        n, k = (I, reduction) if op == M.MM_GLU else (reduction, I)
-        if M.debug_mm_plan(op, e, sum(counts), n, k) == (*shape, 1) and (found is None or sum(counts) * I < found[0]):
-            found = (sum(counts) * I, counts, I)
+        if (found is None or sum(counts) * I * k < found[0]) and plan_of(op, counts, I, k) == (*shape, parts):
+            found = (sum(counts) * I * k, counts, I, k)
     assert found, f"no sizes with tiles of {shape}"
     return found[1:]
 
@@ -223,8 +229,7 @@ def sizes_for(op, shape, reduction):
 @pytest.mark.parametrize("shape", TILES)
 def test_forward_tiles(shape, dtype, gathered):
     """Infinities and NaNs stay in the rows and columns they belong to, over tiles' ends and groups'."""
-    K = 2056 if shape == (16, 8) else 72
-    counts, I = sizes_for(M.MM_GLU, shape, K)
+    counts, I, K = sizes_for(M.MM_GLU, shape, 1)
     R, E = sum(counts), len(counts)
     g = _gen(I)
     x, w = _normal(g, R, K, dtype=dtype), _normal(g, E, 2 * I, K, dtype=dtype, scale=K ** -0.5)
@@ -254,8 +259,7 @@ TILES_DX = {(64, 128): ([70] * 12, 1200, 72), (128, 128): ([130] * 40, 1032, 72)
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 @pytest.mark.parametrize("shape", TILES_DX)
 def test_backward_tiles(shape, dtype):
-    N = 72
-    counts, I = sizes_for(M.MM_GLU_DX, shape, N)
+    counts, I, N = sizes_for(M.MM_GLU_DX, shape, 1)
     dy, w, pre, first = _backward_case(counts, N, I, dtype, seed=I)
     d_pre, h = M.grouped_glu_dx(dy, w, pre, first, keep_h=True, limit=2.0)
     dh, mag, _ = ref_dx(dy, w, first)
@@ -270,7 +274,55 @@ def test_backward_tiles(shape, dtype):
     assert torch.equal(d2[keep], d_pre[keep])
     keep_h = torch.ones_like(h, dtype=torch.bool)
     keep_h[bad + 1, 5] = False
-    assert torch.equal(h2[keep_h], h[keep_h]) and bool(d2[bad + 1, I + 5].isnan()) and bool(h2[bad + 1, 5].isnan())
+    assert torch.equal(h2[keep_h], h[keep_h]) and bool(h2[bad + 1, 5].isnan())
+    assert bool(d2[bad + 1, I + 5].isnan()) == (float(pre[bad + 1, I + 5]) <= 2.0)   # (a gate beyond the limit has no gradient)
+
+
+LAST_ROUNDS = [(M.MM_GLU, (128, 128)), (M.MM_GLU, (256, 64)), (M.MM_GLU_DX, (128, 256)), (M.MM_GLU_DX, (256, 128))]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("op,shape", LAST_ROUNDS)
+def test_last_rounds_in_parts(op, shape, dtype):
+    """The tiles of a last round, split and joined: every row against the reference, twice the same bits, rows in
+    no group left alone, and no tile joined from another call's sums (scratch full of NaN)."""
+    counts, I, K = sizes_for(op, shape, 0)
+    R, E = sum(counts), len(counts)
+    scratch = torch.full((M.mm_scratch_bytes(op, E, R, *((K, I) if op == M.MM_GLU_DX else (I, K))),), 255, dtype=torch.uint8, device="cuda")
+    out2, h2 = torch.full((R, 2 * I), 7.5, dtype=dtype, device="cuda"), torch.full((R, I), 7.5, dtype=dtype, device="cuda")
+    if op == M.MM_GLU:
+        x, w, first, rows = _forward_case(counts, I, K, dtype, True, seed=I)
+        first[-1] -= 2
+        M.grouped_glu(x, w, first, rows=rows, out=h2, pre=out2, scratch=scratch, limit=1.5)
+        ref, mag, _ = ref_mm(x, w, first, rows, R)
+        check_forward(h2[:-2], out2[:-2], ref[:-2], mag[:-2], K, dict(limit=1.5))
+        h, out = M.grouped_glu(x, w, first, rows=rows, keep_pre=True, limit=1.5)
+    else:
+        dy, w, pre, first = _backward_case(counts, K, I, dtype, seed=I)
+        first[-1] -= 2
+        M.grouped_glu_dx(dy, w, pre, first, out=out2, h=h2, scratch=scratch, limit=1.5)
+        dh, mag, _ = ref_dx(dy, w, first)
+        check_backward(out2[:-2], h2[:-2], dh[:-2], (K + 1) * 2.0 ** -24 * mag[:-2], pre[:-2], dict(limit=1.5))
+        out, h = M.grouped_glu_dx(dy, w, pre, first, keep_h=True, limit=1.5)
+    assert torch.equal(out[:-2], out2[:-2]) and torch.equal(h[:-2], h2[:-2])
+    assert bool((out2[-2:] == 7.5).all()) and bool((h2[-2:] == 7.5).all())
+
+
+def test_last_rounds_of_a_dense_block():
+    """4097 rows: a whole round and a few tiles; and groups so unequal that the estimate of the tiles is far off."""
+    g = _gen(4)
+    T, I, K = 4097, 2304, 2056
+    assert plan_of(M.MM_GLU, [T], I, K)[2] == 0
+    x, w = _normal(g, T, K), _normal(g, 2 * I, K, scale=K ** -0.5)
+    h, pre = M.glu(x, w, keep_pre=True)
+    ref, mag, _ = ref_mm(x, w[None], offsets([T]), None, T)
+    check_forward(h, pre, ref, mag, K, {})
+    for counts in ([T - 5, 1, 1, 1, 1, 1], [1] * 5 + [T - 5], [700, 0, 700, 0, 2697, 0]):
+        w6 = _normal(g, 6, 2 * I, K, scale=K ** -0.5)
+        first = offsets(counts).cuda()
+        h = M.grouped_glu(x, w6, first)
+        ref, mag, _ = ref_mm(x, w6, first, None, T)
+        check_forward(h, None, ref, mag, K, {})
 
 
 @pytest.mark.parametrize("counts,I,K", [([300], 64, 8192), ([90, 0, 140], 72, 8192), ([200], 72, 4096)])
@@ -331,6 +383,16 @@ def test_offsets_that_go_wrong_stay_in_bounds():
         d_pre = M.grouped_glu_dx(dy, wd, pre, first)
         dh, mag, _ = ref_dx(dy[:20], wd[:1], offsets([20]))
         check_backward(d_pre[:10], None, dh[:10], 73 * 2.0 ** -24 * mag[:10], pre[:10], {})
+
+
+def test_last_rounds_of_a_dense_backward():
+    """More tiles than a round has, the rest in parts: the estimate is exact for one group."""
+    T, I, N = 4097, 4360, 1032
+    assert plan_of(M.MM_GLU_DX, [T], I, N)[2] == 0 and T // 128 * (I // 256) >= 512
+    dy, w, pre, first = _backward_case([T], N, I, BF16, seed=2)
+    d_pre, h = M.glu_dx(dy, w[0], pre, keep_h=True, limit=2.0)
+    dh, mag, _ = ref_dx(dy, w, first)
+    check_backward(d_pre, h, dh, (N + 1) * 2.0 ** -24 * mag, pre, dict(limit=2.0))
 
 
 class _GatedExperts(torch.autograd.Function):
