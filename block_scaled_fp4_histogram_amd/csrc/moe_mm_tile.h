@@ -367,7 +367,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   constexpr int kOutStage = 16 * (64 * 4 + 16);                 // of one wave, for its outputs
   static_assert(NW * kOutStage <= kStage, "outputs through LDS");
   __shared__ __align__(1024) uint8_t lds[kStage];
-  __shared__ __align__(16) float xsl[F8 ? BQ * 4 : 4];          // scales of x's rows: four blocks of K
+  __shared__ __align__(16) float xsl[F8 ? 2 * BQ * 4 : 4];      // scales of x's rows: twice four blocks of K
 
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   constexpr int BC = mm_tile_cols(OP, BP);
@@ -561,15 +561,17 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   // ---- scales of 8-bit floating point: a row of x has one a step, so has the tile's
   // part of w (two in a gated block: its branches').  w's are read a step ahead into
   // scalar registers; x's, with the tiles, four steps' at once straight to LDS, as
-  // [row][4], or [4][row] from rows of fewer than four.  (A load a row and step into
-  // registers, 16 lines a quarter wave, took half the kernel's time.)
+  // [row][4], or [4][row] from rows of fewer than four, and from there a step ahead.
+  // (A load a row and step into registers, 16 lines a quarter wave, took half the
+  // kernel's time; read from LDS where they are used, a tenth of what is left.)
   const int kbs = (a.K + kF8Block - 1) / kF8Block;
   static_assert(!F8 || kF8Block % TP == 0, "a wave's columns of one block");
   constexpr int NW8 = F8 && GLU ? 2 : 1, XW = F8 ? (BQ / 64 + NW - 1) / NW : 1;
   const float *sxp[XW];
   const MmConstF *swp[NW8];
   float sw[NW8];
-  int sx0 = 0;                                                  // first block of K in LDS
+  int sx0 = 0, sxr = 0, xhalf = 0;                              // first block of K last loaded, and read; the latter's half
+  const int xstep = kbs >= 4 ? 1 : BQ, xrow = kbs >= 4 ? 4 : 1;
   if constexpr (F8) {
 #pragma unroll
     for (int i = 0; i < XW; i++) {
@@ -588,24 +590,39 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   }
   auto load_scales = [&](int s) {
     if constexpr (F8) {
-#pragma unroll
-      for (int i = 0; i < NW8; i++) sw[i] = swp[i][s];
-      if (s > begin && s < sx0 + 4) return;
+      if (s >= steps || (s > begin && s < sx0 + 4)) return;
       sx0 = kbs < 4 ? 0 : min(s, kbs - 4);
+      float *xs = xsl + (s > begin ? (xhalf ^ 1) * BQ * 4 : 0);
 #pragma unroll
       for (int i = 0; i < XW; i++) {
         const int r0 = (i * NW + w) * 64;
         if (r0 >= BQ) break;
         if (kbs >= 4) {
           const float *p = sxp[i] ? sxp[i] + sx0 : (const float *)g_mm_zeros;
-          __builtin_amdgcn_global_load_lds(p, (lds_void *)(xsl + r0 * 4), 16, 0, 0);
+          __builtin_amdgcn_global_load_lds(p, (lds_void *)(xs + r0 * 4), 16, 0, 0);
         } else {
           for (int k = 0; k < kbs; k++) {
             const float *p = sxp[i] ? sxp[i] + k : (const float *)g_mm_zeros;
-            __builtin_amdgcn_global_load_lds(p, (lds_void *)(xsl + k * BQ + r0), 4, 0, 0);
+            __builtin_amdgcn_global_load_lds(p, (lds_void *)(xs + k * BQ + r0), 4, 0, 0);
           }
         }
       }
+    }
+  };
+  auto load_w = [&](int s) {
+    if constexpr (F8) {
+#pragma unroll
+      for (int i = 0; i < NW8; i++) sw[i] = swp[i][s];
+    }
+  };
+  float sx[F8 ? NQ : 1];
+  auto read_x = [&](int s) {             // (s past the last step: the last)
+    if constexpr (F8) {
+      s = min(s, steps - 1);
+      if (kbs >= 4 && s >= sxr + 4) sxr = sx0, xhalf ^= 1;
+      const float *xs = xsl + (wq * TQ + l16) * xrow + xhalf * BQ * 4 + (s - sxr) * xstep;
+#pragma unroll
+      for (int j = 0; j < NQ; j++) sx[j] = xs[16 * j * xrow];
     }
   };
 
@@ -630,6 +647,14 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     gather_rows(begin);
     load(begin);
     load_scales(begin);
+    load_w(begin);
+    if constexpr (F8) {
+      sxr = sx0;
+      __builtin_amdgcn_s_waitcnt(0);
+      mm_barrier();
+      read_x(begin);
+      load_scales(begin + 1);
+    }
     gather_rows(begin + 1);
   }
   for (int s = begin; s < steps; s++) {
@@ -695,14 +720,14 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
     if constexpr (F8) {
 #pragma unroll
       for (int j = 0; j < NQ; j++) {
-        const int q = wq * TQ + 16 * j + l16;
-        zx[j] = mm_scale8(xsl[kbs >= 4 ? q * 4 + s - sx0 : s * BQ + q]);
+        zx[j] = mm_scale8(sx[j]);
 #pragma unroll
         for (int h = 0; h < 2; h++) fq[h][j] = frag_q(lq, j, h);
       }
 #pragma unroll
       for (int i = 0; i < NW8; i++) zw[i] = mm_scale8(sw[i]);
       read8(0);
+      read_x(s + 1);
       mul8(0);
       // (kept in front of the second half's reads and the branch below: sunk past them, both
       // halves' operands would be live and the accumulators spill)
@@ -724,7 +749,8 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       wait_lgkm0();                      // the stage is free once every wave has read it
       mm_barrier();
       load(s + 1);
-      load_scales(s + 1);
+      load_w(s + 1);
+      load_scales(s + 2);
       gather_rows(s + 2);
     }
     if constexpr (F8) {
