@@ -535,7 +535,8 @@ def quant_fp8(x, out=None, scales=None, stream=None):
 
 def fp8_mm(x, x_scales, w, w_scales, out=None, out_dtype=None, scratch=None, stream=None):
     """8-bit floating-point product with a scale for each block of 128 (moe_grouped_fp8_mm): x and w times
-    their scales, x @ w.T, the sums in 32 bits.
+    their scales, x @ w.T, the sums in 32 bits (with out_dtype torch.float32 throughout; 16-bit results of more
+    than a few rows drop what lies 2^-13 below the largest of each eight products).
 
     x float8_e4m3fn [M, K], x_scales fp32 [M, ceil(K / 128)], w float8_e4m3fn [N, K], w_scales fp32
     [ceil(N / 128), ceil(K / 128)]; out [M, N] bf16 (default), fp16 or fp32."""

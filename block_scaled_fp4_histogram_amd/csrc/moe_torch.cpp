@@ -408,7 +408,7 @@ bool truth(PyObject *o) {
   if (v < 0) throw PythonError();
   return v;
 }
-// An output that is made, given, or neither made nor given (want false).
+// A given output among the operands (undefined: not given).
 Tensor optional_out(Operands &ops, PyObject *given, const char *name, at::IntArrayRef shape, ScalarType type) {
   if (none(given)) return Tensor();
   return ops.add(tensor(given, name), name, {type}, shape);

@@ -480,18 +480,23 @@ int moe_glu_grad(int dtype, const void *dh, const void *pre, int R, int I, const
  * scales[r, b] = fp32(amax / 448) of the block's largest magnitude, q = x * fp32(448 / amax)
  * rounded to fp32, then to the nearest code, ties to even.  A block of zeros has scale 0
  * and codes 0; one that holds an infinity or NaN has scale NaN and codes 0, so that
- * products with it are NaN.  (Below amax = 2^-100 both factors of the code's product
- * are taken 2^64 away, so that they stay in range.)  cols % 16 == 0.
+ * products with it are NaN.  (Below amax = 2^-100 the code is that of 2^64 x with
+ * fp32(448 / (2^64 amax)), which stays in range.)  cols % 16 == 0.
  */
 int moe_quant_fp8(int dtype, const void *x, int rows, int cols, uint8_t *q, float *scales, void *stream);
 
 /*
  * moe_grouped_fp8_mm -- out[r, n] = sum over the blocks b of K of
  * x_scales[row(r), b] * w_scales[e, n / 128, b] * sum_{k in b} x[row(r), k] * w[e, n, k].
- * A block's sum is kept in fp32; it is scaled by the two scales' powers of two and by
- * their fractions' product, so only the result's range counts, not that of the scales'
- * product.  out_dtype MOE_T_BF16, MOE_T_FP16 or MOE_T_FP32; out [R, N].  first NULL with
- * E = 1: one group of all R rows.
+ * A block's sum is scaled by the two scales' powers of two and by their fractions'
+ * product, so only the result's range counts, not that of the scales' product; an
+ * infinite or NaN scale makes what it enters infinite or NaN.  Sums are kept in fp32.
+ * With 16-bit results of more than a few rows a group the sum of eight consecutive
+ * products is first formed by the 8-bit matrix instruction, which drops what lies 2^-13
+ * below the largest of them: less than 2^-10 of that product in all, a thirtieth of a bf16
+ * step of a typical result.  fp32 results, and few rows, are summed in fp32 throughout.
+ * out_dtype MOE_T_BF16, MOE_T_FP16 or MOE_T_FP32; out [R, N].  first NULL with E = 1:
+ * one group of all R rows.
  */
 int moe_grouped_fp8_mm(const uint8_t *x, const float *x_scales, long long x_rows, const int32_t *rows, const uint8_t *w,
                        const float *w_scales, const int32_t *first, int E, int R, int N, int K, int out_dtype,

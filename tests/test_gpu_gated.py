@@ -526,6 +526,25 @@ def test_forward_rows_past_4_gib():
     check_forward(h[:2], pre[:2], ref, mag, K, {})
 
 
+@pytest.mark.parametrize("R", [6, 603])
+def test_gathered_rows_past_4_gib(R):
+    """Rows of x on both sides of 2^31 and 2^32 bytes, streamed and tiled; names of no row past them are zeros."""
+    K, T, I = 2048, 1100000, 136
+    g = _gen(5)
+    x = torch.zeros(T, K, dtype=BF16, device="cuda")
+    spots = torch.tensor([0, (1 << 31) // (2 * K) - 1, (1 << 31) // (2 * K), (1 << 32) // (2 * K) - 1, (1 << 32) // (2 * K), T - 1],
+                         device="cuda")
+    x[spots] = _normal(g, 6, K)
+    w = _normal(g, 1, 2 * I, K, scale=K ** -0.5)
+    rows = spots[torch.arange(R, device="cuda") % 6].to(torch.int32)
+    rows[2] = T
+    h, pre = M.grouped_glu(x, w, offsets([R]).cuda(), rows=rows, keep_pre=True)
+    small = x[spots][torch.arange(R, device="cuda") % 6]
+    small[2] = 0
+    ref, mag, _ = ref_mm(small, w, offsets([R]), None, R)
+    check_forward(h, pre, ref, mag, K, {})
+
+
 @pytest.mark.parametrize("form", ["plain", "shifted", "situ"])
 def test_references_agree_with_autograd(form):
     """The formula's gradient that the kernels are held to is autograd's of the definition."""
