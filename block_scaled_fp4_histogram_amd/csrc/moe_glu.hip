@@ -4,6 +4,10 @@
 
 namespace moe {
 
+// Tiles of the products' shapes, whose waves here hold as many columns of each
+// branch; 256 x 128 with all four waves over the rows, so that a wave's rows of h are whole
+// lines (64 columns in 16 bits).  16384 x 2 x 2048 x 4096, bf16: 425, 420, 452, 555 us
+// (1.29 PFLOP/s); bound by the matrix cores and the clock they leave.
 template <int TYPE>
 static hipError_t launch_glu_tiles(const MmArgs &a, int shape, hipStream_t s) {
   switch (shape) {
@@ -14,6 +18,9 @@ static hipError_t launch_glu_tiles(const MmArgs &a, int shape, hipStream_t s) {
   }
 }
 
+// Row gradients with the activation's gradient behind them.  32 groups of 512 rows, 6144 x
+// 1024, h once more: 228, 235, 296, 324 us, the row gradient alone 207, 203, 263, 302; the
+// epilogue's 10 bytes an output are read and written when the products of its round end.
 template <int TYPE>
 static hipError_t launch_glu_dx(const MmArgs &a, int shape, hipStream_t s) {
   switch (shape) {
@@ -34,7 +41,8 @@ hipError_t launch_glu(const MmArgs &a, const MmPlan &m, hipStream_t s) {
   return a.type == MM_BF16 ? launch_glu_type<MM_BF16>(a, m, s) : launch_glu_type<MM_FP16>(a, m, s);
 }
 
-// The gradient where dh is in memory: a pass over it, eight columns a thread.
+// The gradient where dh is in memory: a pass over it, eight columns a thread (16382 x 2048
+// with h once more, 0.4 GB: 70 us, 5.8 TB/s; bound by HBM).
 template <int TYPE>
 __global__ __launch_bounds__(256) void k_glu_grad(const uint16_t *dh, const void *pre, long chunks, int I, GluForm f,
                                                   void *d_pre, void *h) {

@@ -43,8 +43,8 @@ struct MmElem<MM_I8> {
 // register pair of either operand) meet with what lies 13 bits and more below the
 // largest of them cut off, and the eights' sums meet in fp32 (measured on all their
 // positions).  That is 2^-10 of a block's magnitudes at worst and about 5e-5 of a
-// random sum, a thirtieth of a bf16 step and a quarter of an fp16 one; the rate is twice
-// that of any instruction that keeps fp32.  The instruction applies the powers of two
+// random sum, a thirtieth of what rounding it to bf16 costs and a quarter of what
+// rounding it to fp16 does; the rate is twice that of any instruction that keeps fp32.  The instruction applies the powers of two
 // of the block's scales itself.
 // MM_F8X: the codes as fp16 values, which is exact, in fp16 instructions, which sum in
 // fp32: for fp32 results, and where the weights' bytes bound the product anyway.
@@ -497,7 +497,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       lds_void *dst = (lds_void *)(lq + i * NW * 1024);
       if constexpr (NEAR) {
         if (near) {
-          const Rsrc sx = TQ_T ? sq : rx;
+          const Rsrc sx = TQ_T ? sq : rx;   // (a copy, as of the others: the host's pass takes no captured one)
           __builtin_amdgcn_raw_ptr_buffer_load_lds(sx, dst, 16, (int)(NEAR && (int)cq < left ? (uint32_t)grow[GF ? i : 0] : kOutside),
                                                    TQ_T ? 0 : s * 128, 0, 0);
           continue;
