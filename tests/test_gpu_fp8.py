@@ -366,6 +366,38 @@ def test_gathered_rows_past_4_gib():
         _check(out, (small.view(torch.uint8).repeat(R // 6, 1).view(E4M3), xs[spots].repeat(R // 6, 1), w, ws, offsets([R]), None))
 
 
+@pytest.mark.parametrize("T,N,K", [(3, 1 << 20, 16), (70, 1 << 20, 16), (1, 8, 1 << 20), (37, 16, 1 << 20)])
+@pytest.mark.parametrize("out_dtype", [BF16, FP32])
+def test_largest_sizes(T, N, K, out_dtype):
+    case = _case([T], N, K, False, seed=T)
+    x, xs, w, ws = case[:4]
+    _check(M.fp8_mm(x, xs, w[0], ws[0], out_dtype=out_dtype), case)
+    q, s = M.quant_fp8(torch.randn(2, K, device="cuda", generator=_gen(1)).to(BF16))
+    assert q.shape == (2, K) and bool((s > 0).all())
+
+
+def test_most_groups_most_of_them_empty():
+    counts = [0] * 1024
+    counts[0], counts[511], counts[1000], counts[1023] = 3, 40, 150, 1
+    for glu in (False, True):
+        case = _case(counts, 72, 144, True, glu=glu)
+        if glu:
+            _check_glu(M.grouped_fp8_glu(*case[:5], rows=case[5]), case, {})
+        else:
+            _check(M.grouped_fp8_mm(*case[:5], rows=case[5]), case)
+
+
+def test_offsets_that_go_wrong_stay_in_bounds():
+    """Offsets beyond R, below 0 or falling cost rows, never a fault; a correct group next to them is right."""
+    x, xs, w, ws, _, _ = _case([40, 0, 0], 72, 144, False)
+    for f in ([0, 20, 90, 1 << 30], [-5, 20, 10, 40], [0, 20, -(1 << 31), (1 << 31) - 1]):
+        first = torch.tensor(f, dtype=torch.int32, device="cuda")
+        out = M.grouped_fp8_mm(x, xs, w, ws, first)
+        torch.cuda.synchronize()
+        if f[2] >= 0:
+            _check(out[:10].contiguous(), (x[:10], xs[:10], w[:1], ws[:1], offsets([10]), None))
+
+
 # ---- the operators together
 
 

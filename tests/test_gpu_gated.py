@@ -545,6 +545,66 @@ def test_gathered_rows_past_4_gib(R):
     check_forward(h, pre, ref, mag, K, {})
 
 
+@pytest.mark.parametrize("T,I,K", [(3, 1 << 19, 8), (70, 1 << 19, 8), (1, 8, 1 << 20), (37, 16, 1 << 20)])
+def test_largest_sizes(T, I, K):
+    """The longest rows and the most columns that a call takes, forward and backward."""
+    g = _gen(T)
+    x, w = _normal(g, T, K), _normal(g, 2 * I, K, scale=K ** -0.5)
+    h, pre = M.glu(x, w, keep_pre=True, limit=2.0)
+    ref, mag, _ = ref_mm(x, w[None], offsets([T]), None, T)
+    check_forward(h, pre, ref, mag, K, dict(limit=2.0))
+    dy, wd = _normal(g, T, K), _normal(g, K, I, scale=K ** -0.5)
+    d_pre = M.glu_dx(dy, wd, pre, limit=2.0)
+    dh, mag, _ = ref_dx(dy, wd[None], offsets([T]))
+    check_backward(d_pre, None, dh, (K + 1) * 2.0 ** -24 * mag, pre, dict(limit=2.0))
+
+
+def test_most_groups_most_of_them_empty():
+    counts = [0] * 1024
+    counts[0], counts[511], counts[1000], counts[1023] = 3, 40, 150, 1
+    x, w, first, rows = _forward_case(counts, 72, 136, FP16, True)
+    R = sum(counts)
+    h, pre = M.grouped_glu(x, w, first, rows=rows, keep_pre=True)
+    ref, mag, _ = ref_mm(x, w, first, rows, R)
+    check_forward(h, pre, ref, mag, 136, {})
+    dy, wd, pre, first = _backward_case(counts, 136, 72, FP16)
+    d_pre, h = M.grouped_glu_dx(dy, wd, pre, first, keep_h=True)
+    dh, mag, _ = ref_dx(dy, wd, first)
+    check_backward(d_pre, h, dh, 137 * 2.0 ** -24 * mag, pre, {})
+
+
+def test_two_captured_steps_replayed_at_once():
+    """Two graphs, each with split products and last rounds in parts, on two streams: their scratch is their own."""
+    cases = [_forward_case([300], 72, 8192, BF16, False, seed=s) for s in (1, 2)]
+    backs = [_backward_case([430] + [0] * 3, 4104, 1032, BF16, seed=s) for s in (3, 4)]
+    assert plan_of(M.MM_GLU, [300], 72, 8192)[2] > 1
+
+    def step(i):
+        x, w, first, _ = cases[i]
+        dy, wd, pre, bfirst = backs[i]
+        return M.grouped_glu(x, w, first), M.grouped_glu_dx(dy, wd, pre, bfirst)
+
+    graphs, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in (0, 1):
+        step(i)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            outs.append(step(i))
+    want = [[t.clone() for t in step(i)] for i in (0, 1)]
+    for _ in range(4):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for o, v in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, v))
+
+
 @pytest.mark.parametrize("form", ["plain", "shifted", "situ"])
 def test_references_agree_with_autograd(form):
     """The formula's gradient that the kernels are held to is autograd's of the definition."""
