@@ -605,6 +605,34 @@ def test_two_captured_steps_replayed_at_once():
             assert all(torch.equal(a, b) for a, b in zip(o, v))
 
 
+@pytest.mark.parametrize("R", [5, 300, 2000])
+def test_c_abi_gathers_rows_of_one_group(R):
+    """Without offsets but with row numbers: one group whose rows of x are named, 16 bits and 8."""
+    from block_scaled_fp4_histogram_amd import _lib
+    from gated_util import act_bound, assert_close, codes, fp8_bound, ref_fp8
+    L, g = _lib.load(), _gen(R)
+    T, I, K = 50, 136, 272
+    x, w = _normal(g, T, K), _normal(g, 1, 2 * I, K, scale=K ** -0.5)
+    rows = torch.randint(-2, T + 2, (R,), device="cuda", generator=g, dtype=torch.int32)
+    h, pre = torch.empty(R, I, dtype=BF16, device="cuda"), torch.empty(R, 2 * I, dtype=BF16, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    scratch = torch.empty(max(1, M.mm_scratch_bytes(M.MM_GLU, 1, R, I, K)), dtype=torch.uint8, device="cuda")
+    assert L.moe_grouped_glu(M.T_BF16, x.data_ptr(), T, rows.data_ptr(), w.data_ptr(), None, 1, R, I, K, None, M.T_BF16,
+                             h.data_ptr(), pre.data_ptr(), scratch.data_ptr(), scratch.numel(), stream) == M.MOE_OK
+    ref, mag, _ = ref_mm(x, w, offsets([R]), rows, R)
+    check_forward(h, pre, ref, mag, K, {})
+    xq, wq = codes(g, T, K), codes(g, 1, 2 * I, K)
+    xs, ws = torch.rand(T, 3, device="cuda", generator=g) / 100, torch.rand(1, 2, 2, 3, device="cuda", generator=g) / 2000
+    scratch = torch.empty(max(1, M.mm_scratch_bytes(M.MM_FP8_GLU, 1, R, I, K)), dtype=torch.uint8, device="cuda")
+    out = torch.empty(R, I, dtype=FP32, device="cuda")
+    assert L.moe_grouped_fp8_glu(xq.data_ptr(), xs.data_ptr(), T, rows.data_ptr(), wq.data_ptr(), ws.data_ptr(), None, 1, R, I, K,
+                                 None, M.T_FP32, out.data_ptr(), scratch.data_ptr(), scratch.numel(), stream) == M.MOE_OK
+    ref, mag, top, _ = ref_fp8(xq, xs, wq, ws, offsets([R]), rows, R)
+    gate, up = branches(ref, {})
+    dg, du = branches(fp8_bound(K, mag, top, False), {})
+    assert_close(out, ref_act(gate, up, {}), act_bound(gate, up, dg, du, {}))
+
+
 @pytest.mark.parametrize("form", ["plain", "shifted", "situ"])
 def test_references_agree_with_autograd(form):
     """The formula's gradient that the kernels are held to is autograd's of the definition."""
