@@ -7,24 +7,25 @@
 
 namespace moe {
 
+// Clamps that let NaN through.
+__device__ __forceinline__ float clamp_above(float v, float l) { return v > l ? l : v; }
+__device__ __forceinline__ float clamp_both(float v, float l) { return v > l ? l : v < -l ? -l : v; }
+
 // sigmoid(x) and 1 - sigmoid(x) from e = exp(-|x|), which never overflows: 1 / (1 + e)
 // and e / (1 + e), whichever sign x has.  exp2 takes the product's rounding error
-// as a correction, so e keeps its precision at large |x| as well; at 150 it is 0.
+// as a correction, so e keeps its precision at large |x| as well; at 150 it is 0.  NaN
+// stays NaN in both.
 struct Sigmoid {
   float s, r;
 };
 __device__ __forceinline__ Sigmoid sigmoid2(float x) {
   constexpr float kLog2e = 1.44269502f, kLow = 1.92596303e-8f, kLn2 = 0.693147182f;
-  const float n = -fminf(fabsf(x), 150.0f), hi = n * kLog2e, lo = fmaf(n, kLow, fmaf(n, kLog2e, -hi));
+  const float n = -clamp_above(fabsf(x), 150.0f), hi = n * kLog2e, lo = fmaf(n, kLow, fmaf(n, kLog2e, -hi));
   float e = __builtin_amdgcn_exp2f(hi);
   e = fmaf(e, lo * kLn2, e);
   const float q = __builtin_amdgcn_rcpf(1.0f + e), p = e * q;
   return x >= 0.0f ? Sigmoid{q, p} : Sigmoid{p, q};
 }
-
-// The limit's clamps let NaN through.
-__device__ __forceinline__ float clamp_above(float v, float l) { return v > l ? l : v; }
-__device__ __forceinline__ float clamp_both(float v, float l) { return v > l ? l : v < -l ? -l : v; }
 
 // act(gate, up): gate sigmoid(alpha gate) (up + beta) after the limit, or SiTU,
 // silu(4 tanh(gate / 4)) 25 tanh(up / 25).
@@ -47,9 +48,10 @@ __device__ __forceinline__ void glu_grad(float dh, float gate, float up, const G
   float g_in = 1.0f, u_in = 1.0f, alpha = f.alpha, beta = f.beta;
   bool g_out = false, u_out = false;
   if (f.act == ACT_SITU) {               // the same with alpha 1 on the capped branches, by the chain rule
-    const float tg = tanhf(0.25f * gate), tu = tanhf(0.04f * up);
-    gate = 4.0f * tg, up = 25.0f * tu;
-    g_in = (1.0f - tg) * (1.0f + tg), u_in = (1.0f - tu) * (1.0f + tu);
+    // (1 - tanh^2(y) = 4 s (1 - s) at s = sigmoid(2 y), which keeps its precision where the tanh rounds to 1)
+    const Sigmoid sg = sigmoid2(0.5f * gate), su = sigmoid2(0.08f * up);
+    gate = 4.0f * tanhf(0.25f * gate), up = 25.0f * tanhf(0.04f * up);
+    g_in = 4.0f * sg.s * sg.r, u_in = 4.0f * su.s * su.r;
   } else if (f.has_limit) {
     g_out = gate > f.limit, u_out = fabsf(up) > f.limit;
     gate = clamp_above(gate, f.limit);
