@@ -61,7 +61,8 @@ __device__ __forceinline__ void glu_grad(float dh, float gate, float up, const G
   const float a = gate * s.s, u = up + beta;
   h = a * u;
   d_up = u_out ? 0.0f : dh * a * u_in;
-  d_gate = g_out ? 0.0f : dh * u * (s.s * fmaf(alpha * gate, s.r, 1.0f)) * g_in;
+  // (gate s (1 - s) before alpha: where alpha gate passes the range, it is 0)
+  d_gate = g_out ? 0.0f : dh * u * fmaf(alpha, gate * (s.s * s.r), s.s) * g_in;
 }
 
 template <int TYPE>

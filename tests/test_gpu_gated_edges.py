@@ -57,3 +57,20 @@ def test_situ_gradient_of_nan_and_infinite_projections():
     at_cap = 1 / float(torch.tanh(torch.tensor(0.04, dtype=torch.float64)))     # 25 for up's 25 tanh(1 / 25)
     want = float(rg) * at_cap
     assert abs(float(dg[4]) - want) <= 2.0 ** -7 * want and abs(float(dg[5]) + want) <= 2.0 ** -7 * want
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.702, -1.702, 1e30, -1e30, 1e-30, 0.0])
+def test_gradient_where_alpha_gate_passes_the_range(alpha):
+    """Gates to the ends of bf16 times alpha beyond fp32's range: the sigmoid is 0 or 1 there, and so is what the
+    gradient has of it. dh and up + beta are 1, so d gate is sigmoid(z) (1 + z sigmoid(-z)), z = alpha gate, and
+    d up the gated value; the sigmoid's error is within 16 u and 2 |z| u of it wherever it is not 0 (|z| < 90)."""
+    v = torch.tensor([3.3e38, 2e38, 1e38, 1e30, 1e9, 60.0, 1.0, 0.0], dtype=torch.float64).to(BF16).double()
+    gate = torch.cat([v, -v])[None].cuda()
+    up = torch.zeros_like(gate)
+    got = M.glu_grad(torch.ones_like(gate).to(BF16), joined(gate, up, {}).to(BF16), alpha=alpha, beta=1.0).double()
+    z = float(torch.tensor(alpha, dtype=torch.float32)) * gate
+    s, r = torch.sigmoid(z), torch.sigmoid(-z)
+    rg, ru = s * (1 + z * r), gate * s
+    units = (24 + 4 * z.abs().clamp(max=90)) * U
+    assert_close(got[:, 16:].to(BF16), rg, units * s * (1 + (z * r).abs()) + 2.0 ** -120, "d gate")
+    assert_close(got[:, :16].to(BF16), ru, units * ru.abs() + 2.0 ** -120 * (1 + gate.abs()), "d up")
