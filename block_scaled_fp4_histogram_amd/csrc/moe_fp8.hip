@@ -6,13 +6,17 @@
 
 namespace moe {
 
-// One group of 16384 x 4096 x 4096: 278, 266, 287, 344 us (2.07 PFLOP/s; with two waves a
+// One group of 16384 x 4096 x 4096: 313, 295, 312, 356 us (1.87 PFLOP/s; with two waves a
 // SIMD the loads' and the scales' waits stand between the products).  fp32 results are
-// summed in fp32 throughout, in tiles whose operands fit the registers twice.
+// summed in fp32 throughout, in the same tiles: 516, 495, 572, 611 us.
 template <int OP>
 static hipError_t launch_fp8_tiles(const MmArgs &a, int shape, hipStream_t s) {
-  if (a.out_type == MM_FP32)
-    return shape == 3 ? launch_tile<OP, MM_F8X, 64, 128, 2, 2, 3>(a, s) : launch_tile<OP, MM_F8X, 128, 128, 2, 2, 2>(a, s);
+  if (a.out_type == MM_FP32) switch (shape) {
+    case 0: return launch_tile<OP, MM_F8X, 256, 128, 4, 1, 2>(a, s);
+    case 1: return launch_tile<OP, MM_F8X, 128, 256, 2, 2, 2>(a, s);
+    case 2: return launch_tile<OP, MM_F8X, 128, 128, 2, 2, 2>(a, s);
+    default: return launch_tile<OP, MM_F8X, 64, 128, 2, 2, 3>(a, s);
+  }
   switch (shape) {
     case 0: return launch_tile<OP, MM_F8, 256, 128, 4, 1, 2>(a, s);
     case 1: return launch_tile<OP, MM_F8, 128, 256, 2, 2, 2>(a, s);

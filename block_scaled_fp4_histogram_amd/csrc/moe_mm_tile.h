@@ -77,6 +77,14 @@ __device__ __forceinline__ MmScale8 mm_scale8(float s) {
   return MmScale8{__builtin_ldexpf(s, 127 - code), code};
 }
 constexpr int kF8Block = 128;            // values of a scale, along either side
+// The same as two factors, first * second, that a block's sum (2^-18 to 2^25) meets in turn:
+// the first within 2^100 of 1 (but for subnormal scales' fractions), so that the sum times it
+// loses nothing that the result has, and the second 1 unless the scales' product is further off.
+__device__ __forceinline__ void mm_factors8(MmScale8 w, MmScale8 x, float &first, float &second) {
+  const int e = w.code + x.code - 254, near = min(max(e, -100), 100);
+  first = __builtin_ldexpf(w.m * x.m, near);
+  second = __builtin_ldexpf(1.0f, min(max(e - near, -126), 127));
+}
 
 // acc + a block's sum times its scales: w's as the matrix operand's row has it (row),
 // as the sum has it (sum), and x's.
@@ -676,9 +684,11 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
           for (int i = 0; i < NP; i++) acc[i][j] = M::mma(fp[h][i], fq[h][j], acc[i][j]);
       }
     };
-    // 8-bit floating point: the operands of half the columns (gated: of a branch) at a time
+    // 8-bit floating point: the operands of a part of the columns at a time, half of them or, where
+    // the operands as fp16 fill the registers, a quarter (gated: of one branch)
     MmScale8 zx[F8 ? NQ : 1], zw[NW8];
-    constexpr int HF = NP / 2;
+    constexpr int PARTS8 = TYPE == MM_F8X && NP > 4 ? 4 : 2, HF = NP / PARTS8;
+    v8h hq[TYPE == MM_F8X ? NQ : 1][4];
     auto read8 = [&](int b) {
 #pragma unroll
       for (int i = 0; i < HF; i++)
@@ -686,6 +696,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
         for (int h = 0; h < 2; h++) fp[h][b * HF + i] = frag_p(lp, b * HF + i, h);
     };
     auto mul8 = [&](int b) {
+      const MmScale8 zb = zw[GLU ? b / (PARTS8 / 2) : 0];
       if constexpr (TYPE == MM_F8) {
         // a block's sums meet the accumulators two instructions later, in the shadow of the
         // ones between; the order is pinned, or more sums are in flight than registers hold
@@ -693,14 +704,14 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
         v4f d[L + 1];
         float m[NQ];
 #pragma unroll
-        for (int j = 0; j < NQ; j++) m[j] = zw[GLU ? b : 0].m * zx[j].m;
+        for (int j = 0; j < NQ; j++) m[j] = zb.m * zx[j].m;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int c = 0; c < CNT + L; c++) {
           if (c < CNT) {
             const int i = b * HF + c / NQ, j = c % NQ;
             d[c % (L + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                join8(fp[0][i], fp[1][i]), join8(fq[0][j], fq[1][j]), v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, zw[GLU ? b : 0].code, 0, zx[j].code);
+                join8(fp[0][i], fp[1][i]), join8(fq[0][j], fq[1][j]), v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, zb.code, 0, zx[j].code);
           }
           if (c >= L) {
             const int o = c - L, i = b * HF + o / NQ, j = o % NQ;
@@ -710,11 +721,25 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
           __builtin_amdgcn_sched_barrier(0);
         }
       } else if constexpr (F8) {
+        // the block's sums of a fragment of w and all of x's, then their scales in two factors
+        // (mm_factors8), one product and one fused addition a sum
+        float f1[NQ], f2[NQ];
 #pragma unroll
-        for (int i = b * HF; i < b * HF + HF; i++)
+        for (int j = 0; j < NQ; j++) mm_factors8(zb, zx[j], f1[j], f2[j]);
+#pragma unroll
+        for (int i = b * HF; i < b * HF + HF; i++) {
+          v4f d[NQ];
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            const v8h hp = codes_f16(fp[c >> 1][i][2 * (c & 1)], fp[c >> 1][i][2 * (c & 1) + 1]);
+#pragma unroll
+            for (int j = 0; j < NQ; j++) d[j] = mfma_f16(hp, hq[j][c], c ? d[j] : v4f{0.f, 0.f, 0.f, 0.f});
+          }
 #pragma unroll
           for (int j = 0; j < NQ; j++)
-            acc[i][j] = f8_block<TYPE>(acc[i][j], join8(fp[0][i], fp[1][i]), join8(fq[0][j], fq[1][j]), zw[GLU ? b : 0].code, zw[GLU ? b : 0], zx[j]);
+#pragma unroll
+            for (int k = 0; k < 4; k++) acc[i][j][k] = fmaf(d[j][k] * f1[j], f2[j], acc[i][j][k]);
+        }
       }
     };
     if constexpr (F8) {
@@ -728,15 +753,24 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       for (int i = 0; i < NW8; i++) zw[i] = mm_scale8(sw[i]);
       read8(0);
       read_x(s + 1);
-      mul8(0);
-      // (kept in front of the second half's reads and the branch below: sunk past them, both
-      // halves' operands would be live and the accumulators spill)
+      if constexpr (TYPE == MM_F8X) {
 #pragma unroll
-      for (int i = 0; i < HF; i++)
+        for (int j = 0; j < NQ; j++)
 #pragma unroll
-        for (int j = 0; j < NQ; j++) asm volatile("" : "+v"(acc[i][j]));
-      __builtin_amdgcn_sched_barrier(0);
-      read8(1);
+          for (int c = 0; c < 4; c++) hq[j][c] = codes_f16(fq[c >> 1][j][2 * (c & 1)], fq[c >> 1][j][2 * (c & 1) + 1]);
+      }
+#pragma unroll
+      for (int b = 0; b + 1 < PARTS8; b++) {
+        mul8(b);
+        // (kept in front of the next part's reads and the branch below: sunk past them, more
+        // parts' operands would be live and the accumulators spill)
+#pragma unroll
+        for (int i = b * HF; i < b * HF + HF; i++)
+#pragma unroll
+          for (int j = 0; j < NQ; j++) asm volatile("" : "+v"(acc[i][j]));
+        __builtin_amdgcn_sched_barrier(0);
+        read8(b + 1);
+      }
     } else {
       read(0);
       if (GATHER && !NEAR) {
@@ -754,7 +788,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       gather_rows(s + 2);
     }
     if constexpr (F8) {
-      mul8(1);
+      mul8(PARTS8 - 1);
     } else {
       if (!GATHER || NEAR) mul(0);
       mul(1);
