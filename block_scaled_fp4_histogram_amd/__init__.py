@@ -50,6 +50,7 @@ NSLOTS = len(RACE_SLOTS)
 
 T_BF16, T_FP16, T_FP32 = 1, 2, 3
 MM_FORWARD, MM_DX, MM_DW, MM_INT8, MM_GLU, MM_GLU_DX, MM_FP8, MM_FP8_GLU = 1, 2, 3, 4, 5, 6, 7, 8
+FP8_FAST_SUMS = 16
 
 
 class MoeError(RuntimeError):
@@ -382,7 +383,8 @@ def _use(stream, t):
 
 def mm_scratch_bytes(op: int, E: int, R: int, N: int, K: int) -> int:
     """Scratch bytes of a product (moe_mm_scratch_bytes): op MM_FORWARD, MM_DX, MM_DW, MM_INT8, MM_GLU (N: the
-    block's I), MM_GLU_DX (K: the block's I), MM_FP8 or MM_FP8_GLU (N: the block's I)."""
+    block's I), MM_GLU_DX (K: the block's I), MM_FP8 or MM_FP8_GLU (N: the block's I),
+    these two | FP8_FAST_SUMS with fast_sums."""
     return _lib.load().moe_mm_scratch_bytes(op, E, R, N, K)
 
 
@@ -533,50 +535,56 @@ def quant_fp8(x, out=None, scales=None, stream=None):
     return (_binding or _bind()).quant_fp8(x, out, scales)
 
 
-def fp8_mm(x, x_scales, w, w_scales, out=None, out_dtype=None, scratch=None, stream=None):
+def fp8_mm(x, x_scales, w, w_scales, out=None, out_dtype=None, scratch=None, stream=None, fast_sums: bool = False):
     """8-bit floating-point product with a scale for each block of 128 (moe_grouped_fp8_mm): x and w times
-    their scales, x @ w.T, the sums in 32 bits (with out_dtype torch.float32 throughout; 16-bit results of more
-    than a few rows drop what lies 2^-13 below the largest of each eight products).
+    their scales, x @ w.T, summed in 32 bits.
 
     x float8_e4m3fn [M, K], x_scales fp32 [M, ceil(K / 128)], w float8_e4m3fn [N, K], w_scales fp32
-    [ceil(N / 128), ceil(K / 128)]; out [M, N] bf16 (default), fp16 or fp32."""
+    [ceil(N / 128), ceil(K / 128)]; out [M, N] bf16 (default), fp16 or fp32. fast_sums, for 16-bit results: the
+    8-bit matrix instruction sums each eight products, at twice the rate, and drops what lies 2^-13 below the
+    largest of them (about 5e-5 of a random sum; all of one whose large products cancel)."""
     if stream is not None:
         with _use(stream, x):
-            return fp8_mm(x, x_scales, w, w_scales, out, out_dtype, scratch)
-    return (_binding or _bind()).fp8_mm(x, x_scales, w, w_scales, out, out_dtype, scratch)
+            return fp8_mm(x, x_scales, w, w_scales, out, out_dtype, scratch, None, fast_sums)
+    return (_binding or _bind()).fp8_mm(x, x_scales, w, w_scales, out, out_dtype, scratch, fast_sums)
 
 
-def grouped_fp8_mm(x, x_scales, w, w_scales, first, rows=None, out=None, out_dtype=None, scratch=None, stream=None):
+def grouped_fp8_mm(x, x_scales, w, w_scales, first, rows=None, out=None, out_dtype=None, scratch=None, stream=None,
+                   fast_sums: bool = False):
     """fp8_mm over ragged groups (moe_grouped_fp8_mm): w [E, N, K], w_scales [E, ceil(N / 128), ceil(K / 128)],
-    first and rows as in grouped_mm; x_scales belongs to the rows of x."""
+    first and rows as in grouped_mm; x_scales belongs to the rows of x. fast_sums as in fp8_mm."""
     if stream is not None:
         with _use(stream, x):
-            return grouped_fp8_mm(x, x_scales, w, w_scales, first, rows, out, out_dtype, scratch)
-    return (_binding or _bind()).grouped_fp8_mm(x, x_scales, w, w_scales, first, rows, out, out_dtype, scratch)
+            return grouped_fp8_mm(x, x_scales, w, w_scales, first, rows, out, out_dtype, scratch, None, fast_sums)
+    return (_binding or _bind()).grouped_fp8_mm(x, x_scales, w, w_scales, first, rows, out, out_dtype, scratch,
+                                                fast_sums)
 
 
 def fp8_glu(x, x_scales, w, w_scales, activation: int = ACT_SWIGLU, limit: Optional[float] = None, alpha: float = 1.0,
-            beta: float = 0.0, layout: int = W13_UP_GATE, out=None, out_dtype=None, scratch=None, stream=None):
+            beta: float = 0.0, layout: int = W13_UP_GATE, out=None, out_dtype=None, scratch=None, stream=None,
+            fast_sums: bool = False):
     """glu on 8-bit floating-point operands (moe_grouped_fp8_glu): x and x_scales as in fp8_mm, w float8_e4m3fn
-    [2 I, K], w_scales fp32 [2, ceil(I / 128), ceil(K / 128)] by branch; h [M, I] bf16 (default), fp16 or fp32."""
+    [2 I, K], w_scales fp32 [2, ceil(I / 128), ceil(K / 128)] by branch; h [M, I] bf16 (default), fp16 or fp32.
+    fast_sums as in fp8_mm."""
     if stream is not None:
         with _use(stream, x):
-            return fp8_glu(x, x_scales, w, w_scales, activation, limit, alpha, beta, layout, out, out_dtype, scratch)
+            return fp8_glu(x, x_scales, w, w_scales, activation, limit, alpha, beta, layout, out, out_dtype, scratch, None,
+                           fast_sums)
     return (_binding or _bind()).fp8_glu(x, x_scales, w, w_scales, activation, limit, alpha, beta, layout, out, out_dtype,
-                                         scratch)
+                                         scratch, fast_sums)
 
 
 def grouped_fp8_glu(x, x_scales, w, w_scales, first, rows=None, activation: int = ACT_SWIGLU,
                     limit: Optional[float] = None, alpha: float = 1.0, beta: float = 0.0, layout: int = W13_UP_GATE,
-                    out=None, out_dtype=None, scratch=None, stream=None):
+                    out=None, out_dtype=None, scratch=None, stream=None, fast_sums: bool = False):
     """fp8_glu over ragged groups (moe_grouped_fp8_glu): w [E, 2 I, K], w_scales [E, 2, ceil(I / 128),
-    ceil(K / 128)], first and rows as in grouped_mm."""
+    ceil(K / 128)], first and rows as in grouped_mm. fast_sums as in fp8_mm."""
     if stream is not None:
         with _use(stream, x):
             return grouped_fp8_glu(x, x_scales, w, w_scales, first, rows, activation, limit, alpha, beta, layout, out,
-                                   out_dtype, scratch)
+                                   out_dtype, scratch, None, fast_sums)
     return (_binding or _bind()).grouped_fp8_glu(x, x_scales, w, w_scales, first, rows, activation, limit, alpha, beta,
-                                                 layout, out, out_dtype, scratch)
+                                                 layout, out, out_dtype, scratch, fast_sums)
 
 
 def group_routes(topk_ids, num_experts: int, scratch=None, stream=None):

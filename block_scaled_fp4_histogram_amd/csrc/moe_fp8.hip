@@ -6,17 +6,21 @@
 
 namespace moe {
 
-// One group of 16384 x 4096 x 4096: 313, 295, 312, 356 us (1.87 PFLOP/s; with two waves a
-// SIMD the loads' and the scales' waits stand between the products).  fp32 results are
-// summed in fp32 throughout, in the same tiles: 516, 495, 572, 611 us.
+// One group of 16384 x 4096 x 4096, summed in fp32: 516, 495, 572, 611 us (1.11 PFLOP/s).
 template <int OP>
 static hipError_t launch_fp8_tiles(const MmArgs &a, int shape, hipStream_t s) {
-  if (a.out_type == MM_FP32) switch (shape) {
+  switch (shape) {
     case 0: return launch_tile<OP, MM_F8X, 256, 128, 4, 1, 2>(a, s);
     case 1: return launch_tile<OP, MM_F8X, 128, 256, 2, 2, 2>(a, s);
     case 2: return launch_tile<OP, MM_F8X, 128, 128, 2, 2, 2>(a, s);
     default: return launch_tile<OP, MM_F8X, 64, 128, 2, 2, 3>(a, s);
   }
+}
+
+// By the 8-bit instruction: 313, 295, 312, 356 us (1.87 PFLOP/s; with two waves a SIMD the
+// loads' and the scales' waits stand between the products).
+template <int OP>
+static hipError_t launch_fp8_fast(const MmArgs &a, int shape, hipStream_t s) {
   switch (shape) {
     case 0: return launch_tile<OP, MM_F8, 256, 128, 4, 1, 2>(a, s);
     case 1: return launch_tile<OP, MM_F8, 128, 256, 2, 2, 2>(a, s);
@@ -25,9 +29,14 @@ static hipError_t launch_fp8_tiles(const MmArgs &a, int shape, hipStream_t s) {
   }
 }
 
+template <int OP>
+static hipError_t launch_fp8_op(const MmArgs &a, const MmPlan &m, hipStream_t s) {
+  if (m.stream) return launch_stream<OP, MM_F8X>(a, s);
+  return a.type == MM_F8 ? launch_fp8_fast<OP>(a, m.shape, s) : launch_fp8_tiles<OP>(a, m.shape, s);
+}
+
 hipError_t launch_fp8(const MmArgs &a, const MmPlan &m, hipStream_t s) {
-  if (a.op == MM_GLU) return m.stream ? launch_stream<MM_GLU, MM_F8X>(a, s) : launch_fp8_tiles<MM_GLU>(a, m.shape, s);
-  return m.stream ? launch_stream<MM_FORWARD, MM_F8X>(a, s) : launch_fp8_tiles<MM_FORWARD>(a, m.shape, s);
+  return a.op == MM_GLU ? launch_fp8_op<MM_GLU>(a, m, s) : launch_fp8_op<MM_FORWARD>(a, m, s);
 }
 
 // ------------------------------------------------------------ quantiser

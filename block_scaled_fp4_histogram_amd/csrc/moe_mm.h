@@ -10,7 +10,8 @@
 namespace moe {
 
 enum MmType { MM_BF16 = 1, MM_FP16 = 2, MM_FP32 = 3, MM_I8 = 4, MM_F8 = 5, MM_F8X = 6 };
-// (MM_F8X: the same operands as MM_F8, summed without its matrix instruction's cut.)
+// (MM_F8X: the same operands as MM_F8, summed in fp32 in place of by the 8-bit matrix
+// instruction, which the caller asks for.)
 // MM_GLU: a forward product with the gate's and the up branch's rows of w, N of each,
 // then the activation; MM_GLU_DX: MM_DX, then the activation's gradient.
 enum MmOp { MM_FORWARD = 1, MM_DX = 2, MM_DW = 3, MM_GLU = 4, MM_GLU_DX = 5 };
@@ -58,7 +59,7 @@ struct MmPlan {
 MmPlan mm_plan(int op, int type, long E, long R, long N, long K);
 
 hipError_t launch_mm(const MmArgs &a, hipStream_t s);
-// The same for MM_GLU and MM_GLU_DX of 16-bit operands, and for MM_F8, under plan m.
+// The same for MM_GLU and MM_GLU_DX of 16-bit operands, and for MM_F8 and MM_F8X, under plan m.
 hipError_t launch_glu(const MmArgs &a, const MmPlan &m, hipStream_t s);
 hipError_t launch_fp8(const MmArgs &a, const MmPlan &m, hipStream_t s);
 

@@ -29,7 +29,8 @@ static const float kGluStart[kShapes] = {9.f, 8.f, 7.f, 6.f}, kGradStart[kShapes
 enum { kPlain = 0, kBuilt = 1, kBuiltGrad = 2 };
 static MmPlan shape_plan(int op, int type, long E, long R, long N, long K, int built) {
   MmPlan m = {0, 0, 1, 16, 16, 0, 0};
-  const long item = type == MM_I8 || type == MM_F8 ? 1 : 2, groups = E < R ? E : R;
+  const bool f8 = type == MM_F8 || type == MM_F8X;
+  const long item = type == MM_I8 || f8 ? 1 : 2, groups = E < R ? E : R;
   const long pn = op == MM_FORWARD ? N : K, qn = op == MM_DW ? N : R, outs = op == MM_DW ? E * N : R;
   // Few rows a group: the weights pass once, 16 of their rows a block.  Short rows
   // make for blocks that mostly start and end (64 groups of 5 rows, N = 1024:
@@ -60,7 +61,7 @@ static MmPlan shape_plan(int op, int type, long E, long R, long N, long K, int b
     if (op == MM_DW) rows *= E;
     else if (E > 1) rows = (R + groups * (s.bq / 2)) / s.bq > groups ? (R + groups * (s.bq / 2)) / s.bq : groups;
     const long n = rows * ((pn + s.bp - 1) / s.bp), slots = 256l * s.occ;
-    const float weight = type == MM_F8 ? kF8Weights[i] : s.weight;
+    const float weight = f8 ? kF8Weights[i] : s.weight;
     float cost = (float)((n + slots - 1) / slots * s.occ) * (float)(s.bq * s.bp) * weight;
     if (built) cost *= (float)steps + start(i);
     if (!tiles || cost < least) m.shape = i, least = cost, tiles = n;
@@ -105,7 +106,7 @@ static MmPlan shape_plan(int op, int type, long E, long R, long N, long K, int b
     const MmTail t = mm_tail((int)n, (int)slots, (int)steps);
     if (t.parts < 2 || (t.full == 0 && steps < 64)) continue;
     const float cost = ((float)(t.full / slots) * ((float)steps + start(i)) + (1.0f / t.parts + 0.05f) * (float)steps + 8.0f) *
-                       s.occ * (float)(s.bq * s.bp) * (type == MM_F8 ? kF8Weights[i] : s.weight);
+                       s.occ * (float)(s.bq * s.bp) * (f8 ? kF8Weights[i] : s.weight);
     if (cost < least) least = cost, m.shape = i, m.tail = 1, m.rows = s.bq, m.cols = s.bp;
   }
   if (m.tail) m.scratch = 256l * kMmShapes[m.shape].occ * kMmShapes[m.shape].bq * kMmShapes[m.shape].bp * 4;
@@ -115,7 +116,7 @@ static MmPlan shape_plan(int op, int type, long E, long R, long N, long K, int b
 // A gated block is chosen for as the product with both its branches' channels.
 MmPlan mm_plan(int op, int type, long E, long R, long N, long K) {
   if (op == MM_GLU_DX) return shape_plan(MM_DX, type, E, R, N, K, kBuiltGrad);
-  if (op != MM_GLU) return shape_plan(op, type, E, R, N, K, type == MM_F8 ? kBuilt : kPlain);
+  if (op != MM_GLU) return shape_plan(op, type, E, R, N, K, type == MM_F8 || type == MM_F8X ? kBuilt : kPlain);
   MmPlan m = shape_plan(MM_FORWARD, type, E, R, 2 * N, K, kBuilt);
   m.cols /= 2;
   return m;
@@ -147,7 +148,7 @@ hipError_t launch_mm(const MmArgs &args, hipStream_t s) {
   const MmPlan m = mm_plan(args.op, args.type, args.E, args.R, args.N, args.K);
   MmArgs a = args;
   a.splits = m.splits, a.tail = m.tail;
-  if (a.type == MM_F8) return launch_fp8(a, m, s);
+  if (a.type == MM_F8 || a.type == MM_F8X) return launch_fp8(a, m, s);
   if (a.op == MM_GLU || a.op == MM_GLU_DX) return launch_glu(a, m, s);
   return a.type == MM_I8     ? launch_forward<MM_I8>(a, m, s)
          : a.type == MM_BF16 ? launch_16bit<MM_BF16>(a, m, s)

@@ -95,9 +95,15 @@ int check_apart(const char *fn, std::initializer_list<Span> written, std::initia
   return MOE_OK;
 }
 
+// An op without MOE_FP8_FAST_SUMS, which the 8-bit floating-point products may have.
+int plain_op(int op) {
+  const int p = op & ~MOE_FP8_FAST_SUMS;
+  return op >= 0 && (p == MOE_MM_FP8 || p == MOE_MM_FP8_GLU) ? p : op;
+}
 bool one_byte(int op) { return op == MOE_MM_INT8 || op == MOE_MM_FP8 || op == MOE_MM_FP8_GLU; }
 
 int check_op(const char *fn, int op, int E, int R, int N, int K) {
+  op = plain_op(op);
   if (op < MOE_MM_FORWARD || op > MOE_MM_FP8_GLU) return fail(MOE_EINVAL, "%s: op=%d", fn, op);
   // (the gated block's two branches together are as long as a row or column may be)
   const int two = op == MOE_MM_GLU || op == MOE_MM_FP8_GLU ? N : op == MOE_MM_GLU_DX ? K : 0;
@@ -109,8 +115,9 @@ moe::MmPlan plan_of(int op, int E, int R, int N, int K) {
   static const struct { int op, type; } kinds[] = {
       {moe::MM_FORWARD, moe::MM_BF16}, {moe::MM_DX, moe::MM_BF16},     {moe::MM_DW, moe::MM_BF16},
       {moe::MM_FORWARD, moe::MM_I8},   {moe::MM_GLU, moe::MM_BF16},    {moe::MM_GLU_DX, moe::MM_BF16},
-      {moe::MM_FORWARD, moe::MM_F8},   {moe::MM_GLU, moe::MM_F8}};
-  return moe::mm_plan(kinds[op - 1].op, kinds[op - 1].type, E, R, N, K);
+      {moe::MM_FORWARD, moe::MM_F8X},  {moe::MM_GLU, moe::MM_F8X}};
+  const auto &kind = kinds[plain_op(op) - 1];
+  return moe::mm_plan(kind.op, plain_op(op) != op ? moe::MM_F8 : kind.type, E, R, N, K);
 }
 
 // The activation that a call names, for a block of I columns.
@@ -361,11 +368,14 @@ int moe_quant_fp8(int dtype, const void *x, int rows, int cols, uint8_t *q, floa
 namespace {
 
 // The two products of 8-bit floating-point operands: N outputs, of as many or 2 N rows of w.
-int fp8_product(const char *fn, int op, const uint8_t *x, const float *x_scales, long long x_rows, const int32_t *rows,
+int fp8_product(const char *fn, bool glu, const uint8_t *x, const float *x_scales, long long x_rows, const int32_t *rows,
                 const uint8_t *w, const float *w_scales, const int32_t *first, int E, int R, int N, int K,
                 const moe_glu_form *form, int out_dtype, void *out, void *scratch, size_t scratch_bytes, void *stream) {
-  const bool glu = op == MOE_MM_FP8_GLU;
+  const bool fast = out_dtype >= 0 && out_dtype & MOE_FP8_FAST_SUMS;
+  const int op = (glu ? MOE_MM_FP8_GLU : MOE_MM_FP8) | (fast ? MOE_FP8_FAST_SUMS : 0);
   moe::MmArgs a = {};
+  if (fast) out_dtype &= ~MOE_FP8_FAST_SUMS;
+  if (fast && out_dtype == MOE_T_FP32) return fail(MOE_EUNSUPPORTED, "%s: fp32 results have no fast sums", fn);
   if (out_dtype != MOE_T_BF16 && out_dtype != MOE_T_FP16 && out_dtype != MOE_T_FP32)
     return fail(MOE_EUNSUPPORTED, "%s: out_dtype %d", fn, out_dtype);
   TRY(check_op(fn, op, E, R, N, K));
@@ -386,7 +396,7 @@ int fp8_product(const char *fn, int op, const uint8_t *x, const float *x_scales,
                    {w_scales, wide * E * blocks(N) * blocks(K) * sizeof *w_scales}, {first, (E + 1) * sizeof *first},
                    {rows, R * sizeof *rows}}));
   a.part = (float *)scratch;
-  a.op = glu ? moe::MM_GLU : moe::MM_FORWARD, a.type = moe::MM_F8, a.out_type = out_dtype;
+  a.op = glu ? moe::MM_GLU : moe::MM_FORWARD, a.type = fast ? moe::MM_F8 : moe::MM_F8X, a.out_type = out_dtype;
   a.x = x, a.x_rows = (long)x_rows, a.rows = rows, a.x_scales = x_scales, a.w = w, a.w_scales = w_scales;
   a.first = first, a.E = E, a.R = R, a.N = N, a.K = K, a.out = out;
   return launched(moe::launch_mm(a, (hipStream_t)stream), fn);
@@ -397,7 +407,7 @@ int fp8_product(const char *fn, int op, const uint8_t *x, const float *x_scales,
 int moe_grouped_fp8_mm(const uint8_t *x, const float *x_scales, long long x_rows, const int32_t *rows, const uint8_t *w,
                        const float *w_scales, const int32_t *first, int E, int R, int N, int K, int out_dtype,
                        void *out, void *scratch, size_t scratch_bytes, void *stream) {
-  return fp8_product(first ? "moe_grouped_fp8_mm" : "moe_fp8_mm", MOE_MM_FP8, x, x_scales, x_rows, rows, w, w_scales,
+  return fp8_product(first ? "moe_grouped_fp8_mm" : "moe_fp8_mm", false, x, x_scales, x_rows, rows, w, w_scales,
                      first, E, R, N, K, nullptr, out_dtype, out, scratch, scratch_bytes, stream);
 }
 
@@ -405,7 +415,7 @@ int moe_grouped_fp8_glu(const uint8_t *x, const float *x_scales, long long x_row
                         const uint8_t *w, const float *w_scales, const int32_t *first, int E, int R, int I, int K,
                         const moe_glu_form *form, int out_dtype, void *h, void *scratch, size_t scratch_bytes,
                         void *stream) {
-  return fp8_product(first ? "moe_grouped_fp8_glu" : "moe_fp8_glu", MOE_MM_FP8_GLU, x, x_scales, x_rows, rows, w,
+  return fp8_product(first ? "moe_grouped_fp8_glu" : "moe_fp8_glu", true, x, x_scales, x_rows, rows, w,
                      w_scales, first, E, R, I, K, form, out_dtype, h, scratch, scratch_bytes, stream);
 }
 

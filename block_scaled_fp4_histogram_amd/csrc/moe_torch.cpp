@@ -542,10 +542,10 @@ PyObject *quant_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// (x, x_scales, w, w_scales[, first, rows][, the form's five], out, out_dtype, scratch)
+// (x, x_scales, w, w_scales[, first, rows][, the form's five], out, out_dtype, scratch, fast_sums)
 template <bool GROUPED, bool GLU>
 PyObject *fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return guarded(n, 7 + (GROUPED ? 2 : 0) + (GLU ? 5 : 0), [&] {
+  return guarded(n, 8 + (GROUPED ? 2 : 0) + (GLU ? 5 : 0), [&] {
     Operands ops;
     const Tensor &x = tensor_of(a[0], "x", 2), &w = tensor_of(a[2], "w", GROUPED ? 3 : 2);
     const int64_t T = x.size(0), K = x.size(1), E = GROUPED ? w.size(0) : 1, W = w.size(w.dim() - 2);
@@ -563,16 +563,19 @@ PyObject *fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     moe_glu_form f = {};
     if (GLU) f = form(o), o += 5;
     const ScalarType ot = out_type(ops, o[0], o[1], at::kBFloat16, {at::kBFloat16, at::kHalf, at::kFloat}, {g.R, N});
+    const bool fast = truth(o[3]);
+    if (fast && ot == at::kFloat) refuse(PyExc_TypeError, "fast_sums: fp32 results are summed in fp32");
     ops.check();
     const int e = size32(E, "E"), r = size32(g.R, "R"), nn = size32(N, "N"), k = size32(K, "K");
+    const int sums = fast ? MOE_FP8_FAST_SUMS : 0, oc = code(ot) | sums;
     c10::DeviceGuard guard(x.device());
     const Tensor out = none(o[0]) ? make({g.R, N}, ot, x) : tensor(o[0], "out");
-    const Scratch s(o[2], f_mm_scratch(GLU ? MOE_MM_FP8_GLU : MOE_MM_FP8, e, r, nn, k), x);
+    const Scratch s(o[2], f_mm_scratch((GLU ? MOE_MM_FP8_GLU : MOE_MM_FP8) | sums, e, r, nn, k), x);
     const uint8_t *px = (const uint8_t *)ptr(&x), *pw = (const uint8_t *)ptr(&w);
     const float *pxs = (const float *)ptr(&xs), *pws = (const float *)ptr(&ws);
     const int32_t *first = (const int32_t *)ptr(g.first), *rows = (const int32_t *)ptr(g.rows);
-    if (GLU) done(f_fp8_glu(px, pxs, T, rows, pw, pws, first, e, r, nn, k, &f, code(ot), out.data_ptr(), s.p, s.bytes, stream_of(x)));
-    else done(f_fp8(px, pxs, T, rows, pw, pws, first, e, r, nn, k, code(ot), out.data_ptr(), s.p, s.bytes, stream_of(x)));
+    if (GLU) done(f_fp8_glu(px, pxs, T, rows, pw, pws, first, e, r, nn, k, &f, oc, out.data_ptr(), s.p, s.bytes, stream_of(x)));
+    else done(f_fp8(px, pxs, T, rows, pw, pws, first, e, r, nn, k, oc, out.data_ptr(), s.p, s.bytes, stream_of(x)));
     return result(o[0], out);
   });
 }

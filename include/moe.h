@@ -361,11 +361,15 @@ typedef enum {
   MOE_MM_FP8_GLU = 8        /* N is the gated block's I */
 } moe_mm_op;
 
+/* With the 8-bit floating-point products: see moe_grouped_fp8_mm. */
+#define MOE_FP8_FAST_SUMS 16
+
 /* Scratch bytes of one product: op as in moe_mm_op (MOE_MM_FORWARD is
  * moe_grouped_mm, MOE_MM_INT8 moe_int8_mm with E = 1 and R = M, and
  * moe_grouped_int8_mm; MOE_MM_GLU to MOE_MM_FP8_GLU are moe_grouped_glu,
- * moe_grouped_glu_dx, moe_grouped_fp8_mm and moe_grouped_fp8_glu).  Host only; 0
- * on sizes that the call refuses. */
+ * moe_grouped_glu_dx, moe_grouped_fp8_mm and moe_grouped_fp8_glu; the last two with
+ * MOE_FP8_FAST_SUMS or'ed to op as to the call's out_dtype).  Host only; 0 on sizes
+ * that the call refuses. */
 size_t moe_mm_scratch_bytes(int op, int E, int R, int N, int K);
 
 /*
@@ -490,13 +494,15 @@ int moe_quant_fp8(int dtype, const void *x, int rows, int cols, uint8_t *q, floa
  * x_scales[row(r), b] * w_scales[e, n / 128, b] * sum_{k in b} x[row(r), k] * w[e, n, k].
  * A block's sum is scaled by the two scales' powers of two and by their fractions'
  * product, so only the result's range counts, not that of the scales' product; an
- * infinite or NaN scale makes what it enters infinite or NaN.  Sums are kept in fp32.
- * With 16-bit results of more than a few rows a group the sum of eight consecutive
- * products is first formed by the 8-bit matrix instruction, which drops what lies 2^-13
- * below the largest of them: less than 2^-10 of that product in all, a thirtieth of a bf16
- * step of a typical result.  fp32 results, and few rows, are summed in fp32 throughout.
+ * infinite or NaN scale makes what it enters infinite or NaN.  Sums are kept in fp32
+ * throughout.
  * out_dtype MOE_T_BF16, MOE_T_FP16 or MOE_T_FP32; out [R, N].  first NULL with E = 1:
  * one group of all R rows.
+ * MOE_FP8_FAST_SUMS, or'ed to a 16-bit out_dtype, lets the 8-bit matrix instruction form
+ * the sums of eight consecutive products, at twice the rate.  It drops what lies 2^-13
+ * below the largest of the eight: less than 2^-10 of that product in all, about 5e-5 of a
+ * random sum, but all of a sum whose large products cancel.  (A few rows a group are
+ * summed in fp32 all the same.)
  */
 int moe_grouped_fp8_mm(const uint8_t *x, const float *x_scales, long long x_rows, const int32_t *rows, const uint8_t *w,
                        const float *w_scales, const int32_t *first, int E, int R, int N, int K, int out_dtype,
@@ -505,7 +511,7 @@ int moe_grouped_fp8_mm(const uint8_t *x, const float *x_scales, long long x_rows
 /*
  * moe_grouped_fp8_glu -- the gated block on such operands: w [E, 2 I, K], w_scales
  * [E, 2, ceil(I / 128), ceil(K / 128)] (each branch's blocks start at its first row),
- * h [R, I] in out_dtype.
+ * h [R, I] in out_dtype, sums as in moe_grouped_fp8_mm.
  */
 int moe_grouped_fp8_glu(const uint8_t *x, const float *x_scales, long long x_rows, const int32_t *rows,
                         const uint8_t *w, const float *w_scales, const int32_t *first, int E, int R, int I, int K,
