@@ -27,6 +27,19 @@ __device__ __forceinline__ Sigmoid sigmoid2(float x) {
   return x >= 0.0f ? Sigmoid{q, p} : Sigmoid{p, q};
 }
 
+// tanh(y) and 1 - tanh^2(y) from s = sigmoid(2 y): s - (1 - s), or where these come near each
+// other y + y^3 q(y^2), q fitted to (tanh(y) / y - 1) / y^2 up to 0.625 (within 2^-27), and
+// 4 s (1 - s), which keeps its precision where the tanh rounds to 1.
+struct Tanh {
+  float t, d;
+};
+__device__ __forceinline__ Tanh tanh2(float y) {
+  const Sigmoid s = sigmoid2(2.0f * y);
+  const float z = y * y;
+  const float q = fmaf(z, fmaf(z, fmaf(z, fmaf(z, -5.717041902e-3f, 2.065058425e-2f), -5.374349654e-2f), 1.333149076e-1f), -3.333328366e-1f);
+  return Tanh{fabsf(y) < 0.625f ? fmaf(y * z, q, y) : s.s - s.r, 4.0f * s.s * s.r};
+}
+
 // act(gate, up): gate sigmoid(alpha gate) (up + beta) after the limit, or SiTU,
 // silu(4 tanh(gate / 4)) 25 tanh(up / 25).
 __device__ __forceinline__ float glu_act(float gate, float up, const GluForm &f) {
@@ -48,10 +61,9 @@ __device__ __forceinline__ void glu_grad(float dh, float gate, float up, const G
   float g_in = 1.0f, u_in = 1.0f, alpha = f.alpha, beta = f.beta;
   bool g_out = false, u_out = false;
   if (f.act == ACT_SITU) {               // the same with alpha 1 on the capped branches, by the chain rule
-    // (1 - tanh^2(y) = 4 s (1 - s) at s = sigmoid(2 y), which keeps its precision where the tanh rounds to 1)
-    const Sigmoid sg = sigmoid2(0.5f * gate), su = sigmoid2(0.08f * up);
-    gate = 4.0f * tanhf(0.25f * gate), up = 25.0f * tanhf(0.04f * up);
-    g_in = 4.0f * sg.s * sg.r, u_in = 4.0f * su.s * su.r;
+    const Tanh tg = tanh2(0.25f * gate), tu = tanh2(0.04f * up);
+    gate = 4.0f * tg.t, up = 25.0f * tu.t;
+    g_in = tg.d, u_in = tu.d;
   } else if (f.has_limit) {
     g_out = gate > f.limit, u_out = fabsf(up) > f.limit;
     gate = clamp_above(gate, f.limit);
