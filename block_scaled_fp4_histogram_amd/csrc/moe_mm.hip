@@ -14,10 +14,19 @@ namespace moe {
 enum { kShapes = 4 };
 static const struct { int bq, bp, occ; float weight; } kMmShapes[kShapes] = {
     {256, 128, 2, 1.0f}, {128, 256, 2, 1.04f}, {128, 128, 3, 1.2f}, {64, 128, 4, 1.5f}};
-// 8-bit floating point, whose scales of x's rows weigh less on wide tiles (one group of
-// that size: 309, 272, 304, 339 us; 64-row tiles read the weights of more groups twice:
-// 384 groups of 64 rows on average, 1152 x 7168: 870, 622, 680, 733 us).
-static const float kF8Weights[kShapes] = {1.0f, 0.9f, 1.05f, 1.45f};
+// 8-bit floating point, by fp16 instructions: one group of that size 537, 497, 550, 586 us,
+// and with every lane's conversions in front of the products a tile that has its SIMDs to
+// itself pays for its size (20 groups of 30 rows on average, 2040 x 6816: 266, 252, 128, 88
+// us): kF8xFew of launches of up to kF8xFewTiles tiles.  Over 14 drawn calls that this was
+// not fitted to, the choice took at most 3 % longer than the best shape.
+static const int kF8xOcc[kShapes] = {2, 2, 2, 4};
+static const float kF8xWeights[kShapes] = {0.98f, 0.95f, 1.02f, 1.08f}, kF8xFew[kShapes] = {1.3f, 1.3f, 1.2f, 1.0f};
+static const int kF8xFewTiles[kShapes] = {384, 384, 512, 0};
+// By the 8-bit instruction: 313, 295, 312, 356 us; 64-row tiles read the weights of more
+// groups twice (384 groups of 64 rows on average, 1152 x 7168: 891, 630, 681, 734 us) and
+// weigh as the mean over 28 timed calls has it (2.7 % more than the best shape, 21 % in the
+// worst).
+static const float kF8Weights[kShapes] = {1.0f, 0.95f, 1.05f, 1.35f};
 
 // Steps that a tile's start and end cost, fitted to 50 drawn sizes: in the gated block
 // little more than a product's, whose rounds are compared by their steps alone; with the
@@ -29,8 +38,7 @@ static const float kGluStart[kShapes] = {9.f, 8.f, 7.f, 6.f}, kGradStart[kShapes
 enum { kPlain = 0, kBuilt = 1, kBuiltGrad = 2 };
 static MmPlan shape_plan(int op, int type, long E, long R, long N, long K, int built) {
   MmPlan m = {0, 0, 1, 16, 16, 0, 0};
-  const bool f8 = type == MM_F8 || type == MM_F8X;
-  const long item = type == MM_I8 || f8 ? 1 : 2, groups = E < R ? E : R;
+  const long item = type == MM_I8 || type == MM_F8 || type == MM_F8X ? 1 : 2, groups = E < R ? E : R;
   const long pn = op == MM_FORWARD ? N : K, qn = op == MM_DW ? N : R, outs = op == MM_DW ? E * N : R;
   // Few rows a group: the weights pass once, 16 of their rows a block.  Short rows
   // make for blocks that mostly start and end (64 groups of 5 rows, N = 1024:
@@ -53,17 +61,21 @@ static MmPlan shape_plan(int op, int type, long E, long R, long N, long K, int b
   long tiles = 0;
   float least = 0.f;
   const long steps = op == MM_FORWARD ? K * item / 128 : op == MM_DX ? N / 64 : R / E / 64;
-  auto start = [&](int i) { return built ? (built == kBuiltGrad ? kGradStart : kGluStart)[i] : 0.f; };
+  auto start = [&](int i) {
+    return !built ? 0.f : built == kBuiltGrad ? kGradStart[i] : type == MM_F8X ? 0.5f * kGluStart[i] : kGluStart[i];
+  };
+  auto occ = [&](int i) { return type == MM_F8X ? kF8xOcc[i] : kMmShapes[i].occ; };
+  auto weight = [&](int i) { return type == MM_F8X ? kF8xWeights[i] : type == MM_F8 ? kF8Weights[i] : kMmShapes[i].weight; };
   for (int i = 0; i < kShapes; i++) {
     const auto &s = kMmShapes[i];
     if (op == MM_DW && i != 0 && i != 2) continue;
     long rows = (qn + s.bq - 1) / s.bq;
     if (op == MM_DW) rows *= E;
     else if (E > 1) rows = (R + groups * (s.bq / 2)) / s.bq > groups ? (R + groups * (s.bq / 2)) / s.bq : groups;
-    const long n = rows * ((pn + s.bp - 1) / s.bp), slots = 256l * s.occ;
-    const float weight = f8 ? kF8Weights[i] : s.weight;
-    float cost = (float)((n + slots - 1) / slots * s.occ) * (float)(s.bq * s.bp) * weight;
+    const long n = rows * ((pn + s.bp - 1) / s.bp), slots = 256l * occ(i);
+    float cost = (float)((n + slots - 1) / slots * occ(i)) * (float)(s.bq * s.bp) * weight(i);
     if (built) cost *= (float)steps + start(i);
+    if (type == MM_F8X && n <= kF8xFewTiles[i]) cost *= kF8xFew[i];
     if (!tiles || cost < least) m.shape = i, least = cost, tiles = n;
   }
   // Short weight gradients write more than they read, and more blocks store better
@@ -72,17 +84,18 @@ static MmPlan shape_plan(int op, int type, long E, long R, long N, long K, int b
   if (op == MM_DW && R <= 256 * E) m.shape = 2;
   // Too few tiles for the chip: the reduction is split into as many parts as take
   // least time.  The estimate is fitted to whole and split times: a step takes 0.6 us
-  // (1 us with transposed reads of both operands), all blocks' steps no less than
+  // (1 us with transposed reads of both operands and with conversions, 0.8 by the 8-bit
+  // floating-point instruction), all blocks' steps no less than
   // their loads at 12 TB/s (not a bound: full rounds of blocks fill LDS at 14 to 16);
   // the second launch, which joins the parts in order, 4 us, and their bytes twice at
   // 4 TB/s (R = 256, N = 1024, K = 4096: 15.2 us, 41.3 us whole; int8, R = 500,
   // N = 4608, K = 7168: 45.4 us in parts that fill the chip, 39.6 whole).
   const auto &shape = kMmShapes[m.shape];
   m.rows = shape.bq, m.cols = shape.bp;
-  const float step = op == MM_DW ? 1.0f : 0.6f;
+  const float step = op == MM_DW || type == MM_F8X ? 1.0f : type == MM_F8 ? 0.8f : 0.6f;
   const float feed = (float)(tiles * steps * (shape.bq + shape.bp)) * (128 / 12e6f);
   float best = steps * step > feed ? steps * step : feed;
-  for (long n = 2; n <= 16 && n * tiles <= 256l * shape.occ; n++) {
+  for (long n = 2; n <= 16 && n * tiles <= 256l * occ(m.shape); n++) {
     const float run = (float)((steps + n - 1) / n) * step;
     const float us = (run > feed ? run : feed) + 4.0f + (float)(n * outs * pn) * 2e-6f;
     if (us < best) best = us, m.splits = (int)n;
@@ -101,15 +114,15 @@ static MmPlan shape_plan(int op, int type, long E, long R, long N, long K, int b
     const auto &s = kMmShapes[i];
     const long rows = E > 1 ? ((R + groups * (s.bq / 2)) / s.bq > groups ? (R + groups * (s.bq / 2)) / s.bq : groups)
                             : (R + s.bq - 1) / s.bq;
-    const long slots = 256l * s.occ, n = rows * ((pn + s.bp - 1) / s.bp);
+    const long slots = 256l * occ(i), n = rows * ((pn + s.bp - 1) / s.bp);
     if (n > 1l << 23) continue;
     const MmTail t = mm_tail((int)n, (int)slots, (int)steps);
     if (t.parts < 2 || (t.full == 0 && steps < 64)) continue;
     const float cost = ((float)(t.full / slots) * ((float)steps + start(i)) + (1.0f / t.parts + 0.05f) * (float)steps + 8.0f) *
-                       s.occ * (float)(s.bq * s.bp) * (f8 ? kF8Weights[i] : s.weight);
+                       occ(i) * (float)(s.bq * s.bp) * weight(i);
     if (cost < least) least = cost, m.shape = i, m.tail = 1, m.rows = s.bq, m.cols = s.bp;
   }
-  if (m.tail) m.scratch = 256l * kMmShapes[m.shape].occ * kMmShapes[m.shape].bq * kMmShapes[m.shape].bp * 4;
+  if (m.tail) m.scratch = 256l * occ(m.shape) * kMmShapes[m.shape].bq * kMmShapes[m.shape].bp * 4;
   return m;
 }
 
