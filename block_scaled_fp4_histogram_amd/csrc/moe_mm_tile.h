@@ -173,10 +173,10 @@ struct MmConst {
   static constexpr int value = V;
 };
 constexpr int MM_PART = 5;   // 32-bit sums of one part of the reduction, as they are
-template <typename F>
+template <int TYPE, typename F>
 __device__ __forceinline__ void mm_by_output(int out_type, F f) {
   if (out_type == MM_PART) f(MmConst<MM_PART>{});
-  else if (out_type == MM_FP32) f(MmConst<MM_FP32>{});
+  else if (TYPE != MM_F8 && out_type == MM_FP32) f(MmConst<MM_FP32>{});   // (MM_F8 has 16-bit results)
   else if (out_type == MM_BF16) f(MmConst<MM_BF16>{});
   else f(MmConst<MM_FP16>{});
 }
@@ -233,6 +233,10 @@ struct MmTile {
 // row gradients (of dy and w) and weight gradients read theirs transposed.
 constexpr bool mm_forward(int op) { return op == MM_FORWARD || op == MM_GLU; }
 constexpr bool mm_dx(int op) { return op == MM_DX || op == MM_GLU_DX; }
+// The gated block's products and 8-bit floating point; of these the shapes whose last round
+// may be in parts (of two blocks a CU: the plan takes no other).
+constexpr bool mm_built(int op, int type) { return op == MM_GLU || op == MM_GLU_DX || type == MM_F8 || type == MM_F8X; }
+constexpr bool mm_has_tail(int op, int type, int bq, int bp) { return mm_built(op, type) && bq * bp == 256 * 128; }
 // Columns of the output, and of a tile of BP rows of w: the gated block's come from two.
 __host__ __device__ __forceinline__ constexpr int mm_outs(int op, int N, int K) { return mm_forward(op) ? N : K; }
 constexpr int mm_tile_cols(int op, int bp) { return op == MM_GLU ? bp / 2 : bp; }
@@ -383,8 +387,8 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   const int ptiles = (pn + BC - 1) / BC;
   MmTile t;
   int q0 = 0, qn, zn;                                           // output rows of the tile, reduction
-  // of the products built on these: a tile of the last round in parts (mm_tail)
-  constexpr bool TAIL = GLU || OP == MM_GLU_DX || F8;
+  // of the products built on these, in their largest shapes: a tile of the last round in parts (mm_tail)
+  constexpr bool TAIL = mm_has_tail(OP, TYPE, BQ, BP);
   int part = 0, parts = 1, tail_at = 0;                         // this block's part, and its tile's number among them
   if (OP == MM_DW) {
     // each group's tiles spread over the XCDs, so that a large group does not load one of them
@@ -463,7 +467,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
   static_assert(!GLU || (DP <= HP && HP % DP == 0), "branches of P");
   const Rsrc rp = FWD ? mm_rsrc(wt + (size_t)(p0 + (GLU ? a.glu.gate0 : 0)) * ldx, (uint32_t)min(BC, pn - p0) * ldx) : mm_rsrc(wt, 0);
   // Gathered rows within 2 GiB are loaded through one resource over x, as rows in order are.
-  constexpr bool NEAR = GATHER && TAIL;
+  constexpr bool NEAR = GATHER && mm_built(OP, TYPE);
   bool near = false;
   if constexpr (NEAR) near = a.x_rows * (long)ldx < 0x7FFFFFFFl;
   const Rsrc rx = mm_rsrc(x, (uint32_t)(near ? a.x_rows * (long)ldx : 0));
@@ -875,7 +879,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       for (int j = 0; j < NQ; j++)
 #pragma unroll
         for (int k = 0; k < 4; k++) acc[i][j][k] = glu_act(acc[i][j][k], acc[NG + i][j][k], a.glu);
-    mm_by_output(a.out_type, [&](auto out) {
+    mm_by_output<TYPE>(a.out_type, [&](auto out) {
       constexpr int OUT = decltype(out)::value;
       if constexpr (OUT != MM_PART) {
 #pragma unroll
@@ -912,7 +916,7 @@ __global__ __launch_bounds__(64 * WQ * WP, MINW) void k_mm_tile(MmArgs a) {
       }
     return;
   }
-  mm_by_output(a.splits > 1 || parts > 1 ? MM_PART : a.out_type, [&](auto out) {
+  mm_by_output<TYPE>(a.splits > 1 || parts > 1 ? MM_PART : a.out_type, [&](auto out) {
     constexpr int OUT = decltype(out)::value;
     constexpr bool WIDE = OUT == MM_FP32 || OUT == MM_PART, NT = OP == MM_DW && OUT != MM_PART;
     constexpr int RB = WIDE ? 64 * 4 + 16 : 64 * 2 + 16;   // a row, and 16 bytes that spread the rows over the banks
@@ -996,7 +1000,7 @@ __global__ __launch_bounds__(256) void k_mm_join(MmArgs a) {
     const long xr = mm_x_row(a, (int)row);
     if (xr >= 0) xs = mm_scale(a.x_scales[xr]);
   }
-  mm_by_output(a.out_type, [&](auto out) {
+  mm_by_output<TYPE>(a.out_type, [&](auto out) {
     constexpr int OUT = decltype(out)::value;
     if constexpr (OUT != MM_PART) {
       for (int p = threadIdx.x * 8; p < pn; p += 256 * 8) {
@@ -1046,7 +1050,7 @@ __device__ __forceinline__ void glu_finish(const MmArgs &a, int pn, long row, in
       if constexpr (OP == MM_GLU) v[k] = glu_act(s[0][k >> 2][k & 3], s[1][k >> 2][k & 3], a.glu);
       else v[k] = s[0][k >> 2][k & 3];
     }
-    mm_by_output(a.out_type, [&](auto out) {
+    mm_by_output<TYPE>(a.out_type, [&](auto out) {
       constexpr int OUT = decltype(out)::value;
       if constexpr (OUT != MM_PART) mm_store8<OUT>(a, row * pn + p, v);
     });
@@ -1114,7 +1118,7 @@ __global__ __launch_bounds__(256) void k_tail_join(MmArgs a) {
 
 template <int OP, int TYPE, int BQ, int BP, int WQ, int WP, int MINW>
 static hipError_t launch_tile(const MmArgs &a, hipStream_t s) {
-  constexpr bool TAIL = OP == MM_GLU || OP == MM_GLU_DX || TYPE == MM_F8 || TYPE == MM_F8X;
+  constexpr bool TAIL = mm_has_tail(OP, TYPE, BQ, BP);
   constexpr int BC = mm_tile_cols(OP, BP);
   const long pn = mm_outs(OP, a.N, a.K), ptiles = (pn + BC - 1) / BC;
   long blocks;
@@ -1294,7 +1298,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_mm_stream(MmArgs a) {
   // sums of the waves: [wave][row][channel]
   sum[((w * 16 + l16) * RS + 4 * g) >> 2] = acc;
   __syncthreads();
-  mm_by_output(a.out_type, [&](auto out) {
+  mm_by_output<TYPE>(a.out_type, [&](auto out) {
     constexpr int OUT = decltype(out)::value;
     if (!writes) return;
     auto joined = [&](int c) {

@@ -52,16 +52,18 @@ def last_round(counts, N, K, rows, cols, glu):
     return parts, words * parts * (2 if glu else 1)
 
 
-def split_sizes(glu, groups, op=None):
-    """The least (counts, N, K) of a list that the plan takes in parts (0) and whose offsets make a last round that
-    is split."""
+def split_sizes(glu, groups, op=None, shape=None):
+    """The least (counts, N, K) of a list that the plan takes in parts (0), in tiles of `shape` where it is given,
+    and whose offsets make a last round that is split."""
     op = op or (M.MM_FP8_GLU if glu else M.MM_FP8)
     found = None
-    for c, e, n, k in itertools.product([600, 1000, 1100, 2100, 4097], groups, [520, 1032, 2056, 2304, 4608], [2064, 4112, 7168]):
+    for c, e, n, k in itertools.product([600, 1000, 1100, 2100, 2561, 4097], groups, [520, 1032, 2056, 2304, 4608], [2064, 4112, 7168]):
         counts = [c] if e == 1 else [c + 3, 0, c - 2] + [c] * (e - 3)
         if found is not None and sum(counts) * n * k >= found[0]:
             continue
         rows, cols, parts = M.debug_mm_plan(op, e, sum(counts), n, k)
+        if shape and (rows, cols * (2 if glu else 1)) != shape:
+            continue
         if parts == 0 and last_round(counts, n, k, rows, cols, glu)[0] >= 2:
             found = (sum(counts) * n * k, counts, n, k)
     assert found, "no such sizes"
@@ -69,12 +71,12 @@ def split_sizes(glu, groups, op=None):
 
 
 @pytest.mark.parametrize("out_dtype", [BF16, FP16, FP32])
-@pytest.mark.parametrize("groups", [[1], [5, 9, 12, 24, 40]])
+@pytest.mark.parametrize("groups,shape", [([1], None), ([5, 9, 12, 24, 40], (128, 256)), ([5, 9, 12, 24, 40], (256, 128))])
 @pytest.mark.parametrize("glu", [False, True])
-def test_last_rounds_are_split_and_joined(glu, groups, out_dtype):
+def test_last_rounds_are_split_and_joined(glu, groups, shape, out_dtype):
     """The plan's 0 parts, the tile count that the offsets make, and the sums that scratch (all ones before) holds
     afterwards agree, so the split and the join have run; and the results are right."""
-    counts, N, K = split_sizes(glu, groups)
+    counts, N, K = split_sizes(glu, groups, shape=shape)
     op, R, E = M.MM_FP8_GLU if glu else M.MM_FP8, sum(counts), len(counts)
     rows, cols, parts = M.debug_mm_plan(op, E, R, N, K)
     assert parts == 0
@@ -142,15 +144,15 @@ def test_sums_whose_large_products_cancel(how, glu, out_dtype):
 
 @pytest.mark.parametrize("out_dtype", [BF16, FP16])
 @pytest.mark.parametrize("glu", [False, True])
-@pytest.mark.parametrize("shape", [(16, 16), *FAST_TILES, "split", "last round"], ids=str)
+@pytest.mark.parametrize("shape", [(16, 16), *FAST_TILES, "split", "last round 128", "last round 256"], ids=str)
 def test_fast_sums(shape, glu, out_dtype):
     """Every shape by the 8-bit instruction: within its cut of the reference, and exact where no product is cut
     (whole numbers of at most 16 by 16: 2^8 by 1, nothing 2^-13 below)."""
     op = (M.MM_FP8_GLU if glu else M.MM_FP8) | M.FP8_FAST_SUMS
     if shape == "split":
         counts, N, K = [90, 0, 140], 72, 8192
-    elif shape == "last round":
-        counts, N, K = split_sizes(glu, [1, 5, 9, 12, 24], op)
+    elif isinstance(shape, str):
+        counts, N, K = split_sizes(glu, [1, 5, 9, 12, 24, 40], op, (128, 256) if shape.endswith("128") else (256, 128))
     else:
         counts, N, K = sizes_for(op, (shape[0], shape[1] // 2) if glu else shape, 1)
     x, xs, w, ws, first = _operands(counts, N, K, glu, seed=N)
