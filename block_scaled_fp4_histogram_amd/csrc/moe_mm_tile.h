@@ -86,24 +86,15 @@ __device__ __forceinline__ void mm_factors8(MmScale8 w, MmScale8 x, float &first
   second = __builtin_ldexpf(1.0f, min(max(e - near, -126), 127));
 }
 
-// acc + a block's sum times its scales: w's as the matrix operand's row has it (row),
-// as the sum has it (sum), and x's.
-template <int TYPE>
-__device__ __forceinline__ v4f f8_block(v4f acc, v8i p, v8i q, int row, MmScale8 sum, MmScale8 x) {
-  const v4f zero = {0.f, 0.f, 0.f, 0.f};
-  const float m = sum.m * x.m;
-  if constexpr (TYPE == MM_F8) {
-    const v4f d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, zero, 0, 0, 0, row, 0, x.code);
+// acc + a block's sum times its scales.
+__device__ __forceinline__ v4f f8_block(v4f acc, v8i p, v8i q, MmScale8 w, MmScale8 x) {
+  float first, second;
+  mm_factors8(w, x, first, second);
+  v4f d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < 4; k++) acc[k] = fmaf(d[k], m, acc[k]);
-  } else {
-    v4f d = zero;
+  for (int k = 0; k < 4; k++) d = mfma_f16(codes_f16(p[2 * k], p[2 * k + 1]), codes_f16(q[2 * k], q[2 * k + 1]), d);
 #pragma unroll
-    for (int k = 0; k < 4; k++) d = mfma_f16(codes_f16(p[2 * k], p[2 * k + 1]), codes_f16(q[2 * k], q[2 * k + 1]), d);
-#pragma unroll
-    for (int k = 0; k < 4; k++) acc[k] += __builtin_ldexpf(d[k] * m, sum.code + x.code - 254);
-    // (an infinite or NaN scale's factor is one too: NaN or, where MM_F8 gives NaN, infinite)
-  }
+  for (int k = 0; k < 4; k++) acc[k] = fmaf(d[k] * first, second, acc[k]);
   return acc;
 }
 
@@ -1170,20 +1161,19 @@ __device__ __forceinline__ void stream_read(uint32_t pw0, uint32_t pw1, uint32_t
       : "memory");
 }
 
-// The same with a column's three scales.
+// The same with a column's two scales.
 __device__ __forceinline__ void stream_read8(uint32_t pw0, uint32_t pw1, uint32_t px0, uint32_t px1, uint32_t s0,
-                                             uint32_t s1, uint32_t s2, v4i *w, v4i *x, float &a, float &b, float &c) {
+                                             uint32_t s1, v4i *w, v4i *x, float &a, float &b) {
   asm volatile(
-      "ds_read_b128 %0, %7\n"
-      "ds_read_b128 %1, %8\n"
-      "ds_read_b128 %2, %9\n"
-      "ds_read_b128 %3, %10\n"
-      "ds_read_b32 %4, %11\n"
-      "ds_read_b32 %5, %12\n"
-      "ds_read_b32 %6, %13\n"
+      "ds_read_b128 %0, %6\n"
+      "ds_read_b128 %1, %7\n"
+      "ds_read_b128 %2, %8\n"
+      "ds_read_b128 %3, %9\n"
+      "ds_read_b32 %4, %10\n"
+      "ds_read_b32 %5, %11\n"
       "s_waitcnt lgkmcnt(0)"
-      : "=&v"(w[0]), "=&v"(w[1]), "=&v"(x[0]), "=&v"(x[1]), "=&v"(a), "=&v"(b), "=&v"(c)
-      : "v"(pw0), "v"(pw1), "v"(px0), "v"(px1), "v"(s0), "v"(s1), "v"(s2)
+      : "=&v"(w[0]), "=&v"(w[1]), "=&v"(x[0]), "=&v"(x[1]), "=&v"(a), "=&v"(b)
+      : "v"(pw0), "v"(pw1), "v"(px0), "v"(px1), "v"(s0), "v"(s1)
       : "memory");
 }
 
@@ -1280,11 +1270,11 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_mm_stream(MmArgs a) {
       const uint32_t o = (uint32_t)(s % D) * kSlot;
       v4i fw[2], fx[2];
       if constexpr (F8) {
-        // the scale of w that the operand's row l16 has, and that the sums of lane group g have
-        float sr, sc, sx;
-        stream_read8(rd0 + o, rd1 + o, rd0 + o + 2048, rd1 + o + 2048, base + o + 4096 + (GLU && l16 >= 8 ? 68 : 64),
-                     base + o + 4096 + (GLU && g >= 2 ? 68 : 64), base + o + 4096 + l16 * 4, fw, fx, sr, sc, sx);
-        acc = f8_block<TYPE>(acc, join8(fw[0], fw[1]), join8(fx[0], fx[1]), mm_scale8(sr).code, mm_scale8(sc), mm_scale8(sx));
+        // the scale of w that the sums of lane group g have
+        float sc, sx;
+        stream_read8(rd0 + o, rd1 + o, rd0 + o + 2048, rd1 + o + 2048, base + o + 4096 + (GLU && g >= 2 ? 68 : 64),
+                     base + o + 4096 + l16 * 4, fw, fx, sc, sx);
+        acc = f8_block(acc, join8(fw[0], fw[1]), join8(fx[0], fx[1]), mm_scale8(sc), mm_scale8(sx));
       } else {
         stream_read(rd0 + o, rd1 + o, rd0 + o + 2048, rd1 + o + 2048, fw, fx);
         acc = M::mma(fw[0], fx[0], acc);
