@@ -7,6 +7,7 @@ import torch
 
 import block_scaled_fp4_histogram_amd as M
 from gated_util import act_bound, assert_close, branches, codes, fp8_bound, ref_act, ref_fp8
+from last_round_util import last_round
 from products_util import BF16, FP16, FP32, offsets
 from test_gpu_fp8 import TILES, sizes_for
 
@@ -33,25 +34,6 @@ def _operands(counts, N, K, glu, seed=0):
     return x, xs, w, ws / (100 * K ** 0.5), offsets(counts).cuda()
 
 
-def last_round(counts, N, K, rows, cols, glu):
-    """(parts of each tile of the last round, sums that they leave in scratch) for tiles of rows x cols outputs at
-    two blocks a CU: tiles in groups of eight row tiles over the columns, the last 512 or fewer of them in as many
-    parts as fill 512 blocks, at most eight and of at least eight steps each; (1, 0) where they stay whole."""
-    row_tiles = [min(rows, c - r) for c in counts for r in range(0, c, rows)]
-    ptiles, steps = -(-N // cols), -(-K // 128)
-    n = len(row_tiles) * ptiles
-    rest = n % 512
-    parts = min(512 // rest, 8, steps // 8) if rest else 1
-    if parts < 2:
-        return 1, 0
-    words = 0
-    for t in range(n - rest, n):
-        grp, rem = divmod(t, 8 * ptiles)
-        cur = min(8, len(row_tiles) - grp * 8)
-        words += row_tiles[grp * 8 + rem % cur] * min(cols, N - rem // cur * cols)
-    return parts, words * parts * (2 if glu else 1)
-
-
 def split_sizes(glu, groups, op=None, shape=None):
     """The least (counts, N, K) of a list that the plan takes in parts (0), in tiles of `shape` where it is given,
     and whose offsets make a last round that is split."""
@@ -64,7 +46,7 @@ def split_sizes(glu, groups, op=None, shape=None):
         rows, cols, parts = M.debug_mm_plan(op, e, sum(counts), n, k)
         if shape and (rows, cols * (2 if glu else 1)) != shape:
             continue
-        if parts == 0 and last_round(counts, n, k, rows, cols, glu)[0] >= 2:
+        if parts == 0 and last_round(counts, n, rows, cols, -(-k // 128))[0] >= 2:
             found = (sum(counts) * n * k, counts, n, k)
     assert found, "no such sizes"
     return found[1:]
@@ -80,7 +62,7 @@ def test_last_rounds_are_split_and_joined(glu, groups, shape, out_dtype):
     op, R, E = M.MM_FP8_GLU if glu else M.MM_FP8, sum(counts), len(counts)
     rows, cols, parts = M.debug_mm_plan(op, E, R, N, K)
     assert parts == 0
-    split, words = last_round(counts, N, K, rows, cols, glu)
+    split, words = last_round(counts, N, rows, cols, -(-K // 128), 2 if glu else 1)
     assert split >= 2
     x, xs, w, ws, first = _operands(counts, N, K, glu, seed=K)
     scratch = torch.full((M.mm_scratch_bytes(op, E, R, N, K),), 255, dtype=torch.uint8, device="cuda")
@@ -208,3 +190,30 @@ def test_fast_sums_are_for_16_bit_results():
         s.synchronize()
         assert torch.equal(call(fast_sums=True, stream=s), want)
         s.synchronize()
+
+
+# ---- offsets that fall and overlap, where last rounds are in parts
+
+
+@pytest.mark.parametrize("glu", [False, True])
+def test_offsets_that_go_wrong_in_a_last_round(glu):
+    """Three groups of rows 0 to 1200, to 2400 and, the offsets falling, 2000 to 4000, three groups of none: tiles
+    enough for a last round in parts. Rows of one group are right, rows of none stay."""
+    N, K, R = (2304 if glu else 4608), 4112, 4097
+    op = M.MM_FP8_GLU if glu else M.MM_FP8
+    rows, cols, parts = M.debug_mm_plan(op, 6, R, N, K)
+    assert parts == 0 and last_round([1200, 1200, 0, 2000], N, rows, cols, -(-K // 128))[0] >= 2
+    x, xs, w, ws, _ = _operands([R, 0, 0, 0, 0, 0], N, K, glu)
+    first = torch.tensor([0, 1200, 2400, 2000, 4000, 1000, -7], dtype=torch.int32, device="cuda")
+    out = torch.full((R, N), 7.5, dtype=BF16, device="cuda")
+    (M.grouped_fp8_glu if glu else M.grouped_fp8_mm)(x, xs, w, ws, first, out=out)
+    assert bool((out[4000:] == 7.5).all())
+    for e, lo, hi in ((0, 0, 1200), (1, 1200, 2000), (3, 2400, 4000)):
+        one = offsets([hi - lo])
+        ref, mag, top, _ = ref_fp8(x[lo:hi], xs[lo:hi], w[e:e + 1], ws[e:e + 1], one, None, hi - lo)
+        bound = fp8_bound(K, mag, top, False)
+        if glu:
+            (gate, up), (dg, du) = branches(ref, {}), branches(bound, {})
+            assert_close(out[lo:hi], ref_act(gate, up, {}), act_bound(gate, up, dg, du, {}))
+        else:
+            assert_close(out[lo:hi], ref, bound)

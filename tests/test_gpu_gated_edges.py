@@ -4,8 +4,9 @@ import pytest
 import torch
 
 import block_scaled_fp4_histogram_amd as M
-from gated_util import U, assert_close, joined
-from products_util import BF16, FP16
+from gated_util import U, assert_close, check_backward, check_forward, joined
+from last_round_util import last_round
+from products_util import BF16, FP16, offsets, ref_dx, ref_mm
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,83 @@ def test_gradient_where_alpha_gate_passes_the_range(alpha):
     units = (24 + 4 * z.abs().clamp(max=90)) * U
     assert_close(got[:, 16:].to(BF16), rg, units * s * (1 + (z * r).abs()) + 2.0 ** -120, "d gate")
     assert_close(got[:, :16].to(BF16), ru, units * ru.abs() + 2.0 ** -120 * (1 + gate.abs()), "d up")
+
+
+# ---- last rounds in parts: offsets that go wrong, and two graphs at once
+
+FALLING = [0, 1200, 2400, 2000, 4000, 1000, -7]      # rows 2000 to 2400 in two groups, from 4000 on in none
+GLU, DX = (4097, 2304, 2056), (4097, 4360, 1032)     # rows, I, reduction
+
+
+def _normal(seed, *shape, dtype=BF16, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, device="cuda", generator=g).mul_(scale).to(dtype)
+
+
+def _splits(op, E, counts, I, reduction):
+    """That a product of these sizes has a last round in parts."""
+    R = GLU[0]
+    rows, cols, parts = M.debug_mm_plan(op, E, R, *((reduction, I) if op == M.MM_GLU_DX else (I, reduction)))
+    return parts == 0 and last_round(counts, I, rows, cols, -(-reduction // 64))[0] >= 2
+
+
+def test_forward_with_offsets_that_go_wrong_in_a_last_round():
+    """Rows of one group are right, rows of none stay, projections too."""
+    R, I, K = GLU
+    assert _splits(M.MM_GLU, 6, [1200, 1200, 0, 2000], I, K)
+    x, w = _normal(1, R, K), _normal(2, 6, 2 * I, K, scale=K ** -0.5)
+    h, pre = torch.full((R, I), 7.5, dtype=BF16, device="cuda"), torch.full((R, 2 * I), 7.5, dtype=BF16, device="cuda")
+    M.grouped_glu(x, w, torch.tensor(FALLING, dtype=torch.int32, device="cuda"), out=h, pre=pre, limit=2.0)
+    assert bool((h[4000:] == 7.5).all()) and bool((pre[4000:] == 7.5).all())
+    for e, lo, hi in ((0, 0, 1200), (1, 1200, 2000), (3, 2400, 4000)):
+        ref, mag, _ = ref_mm(x[lo:hi], w[e:e + 1], offsets([hi - lo]), None, hi - lo)
+        check_forward(h[lo:hi], pre[lo:hi], ref, mag, K, dict(limit=2.0))
+
+
+def test_backward_with_offsets_that_go_wrong_in_a_last_round():
+    R, I, N = DX
+    assert _splits(M.MM_GLU_DX, 6, [1200, 1200, 0, 2000], I, N)
+    dy, w, pre = _normal(3, R, N), _normal(4, 6, N, I, scale=N ** -0.5), _normal(5, R, 2 * I, scale=2.0)
+    d_pre, h = torch.full((R, 2 * I), 7.5, dtype=BF16, device="cuda"), torch.full((R, I), 7.5, dtype=BF16, device="cuda")
+    M.grouped_glu_dx(dy, w, pre, torch.tensor(FALLING, dtype=torch.int32, device="cuda"), out=d_pre, h=h, limit=2.0)
+    assert bool((d_pre[4000:] == 7.5).all()) and bool((h[4000:] == 7.5).all())
+    for e, lo, hi in ((0, 0, 1200), (1, 1200, 2000), (3, 2400, 4000)):
+        dh, mag, _ = ref_dx(dy[lo:hi].contiguous(), w[e:e + 1], offsets([hi - lo]))
+        check_backward(d_pre[lo:hi], h[lo:hi], dh, (N + 1) * U * mag, pre[lo:hi], dict(limit=2.0))
+
+
+def test_two_captured_last_rounds_replayed_at_once():
+    """Two graphs on two streams, each with last rounds in parts forward and backward: their scratch is their own."""
+    R, I, K = GLU
+    _, I2, N = DX
+    assert _splits(M.MM_GLU, 1, [R], I, K) and _splits(M.MM_GLU_DX, 1, [R], I2, N)
+    first = offsets([R]).cuda()
+    x, w = [_normal(s, R, K) for s in (1, 2)], [_normal(s, 1, 2 * I, K, scale=K ** -0.5) for s in (3, 4)]
+    dy, wd = [_normal(s, R, N) for s in (5, 6)], [_normal(s, 1, N, I2, scale=N ** -0.5) for s in (7, 8)]
+    pre = [_normal(s, R, 2 * I2, scale=2.0) for s in (9, 10)]
+
+    def step(i):
+        return M.grouped_glu(x[i], w[i], first), M.grouped_glu_dx(dy[i], wd[i], pre[i], first)
+
+    graphs, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in (0, 1):
+        step(i)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            outs.append(step(i))
+    for turn in range(4):
+        for i in (0, 1):                     # new inputs, and eager calls beside the replays
+            x[i].copy_(_normal(20 + 2 * turn + i, R, K))
+            dy[i].copy_(_normal(40 + 2 * turn + i, R, N))
+        want = [[t.clone() for t in step(i)] for i in (0, 1)]
+        for o in outs:
+            for t in o:
+                t.zero_()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for o, v in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, v))
