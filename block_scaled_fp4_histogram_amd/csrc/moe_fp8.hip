@@ -6,7 +6,8 @@
 
 namespace moe {
 
-// One group of 16384 x 4096 x 4096, summed in fp32: 537, 497, 550, 586 us (1.11 PFLOP/s).
+// One group of 16384 x 4096 x 4096, summed in fp32: 537, 497, 550, 586 us (1.11 PFLOP/s; the
+// conversions and scales issue about as long as the matrix cores are busy).
 template <int OP>
 static hipError_t launch_fp8_tiles(const MmArgs &a, int shape, hipStream_t s) {
   switch (shape) {
@@ -17,7 +18,7 @@ static hipError_t launch_fp8_tiles(const MmArgs &a, int shape, hipStream_t s) {
   }
 }
 
-// By the 8-bit instruction: 313, 295, 312, 356 us (1.87 PFLOP/s; with two waves a SIMD the
+// By the 8-bit instruction: 313, 295, 312, 356 us, repeated 271 (2.0 PFLOP/s; with two waves a SIMD the
 // loads' and the scales' waits stand between the products).
 template <int OP>
 static hipError_t launch_fp8_fast(const MmArgs &a, int shape, hipStream_t s) {

@@ -564,7 +564,7 @@ int moe_debug_route(moe_plan_t plan, const moe_tier *tiers, int n_tiers, const i
                     int32_t *inv, void *stream);
 
 /*
- * moe_debug_mm_plan -- how a product of these sizes runs (op as in moe_mm_op, so
+ * moe_debug_mm_plan -- how a product of these sizes runs (op as in moe_mm_scratch_bytes, so
  * that the tests of the tile shapes run the shapes they name): output rows and
  * columns of a tile (16 x 16, for a gated block 16 x 8: few rows a group, weights streamed) and the parts of
  * its reduction (0, of the gated and 8-bit floating-point products: where the tiles
